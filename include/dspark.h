@@ -373,6 +373,167 @@ typedef struct {
 DSPARK_API int dspark_train_losses(const dspark_train_loss_args *a, dspark_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* The target's pass: operators between the draft and dspark_verify.  The    */
+/* pages treat the target model as given; a server that runs it over a paged */
+/* key-value cache needs these four next to dspark_build_tags.  Rows are the */
+/* flattened batch of dspark_build_tags: the rows of request r are           */
+/* row_start[r] .. row_start[r + 1] - 1, row j of a request drafted after    */
+/* (some of) the rows before it.  A cache holds n_pages pages of `page`      */
+/* tokens; slot s is token s % page of page s / page.  Token t of request r  */
+/* sits in page table[r, t / page].  Neither call below synchronises; where  */
+/* the device finds an input out of range it writes DSPARK_ERR_RANGE to *err. */
+/* ------------------------------------------------------------------------ */
+
+/* The batch map of one cycle.  Request r has len[r] tokens in the cache, gets
+ * rows[r] new ones and holds held[r] pages.  With need_r = ceil((len_r +
+ * rows_r) / page), pages beyond need_r go back to the stack of free pages
+ * (free_list[0 .. *n_free), the top is taken first) and missing ones are taken
+ * from it:
+ *   given back: in request then page order, the first ends on top;
+ *   taken:      in request then page order, from the top, after all returns.
+ * A request that is done has len = rows = 0 and gives back all its pages.
+ *   row_start [R + 1]  running sum of rows;
+ *   slot [N]  where row j of r is stored: token len_r + j;
+ *   pos [N]   its position: len_r + j, or with `parents` len_r + its depth;
+ *   mask [N, W] 64-bit words, bit j set where row j of the request is the row
+ *             itself or one of its ancestors (with `parents` only).
+ * parents[i] is the parent's index within the request (< its own), negative
+ * for none; any other value is reported and read as none.  Rows at or beyond
+ * row_start[R] get slot -1, pos 0, mask 0.  All or nothing: too few free
+ * pages, more than max_pages pages, N or n_parents rows or 64 W rows of a
+ * request (with `parents`), or a negative size is reported, row_start becomes
+ * 0, every slot -1, held_out = held, n_free_out = n_free, and the table and
+ * the stack stay as they are.  held_out and n_free_out must not be held and
+ * n_free: what the call reads it leaves (but for the table entries and the
+ * stack entries that it fills), so a call may be repeated.  R at most
+ * DSPARK_MAP_MAX_R, n_pages * page below 2^31.  One launch, no workspace. */
+#define DSPARK_MAP_MAX_R 8192
+typedef struct {
+    int32_t R;
+    int32_t page;             /* tokens of a page                               */
+    int32_t n_pages;          /* pages of the cache = capacity of free_list      */
+    int32_t max_pages;        /* columns of the table                           */
+    int32_t N;                /* rows that slot, pos and mask hold               */
+    int32_t n_parents;        /* entries of parents                             */
+    int32_t W;                /* words of a mask row                            */
+    const int32_t *len;       /* [R]                                            */
+    const int32_t *rows;      /* [R]                                            */
+    const int32_t *parents;   /* [n_parents], or NULL for chains                 */
+    const int32_t *held;      /* [R]                                            */
+    const int32_t *n_free;    /* device scalar                                  */
+    int32_t *table;           /* in/out [R, max_pages]                          */
+    int32_t *free_list;       /* in/out [n_pages]                               */
+    int32_t *held_out;        /* out [R]                                        */
+    int32_t *n_free_out;      /* out device scalar                              */
+    int32_t *row_start;       /* out [R + 1]                                    */
+    int32_t *slot;            /* out [N]                                        */
+    int32_t *pos;             /* out [N]                                        */
+    uint64_t *mask;           /* out [N, W]: with parents, else NULL             */
+    int32_t *err;
+} dspark_page_map_args;
+
+DSPARK_API int dspark_page_map(const dspark_page_map_args *a, dspark_stream_t stream);
+
+/* Keys and values of the rows into their slots: k_cache[slot / page, :,
+ * slot % page, :] = k[i], likewise v.  A negative slot is skipped, one beyond
+ * the cache reported and skipped; of two rows with one slot either may stay.
+ * k and v may be views of a fused projection: strides of rows and heads in
+ * elements, the D elements of a head adjacent.  One launch, no workspace. */
+typedef struct {
+    int32_t N, H, D;          /* rows, key-value heads, head size               */
+    int32_t page, n_pages, dtype;
+    const void *k, *v;        /* [N, H, D]                                      */
+    int64_t k_row, k_head, v_row, v_head;  /* strides in elements               */
+    const int32_t *slot;      /* [N]                                            */
+    void *k_cache, *v_cache;  /* [n_pages, H, page, D]                          */
+    int32_t *err;
+} dspark_cache_store_args;
+
+DSPARK_API int dspark_cache_store(const dspark_cache_store_args *a, dspark_stream_t stream);
+
+/* Attention of the drafted rows over the cache.  Row j of request r (its own
+ * keys and values already stored) sees the tokens t < len[r] and, among the
+ * request's new rows, row j' where bit j' of its mask words is set (mask NULL:
+ * j' <= j, a chain):
+ *   s_t = scale q . k_t,  out = sum_t softmax(s)_t v_t,  lse = ln sum_t exp(s_t).
+ * Query head g uses key-value head g / (Hq / H).  What a row does not see has
+ * no influence on it, infinities and NaN included; a row that sees nothing
+ * gives out = 0, lse = -inf.  Rows at or beyond row_start[R] are not written.
+ * A request whose sizes are negative, whose rows pass N (or 64 W with a mask)
+ * or whose tokens pass the table is reported and its rows are not written; a
+ * page number outside the cache is reported and the rows that see it are then
+ * unspecified.  max_rows, the largest number of rows of a request as far as
+ * the host knows, only chooses the tile shape.
+ * Statistics and sums are fp32.  bf16 with D a multiple of 8 up to 128 and
+ * pages of a multiple of 8 tokens runs on the tensor cores (the softmax
+ * weights are rounded to bf16 for the second product); everything else with
+ * D <= DSPARK_ATTN_MAX_D on the CUDA cores in fp32.  Results do not depend on
+ * timing (no atomics on results). */
+#define DSPARK_ATTN_MAX_D 256
+typedef struct {
+    int32_t R, N, Hq, H, D;   /* requests, rows of q, query and key-value heads  */
+    int32_t page, n_pages, max_pages, dtype;
+    int32_t W;                /* words of a mask row                            */
+    int32_t max_rows;         /* hint, at least 1                               */
+    float scale;
+    const void *q;            /* [N, Hq, D], strides below, D adjacent           */
+    int64_t q_row, q_head;
+    const void *k_cache, *v_cache;  /* [n_pages, H, page, D]                    */
+    const int32_t *table;     /* [R, max_pages]                                 */
+    const int32_t *len;       /* [R]                                            */
+    const int32_t *row_start; /* [R + 1]                                        */
+    const uint64_t *mask;     /* [N, W] or NULL                                 */
+    void *out;                /* out [N, Hq, D], contiguous                     */
+    float *lse;               /* out [N, Hq] or NULL                            */
+    int32_t *err;
+} dspark_tree_attention_args;
+
+DSPARK_API size_t dspark_tree_attention_workspace_size(const dspark_tree_attention_args *a);
+DSPARK_API int dspark_tree_attention(const dspark_tree_attention_args *a, void *ws, dspark_stream_t stream);
+
+/* Rules on the target's logits before dspark_verify.  For row i, row j of
+ * request r, and token v, with c the number of times v stands in the output
+ * part of the request's text (hist[r, prompt_len .. hist_len)) and among the
+ * tokens tok of the rows j' >= 1 that the row continues, itself included
+ * (mask as above; row 0 is the text's last token, counted there already):
+ *   z = T[i, v];  if v was said (c > 0, or it stands in hist[r, 0 .. prompt_len)):
+ *       z = z > 0 ? z / rep[r] : z * rep[r];
+ *   z -= freq[r] c + pres[r] [c > 0];  z += the bias entries of v;
+ *   out[i, v] = allow bit v of row allow_row[i] clear ? -inf : z
+ * (allow_row[i] < 0: everything allowed).  Computed in fp32, rounded once.
+ * Any rule may be absent: hist, tok, rep, freq, pres, bias_start, allow NULL.
+ * Several bias entries of one token add in their order.  out may be T.  Rows
+ * at or beyond row_start[R] are not written.  Tokens outside the vocabulary
+ * are reported and ignored; lengths outside their arrays are reported and cut;
+ * a request whose rows pass N (or 64 W with a mask) is reported and skipped.
+ * The text and tok of a request without penalties are not read.
+ * One launch, no workspace. */
+typedef struct {
+    int32_t R, N, V, dtype;
+    int32_t max_hist;         /* columns of hist                                */
+    int32_t n_bias;           /* entries of bias_id and bias_val                */
+    int32_t n_allow;          /* rows of allow                                  */
+    int32_t W;                /* words of a mask row                            */
+    const void *T;            /* [N, V]                                         */
+    const int32_t *row_start; /* [R + 1]                                        */
+    const int32_t *tok;       /* [N] the rows' tokens, or NULL                   */
+    const uint64_t *mask;     /* [N, W] or NULL for chains                      */
+    const int32_t *hist;      /* [R, max_hist] or NULL                          */
+    const int32_t *hist_len;  /* [R]: with hist                                 */
+    const int32_t *prompt_len;/* [R], or NULL: no prompt                        */
+    const float *rep, *freq, *pres;  /* [R] or NULL                             */
+    const int32_t *bias_start;/* [R + 1] or NULL                                */
+    const int32_t *bias_id;   /* [n_bias]                                       */
+    const float *bias_val;    /* [n_bias]                                       */
+    const uint32_t *allow;    /* [n_allow, ceil(V / 32)] or NULL                */
+    const int32_t *allow_row; /* [N]: with allow                                */
+    void *out;                /* out [N, V]                                     */
+    int32_t *err;
+} dspark_logit_rules_args;
+
+DSPARK_API int dspark_logit_rules(const dspark_logit_rules_args *a, dspark_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Helpers                                                                    */
 /* ------------------------------------------------------------------------ */
 /* Message of the last failing call on this host thread ("" if none). */

@@ -7,6 +7,7 @@ library cannot be built or loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -66,6 +67,35 @@ class TrainLossArgs(ctypes.Structure):
                 ("s", P), ("a_ce", ctypes.c_float), ("a_tv", ctypes.c_float), ("a_conf", ctypes.c_float),
                 ("row", P), ("loss", P), ("grad_z", P), ("grad_s", P), ("err", P)]
 
+i64 = ctypes.c_int64
+
+
+class PageMapArgs(ctypes.Structure):
+    _fields_ = [("R", i32), ("page", i32), ("n_pages", i32), ("max_pages", i32), ("N", i32), ("n_parents", i32),
+                ("W", i32), ("len", P), ("rows", P), ("parents", P), ("held", P), ("n_free", P), ("table", P),
+                ("free_list", P), ("held_out", P), ("n_free_out", P), ("row_start", P), ("slot", P), ("pos", P),
+                ("mask", P), ("err", P)]
+
+
+class CacheStoreArgs(ctypes.Structure):
+    _fields_ = [("N", i32), ("H", i32), ("D", i32), ("page", i32), ("n_pages", i32), ("dtype", i32), ("k", P),
+                ("v", P), ("k_row", i64), ("k_head", i64), ("v_row", i64), ("v_head", i64), ("slot", P),
+                ("k_cache", P), ("v_cache", P), ("err", P)]
+
+
+class TreeAttentionArgs(ctypes.Structure):
+    _fields_ = [("R", i32), ("N", i32), ("Hq", i32), ("H", i32), ("D", i32), ("page", i32), ("n_pages", i32),
+                ("max_pages", i32), ("dtype", i32), ("W", i32), ("max_rows", i32), ("scale", ctypes.c_float),
+                ("q", P), ("q_row", i64), ("q_head", i64), ("k_cache", P), ("v_cache", P), ("table", P), ("len", P),
+                ("row_start", P), ("mask", P), ("out", P), ("lse", P), ("err", P)]
+
+
+class LogitRulesArgs(ctypes.Structure):
+    _fields_ = [("R", i32), ("N", i32), ("V", i32), ("dtype", i32), ("max_hist", i32), ("n_bias", i32),
+                ("n_allow", i32), ("W", i32), ("T", P), ("row_start", P), ("tok", P), ("mask", P), ("hist", P),
+                ("hist_len", P), ("prompt_len", P), ("rep", P), ("freq", P), ("pres", P), ("bias_start", P),
+                ("bias_id", P), ("bias_val", P), ("allow", P), ("allow_row", P), ("out", P), ("err", P)]
+
 
 class DSparkError(RuntimeError):
     def __init__(self, code, msg):
@@ -96,6 +126,11 @@ SYMBOLS = {
     "dspark_sts_fit": ([ctypes.POINTER(StsArgs), P, P], ctypes.c_int),
     "dspark_accept_stats": ([ctypes.POINTER(AcceptStatsArgs), P], ctypes.c_int),
     "dspark_train_losses": ([ctypes.POINTER(TrainLossArgs), P], ctypes.c_int),
+    "dspark_page_map": ([ctypes.POINTER(PageMapArgs), P], ctypes.c_int),
+    "dspark_cache_store": ([ctypes.POINTER(CacheStoreArgs), P], ctypes.c_int),
+    "dspark_tree_attention_workspace_size": ([ctypes.POINTER(TreeAttentionArgs)], ctypes.c_size_t),
+    "dspark_tree_attention": ([ctypes.POINTER(TreeAttentionArgs), P, P], ctypes.c_int),
+    "dspark_logit_rules": ([ctypes.POINTER(LogitRulesArgs), P], ctypes.c_int),
 }
 
 
@@ -440,4 +475,157 @@ def train_losses(zd, zt, xs, s, gamma, *, a_ce=0.1, a_tv=0.9, a_conf=1.0, want_r
     a.row, a.loss, a.grad_z, a.grad_s = _ptr(out["row"]), _ptr(out["loss"]), _ptr(out["grad_z"]), _ptr(out["grad_s"])
     a.err = _ptr(err)
     _check(L.dspark_train_losses(ctypes.byref(a), _stream(stream)))
+    return out
+
+
+# --------------------------------------------------------------------- the target's pass
+def _want(name, t, dtype, shape=None):
+    """Pointer of a contiguous GPU tensor of this element type (and shape), or of None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    return _ptr(t)
+
+
+def _strided(name, t, dtype, shape):
+    """Pointer, row stride and head stride of a [N, H, D] view whose D elements are adjacent."""
+    if not t.is_cuda:
+        raise ValueError("dspark tensors must live on the GPU")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.stride(2) != 1 and shape[2] > 1:
+        raise ValueError(f"the elements of a head of {name} must be adjacent")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _on(stream):
+    """Allocate for `stream`: what is made here may be used and freed on it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def page_map(lens, rows, table, held, free, n_free, *, page, N, parents=None, max_rows=None, out=None, err=None,
+             stream=None):
+    """The batch map of one cycle over a paged cache (include/dspark.h): lens, rows,
+    held [R] int32, table [R, max_pages] int32 and free [n_pages] int32 (both
+    updated), n_free [1] int32; N rows at most.  `parents` [N'] int32 makes the
+    rows trees; max_rows is then the largest number of rows of a request.
+    Returns {"held", "n_free", "row_start", "slot", "pos"} and, for trees,
+    "mask" [N, ceil(max_rows / 64)] int64.  The new held and n_free are other
+    tensors than the ones passed in: hand them to the next call."""
+    L = load()
+    R, max_pages = table.shape
+    dev = table.device
+    W = 0
+    if parents is not None:
+        if max_rows is None or max_rows < 1:
+            raise ValueError("trees need max_rows")
+        W = (max_rows + 63) // 64
+    if out is None:
+        with _on(stream):
+            new = lambda *n: torch.empty(n, dtype=torch.int32, device=dev)  # noqa: E731
+            out = {"held": new(R), "n_free": new(1), "row_start": new(R + 1), "slot": new(N), "pos": new(N)}
+            if W:
+                out["mask"] = torch.empty((N, W), dtype=torch.int64, device=dev)
+    i = torch.int32
+    a = PageMapArgs(R, page, free.numel(), max_pages, N, 0 if parents is None else parents.numel(), W,
+                    _want("lens", lens, i, (R,)), _want("rows", rows, i, (R,)), _want("parents", parents, i),
+                    _want("held", held, i, (R,)), _want("n_free", n_free, i, (1,)), _want("table", table, i),
+                    _want("free", free, i), _want("held", out["held"], i, (R,)), _want("n_free", out["n_free"], i, (1,)),
+                    _want("row_start", out["row_start"], i, (R + 1,)), _want("slot", out["slot"], i, (N,)),
+                    _want("pos", out["pos"], i, (N,)), _want("mask", out["mask"], torch.int64, (N, W)) if W else None,
+                    _want("err", err, i))
+    _check(L.dspark_page_map(ctypes.byref(a), _stream(stream)))
+    return out
+
+
+def cache_store(k, v, slot, k_cache, v_cache, *, err=None, stream=None):
+    """Write the rows' keys and values k, v [N, H, D] (views of a fused projection
+    are fine) into the slots slot [N] int32 of the caches [n_pages, H, page, D]."""
+    L = load()
+    n_pages, H, page, D = k_cache.shape
+    N = k.shape[0]
+    dt = k_cache.dtype
+    kp, k_row, k_head = _strided("k", k, dt, (N, H, D))
+    vp, v_row, v_head = _strided("v", v, dt, (N, H, D))
+    a = CacheStoreArgs(N, H, D, page, n_pages, _dtype_code(k_cache), kp, vp, k_row, k_head, v_row, v_head,
+                       _want("slot", slot, torch.int32, (N,)), _ptr(k_cache),
+                       _want("v_cache", v_cache, dt, (n_pages, H, page, D)), _want("err", err, torch.int32))
+    _check(L.dspark_cache_store(ctypes.byref(a), _stream(stream)))
+
+
+def _tree_attention_struct(q, k_cache, v_cache, table, lens, row_start, mask, scale, max_rows, out, lse, err):
+    n_pages, H, page, D = k_cache.shape
+    N, Hq = q.shape[0], q.shape[1]
+    R, max_pages = table.shape
+    dt = k_cache.dtype
+    i = torch.int32
+    qp, q_row, q_head = _strided("q", q, dt, (N, Hq, D))
+    W = 0 if mask is None else mask.shape[1]
+    return TreeAttentionArgs(R, N, Hq, H, D, page, n_pages, max_pages, _dtype_code(k_cache), W, int(max_rows),
+                             D ** -0.5 if scale is None else scale, qp, q_row, q_head, _ptr(k_cache),
+                             _want("v_cache", v_cache, dt, (n_pages, H, page, D)), _want("table", table, i),
+                             _want("lens", lens, i, (R,)), _want("row_start", row_start, i, (R + 1,)),
+                             _want("mask", mask, torch.int64, (N, W)), _want("out", out, dt, (N, Hq, D)),
+                             _want("lse", lse, torch.float32, (N, Hq)), _want("err", err, i))
+
+
+def tree_attention(q, k_cache, v_cache, table, lens, row_start, *, mask=None, scale=None, max_rows=1, out=None, ws=None,
+                   err=None, stream=None):
+    """Attention of the drafted rows q [N, Hq, D] over the cache and over their
+    ancestors among the rows (include/dspark.h): table, row_start and mask as
+    page_map gives them (mask None: chains), lens [R] the tokens before the
+    rows.  Returns {"out": [N, Hq, D], "lse": [N, Hq] fp32}; an `out` passed in
+    may leave "lse" out."""
+    L = load()
+    with _on(stream):
+        if out is None:
+            out = {"out": torch.empty(q.shape, dtype=q.dtype, device=q.device),
+                   "lse": torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)}
+        a = _tree_attention_struct(q, k_cache, v_cache, table, lens, row_start, mask, scale, max_rows, out["out"],
+                                   out.get("lse"), err)
+        nbytes = L.dspark_tree_attention_workspace_size(ctypes.byref(a))
+        ws = _workspace(nbytes, q.device, ws)
+    _check(L.dspark_tree_attention(ctypes.byref(a), _ptr(ws), _stream(stream)))
+    return out
+
+
+def tree_attention_workspace_size(q, k_cache, v_cache, table, lens, row_start, *, mask=None, max_rows=1):
+    """Scratch bytes dspark_tree_attention needs for this shape."""
+    a = _tree_attention_struct(q, k_cache, v_cache, table, lens, row_start, mask, None, max_rows, None, None, None)
+    return load().dspark_tree_attention_workspace_size(ctypes.byref(a))
+
+
+def logit_rules(T, row_start, *, tok=None, mask=None, hist=None, hist_len=None, prompt_len=None, rep=None, freq=None,
+                pres=None, bias_start=None, bias_id=None, bias_val=None, allow=None, allow_row=None, out=None, err=None,
+                stream=None):
+    """Penalties, biases and grammar masks on the target's logits T [N, V]
+    (include/dspark.h).  hist [R, max_hist] int32 with hist_len, prompt_len [R];
+    tok [N] the rows' tokens and mask their trees; rep, freq, pres [R] fp32;
+    bias_start [R + 1], bias_id, bias_val; allow [n, ceil(V / 32)] int32 bits and
+    allow_row [N].  Every rule may be None.  Returns out (T itself is fine)."""
+    L = load()
+    N, V = T.shape
+    R = row_start.numel() - 1
+    i, f = torch.int32, torch.float32
+    if out is None:
+        with _on(stream):
+            out = torch.empty_like(T)
+    W = 0 if mask is None else mask.shape[1]
+    n_bias = 0 if bias_id is None else bias_id.numel()
+    n_allow = 0 if allow is None else allow.shape[0]
+    max_hist = 0 if hist is None else hist.shape[1]
+    a = LogitRulesArgs(R, N, V, _dtype_code(T), max_hist, n_bias, n_allow, W, _ptr(T),
+                       _want("row_start", row_start, i), _want("tok", tok, i, (N,)),
+                       _want("mask", mask, torch.int64, (N, W)), _want("hist", hist, i, (R, max_hist)),
+                       _want("hist_len", hist_len, i, (R,)), _want("prompt_len", prompt_len, i, (R,)),
+                       _want("rep", rep, f, (R,)), _want("freq", freq, f, (R,)), _want("pres", pres, f, (R,)),
+                       _want("bias_start", bias_start, i, (R + 1,)), _want("bias_id", bias_id, i),
+                       _want("bias_val", bias_val, f, (n_bias,)), _want("allow", allow, i, (n_allow, (V + 31) // 32)),
+                       _want("allow_row", allow_row, i, (N,)), _want("out", out, T.dtype, (N, V)), _want("err", err, i))
+    _check(L.dspark_logit_rules(ctypes.byref(a), _stream(stream)))
     return out

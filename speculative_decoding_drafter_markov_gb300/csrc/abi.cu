@@ -464,6 +464,84 @@ DSPARK_API int dspark_train_losses(const dspark_train_loss_args *a, dspark_strea
     return e == cudaSuccess ? ok() : cuda_fail(e, "train losses");
 }
 
+DSPARK_API int dspark_page_map(const dspark_page_map_args *a, dspark_stream_t stream) {
+    if (!a) return fail(DSPARK_ERR_INVAL, "null argument struct");
+    if (a->R < 1 || a->page < 1 || a->n_pages < 1 || a->max_pages < 1 || a->N < 0)
+        return fail(DSPARK_ERR_INVAL, "bad shape R=%d page=%d n_pages=%d max_pages=%d N=%d", a->R, a->page, a->n_pages,
+                    a->max_pages, a->N);
+    if (a->R > DSPARK_MAP_MAX_R) return fail(DSPARK_ERR_UNSUPPORTED, "R=%d above %d", a->R, DSPARK_MAP_MAX_R);
+    if ((long long)a->n_pages * a->page > 0x7fffffffll)
+        return fail(DSPARK_ERR_UNSUPPORTED, "%lld slots, above 2^31 - 1", (long long)a->n_pages * a->page);
+    if (!a->len || !a->rows || !a->held || !a->n_free || !a->table || !a->free_list || !a->held_out || !a->n_free_out ||
+        !a->row_start || (a->N > 0 && (!a->slot || !a->pos)))
+        return fail(DSPARK_ERR_INVAL, "null tensor pointer");
+    if ((a->parents != nullptr) != (a->mask != nullptr)) return fail(DSPARK_ERR_INVAL, "parents and mask go together");
+    if (a->parents && (a->W < 1 || a->n_parents < 0)) return fail(DSPARK_ERR_INVAL, "bad W=%d or n_parents=%d", a->W, a->n_parents);
+    if (a->held_out == a->held || a->n_free_out == a->n_free)
+        return fail(DSPARK_ERR_INVAL, "held_out and n_free_out must be other arrays than held and n_free");
+    cudaError_t e = dspark::launch_page_map(*a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "page map");
+}
+
+DSPARK_API int dspark_cache_store(const dspark_cache_store_args *a, dspark_stream_t stream) {
+    if (!a) return fail(DSPARK_ERR_INVAL, "null argument struct");
+    if (a->N < 0 || a->H < 1 || a->D < 1 || a->page < 1 || a->n_pages < 1)
+        return fail(DSPARK_ERR_INVAL, "bad shape N=%d H=%d D=%d page=%d n_pages=%d", a->N, a->H, a->D, a->page, a->n_pages);
+    if (a->dtype != DSPARK_F32 && a->dtype != DSPARK_BF16) return fail(DSPARK_ERR_INVAL, "bad dtype %d", a->dtype);
+    if ((long long)a->H * a->D > (1 << 20)) return fail(DSPARK_ERR_UNSUPPORTED, "H * D = %lld above 2^20", (long long)a->H * a->D);
+    if (a->N == 0) return ok();
+    if (!a->k || !a->v || !a->slot || !a->k_cache || !a->v_cache) return fail(DSPARK_ERR_INVAL, "null tensor pointer");
+    cudaError_t e = dspark::launch_cache_store(*a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "cache store");
+}
+
+static int check_tree_attention(const dspark_tree_attention_args *a) {
+    if (!a) return fail(DSPARK_ERR_INVAL, "null argument struct");
+    if (a->R < 1 || a->N < 0 || a->H < 1 || a->Hq < a->H || a->Hq % a->H || a->D < 1 || a->page < 1 || a->n_pages < 1 ||
+        a->max_pages < 1 || a->max_rows < 1)
+        return fail(DSPARK_ERR_INVAL, "bad shape R=%d N=%d Hq=%d H=%d D=%d page=%d n_pages=%d max_pages=%d max_rows=%d", a->R,
+                    a->N, a->Hq, a->H, a->D, a->page, a->n_pages, a->max_pages, a->max_rows);
+    if (a->dtype != DSPARK_F32 && a->dtype != DSPARK_BF16) return fail(DSPARK_ERR_INVAL, "bad dtype %d", a->dtype);
+    if (a->D > DSPARK_ATTN_MAX_D) return fail(DSPARK_ERR_UNSUPPORTED, "D=%d above %d", a->D, DSPARK_ATTN_MAX_D);
+    if ((long long)a->N * a->Hq > 0x7fffffffll || (long long)a->n_pages * a->H > 0x7fffffffll ||
+        (long long)a->max_pages * a->page > 0x7fffffffll)
+        return fail(DSPARK_ERR_UNSUPPORTED, "too many rows, pages or tokens");
+    if (a->mask && a->W < 1) return fail(DSPARK_ERR_INVAL, "bad W=%d", a->W);
+    return DSPARK_OK;
+}
+
+DSPARK_API size_t dspark_tree_attention_workspace_size(const dspark_tree_attention_args *a) {
+    if (check_tree_attention(a) != DSPARK_OK) return 0;
+    return dspark::tree_attention_ws_bytes(*a);
+}
+
+DSPARK_API int dspark_tree_attention(const dspark_tree_attention_args *a, void *ws, dspark_stream_t stream) {
+    int rc = check_tree_attention(a);
+    if (rc != DSPARK_OK) return rc;
+    if (a->N == 0) return ok();
+    if (!a->q || !a->k_cache || !a->v_cache || !a->table || !a->len || !a->row_start || !a->out)
+        return fail(DSPARK_ERR_INVAL, "null tensor pointer");
+    if (!ws) return fail(DSPARK_ERR_INVAL, "null workspace");
+    cudaError_t e = dspark::launch_tree_attention(*a, ws, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "tree attention");
+}
+
+DSPARK_API int dspark_logit_rules(const dspark_logit_rules_args *a, dspark_stream_t stream) {
+    if (!a) return fail(DSPARK_ERR_INVAL, "null argument struct");
+    if (a->R < 1 || a->N < 0 || a->V < 1) return fail(DSPARK_ERR_INVAL, "bad shape R=%d N=%d V=%d", a->R, a->N, a->V);
+    if (a->dtype != DSPARK_F32 && a->dtype != DSPARK_BF16) return fail(DSPARK_ERR_INVAL, "bad dtype %d", a->dtype);
+    if (a->R > 65535) return fail(DSPARK_ERR_UNSUPPORTED, "R=%d above 65535", a->R);
+    if (a->N == 0) return ok();
+    if (!a->T || !a->row_start || !a->out) return fail(DSPARK_ERR_INVAL, "null tensor pointer");
+    if (a->hist && (!a->hist_len || a->max_hist < 0)) return fail(DSPARK_ERR_INVAL, "hist needs hist_len");
+    if (a->bias_start && (a->n_bias < 0 || (a->n_bias > 0 && (!a->bias_id || !a->bias_val))))
+        return fail(DSPARK_ERR_INVAL, "bias_start needs bias_id and bias_val");
+    if (a->allow && (!a->allow_row || a->n_allow < 0)) return fail(DSPARK_ERR_INVAL, "allow needs allow_row");
+    if (a->mask && a->W < 1) return fail(DSPARK_ERR_INVAL, "bad W=%d", a->W);
+    cudaError_t e = dspark::launch_logit_rules(*a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "logit rules");
+}
+
 DSPARK_API int dspark_wait_selfcheck(const int32_t *flag, int32_t target, int32_t mode, uint64_t limit_ns,
                                      int32_t *err, dspark_stream_t stream) {
     if (!flag || !err) return fail(DSPARK_ERR_INVAL, "null pointer");

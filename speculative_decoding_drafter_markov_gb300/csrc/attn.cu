@@ -1,0 +1,320 @@
+// attn.cu -- attention of drafted rows over a paged cache: the CUDA-core kernel
+// (fp32, and the bf16 shapes the tensor-core kernel does not take) and the join
+// of the pieces of a unit.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "attn_common.cuh"
+
+namespace dspark {
+namespace attn {
+
+namespace {
+
+// ---------------------------------------------------------------- CUDA cores
+// A unit of 16 lines (4 per warp) over tiles of 32 tokens; keys and values of a
+// tile are staged in shared memory as fp32 and shared by the lines.  A thread
+// scores one line against four tokens, then each warp adds its four lines'
+// weighted values, the lanes side by side over D.
+constexpr int kLines = 16, kTile = 32, kThreads = 128;
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T *p);
+template <>
+__device__ __forceinline__ float4 load4(const float *p) {
+    return *reinterpret_cast<const float4 *>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xffff0000u));
+}
+
+__host__ __device__ inline int padded(int D) { return (D + 3) / 4 * 4; }
+inline size_t smem_bytes(int D) {
+    const int d = padded(D);
+    return sizeof(float) * ((size_t)kLines * d + (size_t)kTile * (d + 4) + (size_t)kTile * d + kLines * kTile);
+}
+
+template <typename T, int kDV>  // kDV: float4 columns per lane, ceil(D / 128)
+__global__ void __launch_bounds__(kThreads) tree_attention_simt(const __grid_constant__ Params p) {
+    extern __shared__ __align__(16) float sh[];
+    __shared__ long long scratch[2 + kThreads / 32];
+    const dspark_tree_attention_args &a = p.a;
+    const int D = a.D, DP = padded(D), KS = DP + 4;
+    float *sq = sh, *sk = sq + kLines * DP, *sv = sk + kTile * KS, *sp = sv + kTile * DP;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int line = tid >> 3, tx = tid & 7;  // scores: this thread's line and its tokens tx + 8 i
+    const Share share = share_of(p, scratch);
+    Walk walk(p, share);
+    if (tid == 0) p.join[blockIdx.x].pieces = 0;
+    Piece x;
+    while (walk.next(x)) {
+        __syncthreads();
+        // the lines' queries, zero beyond them
+        for (int i = tid; i < kLines * DP; i += kThreads) {
+            const int l = i / DP, d = i % DP, m = x.line0 + l;
+            float v = 0.f;
+            if (l < x.lines && d < D)
+                v = to_f32(static_cast<const T *>(a.q)[(size_t)(x.row0 + m / p.G) * a.q_row +
+                                                       (size_t)(x.h * p.G + m % p.G) * a.q_head + d]);
+            sq[l * DP + d] = v;
+        }
+        const int j = (x.line0 + line) / p.G;  // the scored line's row in its request
+        const bool live = line < x.lines;
+        const uint64_t *words = a.mask && live ? a.mask + (size_t)(x.row0 + j) * a.W : nullptr;
+        float m = -INFINITY, l = 0.f;
+        float4 acc[4][kDV];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < kDV; ++c) acc[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+
+        for (int t = x.t0; t < x.t1; ++t) {
+            const int tok0 = t * kTile;
+            __syncthreads();
+            // keys and values of the tile, zero beyond the unit's tokens
+            const T *kc = static_cast<const T *>(a.k_cache), *vc = static_cast<const T *>(a.v_cache);
+            const int per = DP / 4;
+            for (int i = tid; i < kTile * per; i += kThreads) {
+                const int tk = i / per, d = i % per * 4, tok = tok0 + tk;
+                float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+                if (tok < x.tokens) {
+                    int pg = a.table[(size_t)x.r * a.max_pages + tok / a.page];
+                    if (pg < 0 || pg >= a.n_pages) {
+                        set_err(a.err, DSPARK_ERR_RANGE);
+                        pg = 0;
+                    }
+                    const size_t at = (((size_t)pg * a.H + x.h) * a.page + tok % a.page) * D + d;
+                    if (p.vec) {
+                        kv = load4(kc + at);
+                        vv = load4(vc + at);
+                    } else {
+                        kv.x = to_f32(kc[at]);
+                        vv.x = to_f32(vc[at]);
+                        if (d + 1 < D) kv.y = to_f32(kc[at + 1]), vv.y = to_f32(vc[at + 1]);
+                        if (d + 2 < D) kv.z = to_f32(kc[at + 2]), vv.z = to_f32(vc[at + 2]);
+                        if (d + 3 < D) kv.w = to_f32(kc[at + 3]), vv.w = to_f32(vc[at + 3]);
+                    }
+                }
+                *reinterpret_cast<float4 *>(sk + tk * KS + d) = kv;
+                *reinterpret_cast<float4 *>(sv + tk * DP + d) = vv;
+            }
+            __syncthreads();
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int d = 0; d < DP; d += 4) {
+                const float4 q4 = *reinterpret_cast<const float4 *>(sq + line * DP + d);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 k4 = *reinterpret_cast<const float4 *>(sk + (tx + 8 * i) * KS + d);
+                    s[i] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[i]))));
+                }
+            }
+            const bool tail = tok0 + kTile > x.len;  // rows of this cycle, or tokens beyond the unit's
+            bool see[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int rel = tok0 + tx + 8 * i - x.len;
+                see[i] = rel < 0 || (rel < x.rows && (words ? ((words[rel >> 6] >> (rel & 63)) & 1) : !a.mask && rel <= j));
+                s[i] = see[i] ? s[i] * p.scale_log2 : -INFINITY;
+            }
+            // a NaN score stays one: the maximum skips it, its weight is NaN
+            float mt = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, d));
+            const float mn = fmaxf(m, mt), ref = mn == -INFINITY ? 0.f : mn;
+            const float keep = ex2(m - ref);  // m = -inf: 0
+            float w[4], sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = ex2(s[i] - ref);
+                sum += w[i];
+                // what the line does not see is marked, so that its value is left out below
+                sp[line * kTile + tx + 8 * i] = see[i] ? w[i] : -1.f;
+            }
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            l = fmaf(l, keep, sum);
+            m = mn;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float f = __shfl_sync(0xffffffffu, keep, 8 * i);
+#pragma unroll
+                for (int c = 0; c < kDV; ++c) {
+                    acc[i][c].x *= f;
+                    acc[i][c].y *= f;
+                    acc[i][c].z *= f;
+                    acc[i][c].w *= f;
+                }
+            }
+            const float *wp = sp + 4 * warp * kTile;
+            for (int tk = 0; tk < kTile; ++tk) {
+                float pw[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) pw[i] = wp[i * kTile + tk];
+#pragma unroll
+                for (int c = 0; c < kDV; ++c) {
+                    const int d = 4 * lane + 128 * c;
+                    if (d >= DP) break;
+                    const float4 v = *reinterpret_cast<const float4 *>(sv + tk * DP + d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (tail && pw[i] < 0.f) continue;
+                        acc[i][c].x = fmaf(pw[i], v.x, acc[i][c].x);
+                        acc[i][c].y = fmaf(pw[i], v.y, acc[i][c].y);
+                        acc[i][c].z = fmaf(pw[i], v.z, acc[i][c].z);
+                        acc[i][c].w = fmaf(pw[i], v.w, acc[i][c].w);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int ln = 4 * warp + i;
+            const float mm = __shfl_sync(0xffffffffu, m, 8 * i), ll = __shfl_sync(0xffffffffu, l, 8 * i);
+            if (ln >= x.lines) continue;
+            if (x.slot < 0) {
+                const int mm_line = x.line0 + ln;
+                const size_t row = x.row0 + mm_line / p.G, head = x.h * p.G + mm_line % p.G;
+                const float inv = ll == 0.f ? 0.f : 1.f / ll;
+#pragma unroll
+                for (int c = 0; c < kDV; ++c) {
+                    const float v[4] = {acc[i][c].x, acc[i][c].y, acc[i][c].z, acc[i][c].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int d = 4 * lane + 128 * c + e;
+                        if (d < D) store_out(p, (row * a.Hq + head) * D + d, v[e] * inv);
+                    }
+                }
+                if (a.lse && lane == 0) a.lse[row * a.Hq + head] = lse_of(mm, ll);
+            } else {
+                const size_t at = (size_t)x.slot * kLines + ln;
+#pragma unroll
+                for (int c = 0; c < kDV; ++c) {
+                    const float v[4] = {acc[i][c].x, acc[i][c].y, acc[i][c].z, acc[i][c].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int d = 4 * lane + 128 * c + e;
+                        if (d < D) p.part_o[at * D + d] = v[e];
+                    }
+                }
+                if (lane == 0) p.part_ml[at] = make_float2(mm, ll);
+            }
+        }
+        if (tid == 0 && x.t0 == 0 && x.t1 < x.tiles) p.join[blockIdx.x] = walk.join_of(x);
+    }
+}
+
+// ---------------------------------------------------------------- join
+// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over a unit's partials.
+// At most one unit starts in a CTA and ends in a later one, so CTA (c, z) joins
+// line z of CTA c's unit: a warp per line.
+constexpr int kJoinWarps = 4;
+
+__global__ void __launch_bounds__(32 * kJoinWarps) tree_attention_join(const __grid_constant__ Params p) {
+    const Join n = p.join[blockIdx.x];
+    const int lane = threadIdx.x & 31, ln = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+    if (n.pieces == 0 || ln >= n.lines) return;
+    const int D = p.a.D;
+    // partial i: the first one, then the first partials of the CTAs after it
+    auto slot = [&](int i) { return (size_t)(i == 0 ? n.first : 2 * ((int)blockIdx.x + i)) * p.block + ln; };
+    float M = -INFINITY;
+    for (int i = lane; i < n.pieces; i += 32) M = fmaxf(M, p.part_ml[slot(i)].x);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    const float ref = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    for (int i = lane; i < n.pieces; i += 32) {
+        const float2 ml = p.part_ml[slot(i)];
+        L = fmaf(ex2(ml.x - ref), ml.y, L);
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+    const int m = n.line0 + ln;
+    const size_t row = n.row0 + m / p.G, head = n.h * p.G + m % p.G;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    for (int d = lane; d < D; d += 32) {
+        float o = 0.f;
+        for (int i = 0; i < n.pieces; ++i) {
+            const size_t at = slot(i);
+            const float w = ex2(p.part_ml[at].x - ref);
+            // a partial that saw nothing is zero, not a weight times it
+            o = fmaf(w, p.part_o[at * D + d], o);
+        }
+        store_out(p, (row * p.a.Hq + head) * D + d, o * inv);
+    }
+    if (p.a.lse && lane == 0) p.a.lse[row * p.a.Hq + head] = lse_of(M, L);
+}
+
+template <typename T, int kDV>
+cudaError_t launch_as(const Params &p, int grid, size_t smem, cudaStream_t s) {
+    auto kern = tree_attention_simt<T, kDV>;
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    kern<<<grid, kThreads, smem, s>>>(p);
+    return cudaGetLastError();
+}
+
+// CTAs of the CUDA-core kernel that fit an SM's shared memory (capped by its threads)
+int simt_grid(int D) {
+    const int fit = (int)(220 * 1024 / (smem_bytes(D) + 1024));
+    return sm_count() * (fit < 1 ? 1 : fit > 8 ? 8 : fit);
+}
+
+}  // namespace
+
+size_t workspace_bytes(int grid, int block, int D) {
+    return align256(sizeof(Join) * grid) + align256(sizeof(float2) * 2 * (size_t)grid * block) +
+           align256(sizeof(float) * 2 * (size_t)grid * block * D);
+}
+
+void carve(Params &p, void *ws, int grid) {
+    char *c = static_cast<char *>(ws);
+    p.join = reinterpret_cast<Join *>(c);
+    c += align256(sizeof(Join) * grid);
+    p.part_ml = reinterpret_cast<float2 *>(c);
+    c += align256(sizeof(float2) * 2 * (size_t)grid * p.block);
+    p.part_o = reinterpret_cast<float *>(c);
+}
+
+cudaError_t launch_join(const Params &p, int grid, cudaStream_t s) {
+    tree_attention_join<<<dim3(grid, (p.block + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace attn
+
+size_t tree_attention_ws_bytes(const dspark_tree_attention_args &a) {
+    return attn::workspace_bytes(attn::simt_grid(a.D), attn::kLines, a.D);
+}
+
+cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws, cudaStream_t s) {
+    using namespace attn;
+    Params p{};
+    p.a = a;
+    p.G = a.Hq / a.H;
+    p.scale_log2 = a.scale * kLog2e;
+    p.block = kLines;
+    p.tile = kTile;
+    const int es = a.dtype == DSPARK_BF16 ? 2 : 4;
+    p.vec = a.D % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.k_cache) | reinterpret_cast<uintptr_t>(a.v_cache)) & (4 * es - 1)) == 0;
+    const int grid = simt_grid(a.D);
+    carve(p, ws, grid);
+    const size_t smem = smem_bytes(a.D);
+    const bool wide = a.D > 128;
+    cudaError_t e;
+    if (a.dtype == DSPARK_BF16)
+        e = wide ? launch_as<__nv_bfloat16, 2>(p, grid, smem, s) : launch_as<__nv_bfloat16, 1>(p, grid, smem, s);
+    else
+        e = wide ? launch_as<float, 2>(p, grid, smem, s) : launch_as<float, 1>(p, grid, smem, s);
+    if (e != cudaSuccess) return e;
+    return launch_join(p, grid, s);
+}
+
+}  // namespace dspark

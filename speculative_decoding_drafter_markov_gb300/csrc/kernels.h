@@ -146,6 +146,13 @@ cudaError_t launch_verify_phase2_tc(const dspark_verify_args &a, VerifyWs &w, cu
 cudaError_t launch_accept_stats(const dspark_accept_stats_args &a, cudaStream_t s);
 cudaError_t launch_train_losses(const dspark_train_loss_args &a, cudaStream_t s);
 
+// ----- the target's pass: paged cache, attention of drafted rows, logit rules ---------
+cudaError_t launch_page_map(const dspark_page_map_args &a, cudaStream_t s);
+cudaError_t launch_cache_store(const dspark_cache_store_args &a, cudaStream_t s);
+size_t tree_attention_ws_bytes(const dspark_tree_attention_args &a);
+cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws, cudaStream_t s);
+cudaError_t launch_logit_rules(const dspark_logit_rules_args &a, cudaStream_t s);
+
 // ----- philox check ------------------------------------------------------------------
 cudaError_t launch_philox(const uint32_t *ctr, uint64_t seed, int n, uint32_t *out, cudaStream_t s);
 
