@@ -465,11 +465,14 @@ DSPARK_API int dspark_cache_store(const dspark_cache_store_args *a, dspark_strea
  * unspecified.  max_rows, the largest number of rows of a request as far as
  * the host knows, only chooses the tile shape.
  * Statistics and sums are fp32.  bf16 with D a multiple of 8 up to 128 and
- * pages of a multiple of 8 tokens runs on the tensor cores (the softmax
- * weights are rounded to bf16 for the second product); everything else with
- * D <= DSPARK_ATTN_MAX_D on the CUDA cores in fp32.  Results do not depend on
+ * pages of a multiple of 8 tokens, and q (its strides too), the caches and out
+ * 16-byte aligned, runs on the tensor cores (the softmax weights are rounded
+ * to bf16 for the second product); everything else
+ * with D <= DSPARK_ATTN_MAX_D on the CUDA cores in fp32.  With a mask a request
+ * has at most DSPARK_ATTN_MAX_TREE rows (W <= 4).  Results do not depend on
  * timing (no atomics on results). */
 #define DSPARK_ATTN_MAX_D 256
+#define DSPARK_ATTN_MAX_TREE 256
 typedef struct {
     int32_t R, N, Hq, H, D;   /* requests, rows of q, query and key-value heads  */
     int32_t page, n_pages, max_pages, dtype;

@@ -507,6 +507,8 @@ static int check_tree_attention(const dspark_tree_attention_args *a) {
         (long long)a->max_pages * a->page > 0x7fffffffll)
         return fail(DSPARK_ERR_UNSUPPORTED, "too many rows, pages or tokens");
     if (a->mask && a->W < 1) return fail(DSPARK_ERR_INVAL, "bad W=%d", a->W);
+    if (a->mask && a->W > DSPARK_ATTN_MAX_TREE / 64)
+        return fail(DSPARK_ERR_UNSUPPORTED, "masks of W=%d words, above %d", a->W, DSPARK_ATTN_MAX_TREE / 64);
     return DSPARK_OK;
 }
 

@@ -291,7 +291,11 @@ cudaError_t launch_join(const Params &p, int grid, cudaStream_t s) {
 }  // namespace attn
 
 size_t tree_attention_ws_bytes(const dspark_tree_attention_args &a) {
-    return attn::workspace_bytes(attn::simt_grid(a.D), attn::kLines, a.D);
+    // enough for either kernel: which one runs also depends on the pointers
+    const size_t simt = attn::workspace_bytes(attn::simt_grid(a.D), attn::kLines, a.D);
+    if (a.dtype != DSPARK_BF16 || a.D > 128 || a.Hq / a.H > 128) return simt;
+    const size_t tc = attn::workspace_bytes(sm_count(), attn::tc_block(a), a.D);
+    return tc > simt ? tc : simt;
 }
 
 cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws, cudaStream_t s) {
@@ -300,6 +304,13 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws,
     p.a = a;
     p.G = a.Hq / a.H;
     p.scale_log2 = a.scale * kLog2e;
+    if (tc_supported(a)) {
+        p.block = tc_block(a);
+        const int grid = sm_count();
+        carve(p, ws, grid);
+        cudaError_t e = launch_tc(p, grid, s);
+        return e == cudaSuccess ? launch_join(p, grid, s) : e;
+    }
     p.block = kLines;
     p.tile = kTile;
     const int es = a.dtype == DSPARK_BF16 ? 2 : 4;

@@ -216,6 +216,10 @@ __device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f ? (m 
 
 size_t workspace_bytes(int grid, int block, int D);
 void carve(Params &p, void *ws, int grid);
+// the tensor-core kernel: one CTA per SM
+bool tc_supported(const dspark_tree_attention_args &a);
+int tc_block(const dspark_tree_attention_args &a);
+cudaError_t launch_tc(Params p, int grid, cudaStream_t s);
 cudaError_t launch_join(const Params &p, int grid, cudaStream_t s);
 
 }  // namespace attn

@@ -79,6 +79,8 @@ bool tc_available();
 bool tc_kernels_enabled();
 bool encode_w2t_map(CUtensorMap *m, const void *W2t, int V, int r, int BN);
 bool encode_kmajor_map(CUtensorMap *m, const void *base, int rows, int K, int ld, int box_rows);
+bool encode_bf16_map3(CUtensorMap *m, const void *base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
+                      const uint32_t (&box)[3]);
 bool encode_u_map(CUtensorMap *m, const void *U, int R, int gamma, int V, int MV);
 void tc_grid_shape(int R, int V, int MV, int BN, int *nparts, int *n_mtiles);
 
