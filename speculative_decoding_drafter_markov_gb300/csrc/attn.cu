@@ -46,6 +46,7 @@ __global__ void __launch_bounds__(kThreads) tree_attention_simt(const __grid_con
     float *sq = sh, *sk = sq + kLines * DP, *sv = sk + kTile * KS, *sp = sv + kTile * DP;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int line = tid >> 3, tx = tid & 7;  // scores: this thread's line and its tokens tx + 8 i
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Share share = share_of(p, scratch);
     Walk walk(p, share);
     if (tid == 0) p.join[blockIdx.x].pieces = 0;
@@ -212,42 +213,97 @@ __global__ void __launch_bounds__(kThreads) tree_attention_simt(const __grid_con
 // ---------------------------------------------------------------- join
 // out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over a unit's partials.
 // At most one unit starts in a CTA and ends in a later one, so CTA (c, z) joins
-// line z of CTA c's unit: a warp per line.
-constexpr int kJoinWarps = 4;
+// lines z, z + kJoinSplit, .. of CTA c's unit.  A warp takes a line, or, where a
+// unit has many pieces (one long cache over the whole GPU), the four warps share
+// a line's pieces.  Bound by latency: a few dependent reads of partials that are
+// still in L2, eight pieces in flight.
+constexpr int kJoinWarps = 4, kJoinSplit = 8, kJoinMany = 8;
 
+template <bool kFour>  // D a multiple of 4: four columns per lane and load
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_attention_join(const __grid_constant__ Params p) {
+    constexpr int E = kFour ? 4 : 1, kMaxCols = 256 / (32 * E);
+    __shared__ float sum_o[kJoinWarps - 1][256];
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are written
     const Join n = p.join[blockIdx.x];
-    const int lane = threadIdx.x & 31, ln = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
-    if (n.pieces == 0 || ln >= n.lines) return;
-    const int D = p.a.D;
+    if (n.pieces == 0) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.a.D;
+    const bool many = n.pieces > kJoinMany;
+    const int cols = (D + 32 * E - 1) / (32 * E);
     // partial i: the first one, then the first partials of the CTAs after it
-    auto slot = [&](int i) { return (size_t)(i == 0 ? n.first : 2 * ((int)blockIdx.x + i)) * p.block + ln; };
-    float M = -INFINITY;
-    for (int i = lane; i < n.pieces; i += 32) M = fmaxf(M, p.part_ml[slot(i)].x);
+    auto slot = [&](int i, int ln) { return (size_t)(i == 0 ? n.first : 2 * ((int)blockIdx.x + i)) * p.block + ln; };
+    const int stride = many ? kJoinSplit : kJoinSplit * kJoinWarps;
+    for (int ln = many ? blockIdx.y : blockIdx.y * kJoinWarps + warp; ln < n.lines; ln += stride) {
+        // weights of pieces lane, lane + 32, ..: every warp has them all
+        float M = -INFINITY;
+        for (int i = lane; i < n.pieces; i += 32) M = fmaxf(M, p.part_ml[slot(i, ln)].x);
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    const float ref = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    for (int i = lane; i < n.pieces; i += 32) {
-        const float2 ml = p.part_ml[slot(i)];
-        L = fmaf(ex2(ml.x - ref), ml.y, L);
-    }
+        for (int d = 1; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        const float ref = M == -INFINITY ? 0.f : M;
+        float o[kMaxCols][E], L = 0.f;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
-    const int m = n.line0 + ln;
-    const size_t row = n.row0 + m / p.G, head = n.h * p.G + m % p.G;
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    for (int d = lane; d < D; d += 32) {
-        float o = 0.f;
-        for (int i = 0; i < n.pieces; ++i) {
-            const size_t at = slot(i);
-            const float w = ex2(p.part_ml[at].x - ref);
-            // a partial that saw nothing is zero, not a weight times it
-            o = fmaf(w, p.part_o[at * D + d], o);
+        for (int c = 0; c < kMaxCols; ++c)
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[c][e] = 0.f;
+        for (int i0 = 0; i0 < n.pieces; i0 += 32) {
+            float w = 0.f;
+            if (i0 + lane < n.pieces) {
+                const float2 ml = p.part_ml[slot(i0 + lane, ln)];
+                w = ex2(ml.x - ref);
+                L = fmaf(w, ml.y, L);
+            }
+            const int end = min(32, n.pieces - i0);
+#pragma unroll 8
+            for (int i = many ? warp : 0; i < end; i += many ? kJoinWarps : 1) {
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+                const float *from = p.part_o + slot(i0 + i, ln) * D;
+#pragma unroll
+                for (int c = 0; c < kMaxCols; ++c) {
+                    const int d = E * (lane + 32 * c);
+                    if (c >= cols || d >= D) break;
+                    if (kFour) {
+                        const float4 v = *reinterpret_cast<const float4 *>(from + d);
+                        o[c][0] = fmaf(wi, v.x, o[c][0]);
+                        o[c][E > 1 ? 1 : 0] = fmaf(wi, v.y, o[c][E > 1 ? 1 : 0]);
+                        o[c][E > 2 ? 2 : 0] = fmaf(wi, v.z, o[c][E > 2 ? 2 : 0]);
+                        o[c][E > 3 ? 3 : 0] = fmaf(wi, v.w, o[c][E > 3 ? 3 : 0]);
+                    } else {
+                        o[c][0] = fmaf(wi, from[d], o[c][0]);
+                    }
+                }
+            }
         }
-        store_out(p, (row * p.a.Hq + head) * D + d, o * inv);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+        if (many) {
+            __syncthreads();
+            if (warp > 0) {
+#pragma unroll
+                for (int c = 0; c < kMaxCols; ++c)
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if (E * (lane + 32 * c) + e < D) sum_o[warp - 1][E * (lane + 32 * c) + e] = o[c][e];
+            }
+            __syncthreads();
+            if (warp > 0) continue;
+#pragma unroll
+            for (int c = 0; c < kMaxCols; ++c)
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (E * (lane + 32 * c) + e < D)
+                        for (int x = 0; x < kJoinWarps - 1; ++x) o[c][e] += sum_o[x][E * (lane + 32 * c) + e];
+        }
+        const int m = n.line0 + ln;
+        const size_t at = (size_t)(n.row0 + m / p.G) * p.a.Hq + n.h * p.G + m % p.G;
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+        for (int c = 0; c < kMaxCols; ++c)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int d = E * (lane + 32 * c) + e;
+                if (d < D) store_out(p, at * D + d, o[c][e] * inv);
+            }
+        if (p.a.lse && lane == 0) p.a.lse[at] = lse_of(M, L);
     }
-    if (p.a.lse && lane == 0) p.a.lse[row * p.a.Hq + head] = lse_of(M, L);
 }
 
 template <typename T, int kDV>
@@ -284,8 +340,18 @@ void carve(Params &p, void *ws, int grid) {
 }
 
 cudaError_t launch_join(const Params &p, int grid, cudaStream_t s) {
-    tree_attention_join<<<dim3(grid, (p.block + kJoinWarps - 1) / kJoinWarps), 32 * kJoinWarps, 0, s>>>(p);
-    return cudaGetLastError();
+    // its CTAs come up while the first launch runs, and wait there for its end
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid, kJoinSplit);
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.stream = s;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return p.a.D % 4 == 0 ? cudaLaunchKernelEx(&cfg, tree_attention_join<true>, p)
+                          : cudaLaunchKernelEx(&cfg, tree_attention_join<false>, p);
 }
 
 }  // namespace attn

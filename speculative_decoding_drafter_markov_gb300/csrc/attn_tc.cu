@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tc::smem_u32(smem) & 1023u) {  // the swizzled tiles need it; the launch gives it
         if (tid == 0) set_err(a.err, DSPARK_ERR_UNSUPPORTED);
         return;
