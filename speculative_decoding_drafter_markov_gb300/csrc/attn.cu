@@ -16,7 +16,7 @@ namespace {
 // tile are staged in shared memory as fp32 and shared by the lines.  A thread
 // scores one line against four tokens, then each warp adds its four lines'
 // weighted values, the lanes side by side over D.
-constexpr int kLines = 16, kTile = 32, kThreads = 128;
+constexpr int kLines = 16, kTileLog2 = 5, kTile = 1 << kTileLog2, kThreads = 128;
 
 template <typename T>
 __device__ __forceinline__ float4 load4(const T *p);
@@ -54,16 +54,16 @@ __global__ void __launch_bounds__(kThreads) tree_attention_simt(const __grid_con
     while (walk.next(x)) {
         __syncthreads();
         // the lines' queries, zero beyond them
+        const int h = x.head / p.subs, head0 = h * p.G + x.head % p.subs * p.heads, heads = min(p.heads, (h + 1) * p.G - head0);
         for (int i = tid; i < kLines * DP; i += kThreads) {
-            const int l = i / DP, d = i % DP, m = x.line0 + l;
+            const int l = i / DP, d = i % DP, jj = l / p.heads, g = l % p.heads;
             float v = 0.f;
-            if (l < x.lines && d < D)
-                v = to_f32(static_cast<const T *>(a.q)[(size_t)(x.row0 + m / p.G) * a.q_row +
-                                                       (size_t)(x.h * p.G + m % p.G) * a.q_head + d]);
+            if (jj < x.n && g < heads && d < D)
+                v = to_f32(static_cast<const T *>(a.q)[(x.row0 + x.first + jj) * a.q_row + (head0 + g) * a.q_head + d]);
             sq[l * DP + d] = v;
         }
-        const int j = (x.line0 + line) / p.G;  // the scored line's row in its request
-        const bool live = line < x.lines;
+        const int j = x.first + line / p.heads;  // the scored line's row in its request
+        const bool live = line / p.heads < x.n;
         const uint64_t *words = a.mask && live ? a.mask + (size_t)(x.row0 + j) * a.W : nullptr;
         float m = -INFINITY, l = 0.f;
         float4 acc[4][kDV];
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) tree_attention_simt(const __grid_con
                         set_err(a.err, DSPARK_ERR_RANGE);
                         pg = 0;
                     }
-                    const size_t at = (((size_t)pg * a.H + x.h) * a.page + tok % a.page) * D + d;
+                    const size_t at = (((size_t)pg * a.H + h) * a.page + tok % a.page) * D + d;
                     if (p.vec) {
                         kv = load4(kc + at);
                         vv = load4(vc + at);
@@ -175,35 +175,26 @@ __global__ void __launch_bounds__(kThreads) tree_attention_simt(const __grid_con
 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int ln = 4 * warp + i;
+            const int ln = 4 * warp + i, jj = ln / p.heads, g = ln % p.heads;
             const float mm = __shfl_sync(0xffffffffu, m, 8 * i), ll = __shfl_sync(0xffffffffu, l, 8 * i);
-            if (ln >= x.lines) continue;
-            if (x.slot < 0) {
-                const int mm_line = x.line0 + ln;
-                const size_t row = x.row0 + mm_line / p.G, head = x.h * p.G + mm_line % p.G;
-                const float inv = ll == 0.f ? 0.f : 1.f / ll;
+            if (jj >= x.n || g >= heads) continue;
+            const size_t orow = (size_t)(x.row0 + x.first + jj) * a.Hq + head0 + g;
+            const size_t prow = (size_t)(x.slot < 0 ? 0 : x.slot) * p.lines + ln;
+            const float inv = ll == 0.f ? 0.f : 1.f / ll;
 #pragma unroll
-                for (int c = 0; c < kDV; ++c) {
-                    const float v[4] = {acc[i][c].x, acc[i][c].y, acc[i][c].z, acc[i][c].w};
+            for (int c = 0; c < kDV; ++c) {
+                const float v[4] = {acc[i][c].x, acc[i][c].y, acc[i][c].z, acc[i][c].w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int d = 4 * lane + 128 * c + e;
-                        if (d < D) store_out(p, (row * a.Hq + head) * D + d, v[e] * inv);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const int d = 4 * lane + 128 * c + e;
+                    if (d >= D) break;
+                    if (x.slot < 0) store_out(p, orow * D + d, v[e] * inv);
+                    else p.part_o[prow * p.stride + d] = v[e];
                 }
-                if (a.lse && lane == 0) a.lse[row * a.Hq + head] = lse_of(mm, ll);
-            } else {
-                const size_t at = (size_t)x.slot * kLines + ln;
-#pragma unroll
-                for (int c = 0; c < kDV; ++c) {
-                    const float v[4] = {acc[i][c].x, acc[i][c].y, acc[i][c].z, acc[i][c].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int d = 4 * lane + 128 * c + e;
-                        if (d < D) p.part_o[at * D + d] = v[e];
-                    }
-                }
-                if (lane == 0) p.part_ml[at] = make_float2(mm, ll);
+            }
+            if (lane == 0) {
+                if (x.slot >= 0) p.part_ml[prow] = make_float2(mm, ll);
+                else if (a.lse) a.lse[orow] = lse_of(mm, ll);
             }
         }
         if (tid == 0 && x.t0 == 0 && x.t1 < x.tiles) p.join[blockIdx.x] = walk.join_of(x);
@@ -226,13 +217,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_attention_join(const __g
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are written
     const Join n = p.join[blockIdx.x];
     if (n.pieces == 0) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.a.D;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.stride;
     const bool many = n.pieces > kJoinMany;
     const int cols = (D + 32 * E - 1) / (32 * E);
     // partial i: the first one, then the first partials of the CTAs after it
-    auto slot = [&](int i, int ln) { return (size_t)(i == 0 ? n.first : 2 * ((int)blockIdx.x + i)) * p.block + ln; };
+    auto slot = [&](int i, int ln) { return (size_t)(i == 0 ? n.first : 2 * ((int)blockIdx.x + i)) * p.lines + ln; };
     const int stride = many ? kJoinSplit : kJoinSplit * kJoinWarps;
+    const int unit_heads = p.heads;
     for (int ln = many ? blockIdx.y : blockIdx.y * kJoinWarps + warp; ln < n.lines; ln += stride) {
+        const int jj = ln / unit_heads, g = ln % unit_heads;
+        if (g >= n.heads) continue;
         // weights of pieces lane, lane + 32, ..: every warp has them all
         float M = -INFINITY;
         for (int i = lane; i < n.pieces; i += 32) M = fmaxf(M, p.part_ml[slot(i, ln)].x);
@@ -292,15 +286,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_attention_join(const __g
                     if (E * (lane + 32 * c) + e < D)
                         for (int x = 0; x < kJoinWarps - 1; ++x) o[c][e] += sum_o[x][E * (lane + 32 * c) + e];
         }
-        const int m = n.line0 + ln;
-        const size_t at = (size_t)(n.row0 + m / p.G) * p.a.Hq + n.h * p.G + m % p.G;
+        const size_t at = (size_t)(n.row + jj) * p.a.Hq + n.head + g;
         const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
         for (int c = 0; c < kMaxCols; ++c)
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const int d = E * (lane + 32 * c) + e;
-                if (d < D) store_out(p, at * D + d, o[c][e] * inv);
+                const int place = E * (lane + 32 * c) + e, d = p.mixed ? plain_column(place) : place;
+                if (place < D && d < p.a.D) store_out(p, at * p.a.D + d, o[c][e] * inv);
             }
         if (p.a.lse && lane == 0) p.a.lse[at] = lse_of(M, L);
     }
@@ -325,9 +318,9 @@ int simt_grid(int D) {
 
 }  // namespace
 
-size_t workspace_bytes(int grid, int block, int D) {
-    return align256(sizeof(Join) * grid) + align256(sizeof(float2) * 2 * (size_t)grid * block) +
-           align256(sizeof(float) * 2 * (size_t)grid * block * D);
+size_t workspace_bytes(int grid, int lines, int stride) {
+    return align256(sizeof(Join) * grid) + align256(sizeof(float2) * 2 * (size_t)grid * lines) +
+           align256(sizeof(float) * 2 * (size_t)grid * lines * stride);
 }
 
 void carve(Params &p, void *ws, int grid) {
@@ -335,7 +328,7 @@ void carve(Params &p, void *ws, int grid) {
     p.join = reinterpret_cast<Join *>(c);
     c += align256(sizeof(Join) * grid);
     p.part_ml = reinterpret_cast<float2 *>(c);
-    c += align256(sizeof(float2) * 2 * (size_t)grid * p.block);
+    c += align256(sizeof(float2) * 2 * (size_t)grid * p.lines);
     p.part_o = reinterpret_cast<float *>(c);
 }
 
@@ -350,7 +343,7 @@ cudaError_t launch_join(const Params &p, int grid, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    return p.a.D % 4 == 0 ? cudaLaunchKernelEx(&cfg, tree_attention_join<true>, p)
+    return p.stride % 4 == 0 ? cudaLaunchKernelEx(&cfg, tree_attention_join<true>, p)
                           : cudaLaunchKernelEx(&cfg, tree_attention_join<false>, p);
 }
 
@@ -360,7 +353,9 @@ size_t tree_attention_ws_bytes(const dspark_tree_attention_args &a) {
     // enough for either kernel: which one runs also depends on the pointers
     const size_t simt = attn::workspace_bytes(attn::simt_grid(a.D), attn::kLines, a.D);
     if (a.dtype != DSPARK_BF16 || a.D > 128 || a.Hq / a.H > 128) return simt;
-    const size_t tc = attn::workspace_bytes(sm_count(), attn::tc_block(a), a.D);
+    int block_rows, lines, stride;
+    attn::tc_shape(a, &block_rows, &lines, &stride);
+    const size_t tc = attn::workspace_bytes(sm_count(), lines, stride);
     return tc > simt ? tc : simt;
 }
 
@@ -371,14 +366,21 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws,
     p.G = a.Hq / a.H;
     p.scale_log2 = a.scale * kLog2e;
     if (tc_supported(a)) {
-        p.block = tc_block(a);
+        p.heads = p.G;
+        p.subs = 1;
+        tc_shape(a, &p.block_rows, &p.lines, &p.stride);
+        p.mixed = 1;
         const int grid = sm_count();
         carve(p, ws, grid);
         cudaError_t e = launch_tc(p, grid, s);
         return e == cudaSuccess ? launch_join(p, grid, s) : e;
     }
-    p.block = kLines;
-    p.tile = kTile;
+    p.heads = p.G < kLines ? p.G : kLines;
+    p.subs = (p.G + p.heads - 1) / p.heads;
+    p.block_rows = kLines / p.heads;
+    p.lines = p.block_rows * p.heads;
+    p.tile_log2 = kTileLog2;
+    p.stride = a.D;
     const int es = a.dtype == DSPARK_BF16 ? 2 : 4;
     p.vec = a.D % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.k_cache) | reinterpret_cast<uintptr_t>(a.v_cache)) & (4 * es - 1)) == 0;
     const int grid = simt_grid(a.D);

@@ -1,15 +1,15 @@
 // attn_common.cuh -- how the attention of drafted rows is cut into work, and how
 // the pieces of a row are joined.
 //
-// A unit is one key-value head of one request and a block of up to `block` of
-// its query rows (row j and query head g of the group in line j G + g, so the
-// heads that share keys share a unit).  Its tokens are walked in tiles.  The
-// tiles of all units stand in one line -- by request, block of rows, head --
+// A unit is one key-value head of one request and a block of its rows: every
+// row with every query head of the group that shares the keys (row jj of the
+// block and head g of the group in line jj heads + g).  Its tokens are walked in
+// tiles.  The tiles of all units stand in one line -- by request, block, head --
 // and each CTA takes an equal, consecutive share of the line, whatever the
-// lengths of the requests are: a long cache is spread over many CTAs, many
-// short ones are packed into one, and no length reaches the host.  A CTA leaves
-// a unit that it did not do whole as a partial (unnormalised sums, maximum and
-// sum of the weights); a second launch joins the partials of each unit.
+// lengths of the requests are: a long cache is spread over many CTAs, many short
+// ones are packed into one, and no length reaches the host.  A CTA leaves a unit
+// that it did not do whole as a partial (unnormalised sums, maximum and sum of
+// the weights); a second launch joins the partials of each unit.
 #pragma once
 
 #include "common.cuh"
@@ -18,23 +18,36 @@
 namespace dspark {
 namespace attn {
 
-struct Params {
-    dspark_tree_attention_args a;
-    int G;            // query heads per key-value head
-    int block;        // lines of a unit
-    int tile;         // tokens of a tile
-    int vec;          // CUDA-core kernel: 16-byte loads are possible
-    float scale_log2; // scale * log2(e)
-    float *part_o;    // [2 grid][block][D]  unnormalised sums
-    float2 *part_ml;  // [2 grid][block]     (maximum of s log2(e), sum of weights)
-    struct Join *join;  // [grid]            the unit that starts in this CTA and ends in a later one
-};
-
 struct Join {
     int pieces;       // 0: none
     int first;        // its first partial; the others are the first partials of the next CTAs
-    int row0, h, line0, lines;
+    int row, head, heads, lines;
 };
+
+struct Params {
+    dspark_tree_attention_args a;
+    int G;            // query heads per key-value head
+    int heads;        // of them in a unit: G, or fewer where a unit has not the lines
+    int subs;         // units that a group is cut into: ceil(G / heads)
+    int block_rows;   // rows of a unit
+    int lines;        // block_rows * heads
+    int tile_log2;    // tokens of a tile
+    int stride;       // floats of a partial's line
+    int mixed;        // partials in the order of the tensor-core fragments (see `plain_column`)
+    int vec;          // CUDA-core kernel: 16-byte loads are possible
+    float scale_log2; // scale * log2(e)
+    float *part_o;    // [2 grid][lines][stride]  unnormalised sums
+    float2 *part_ml;  // [2 grid][lines]          (maximum of s log2(e), sum of weights)
+    Join *join;       // [grid]                   the unit that starts in this CTA and ends in a later one
+};
+
+// Column of place d of a partial's line.  A tensor-core fragment gives a lane the
+// columns 8 k + 2 (lane % 4) + {0, 1}; two of them stand side by side, so that the
+// four lanes of a row write 64 bytes in one piece.
+__device__ __forceinline__ int plain_column(int d) {
+    const int in16 = d & 15, pair = (in16 >> 1) & 1;
+    return (d & ~15) + 8 * pair + 2 * (in16 >> 2) + (d & 1);
+}
 
 // a request's place: zero rows where its sizes are not usable
 struct Request {
@@ -51,51 +64,50 @@ __device__ __forceinline__ Request request_of(const Params &p, int r, bool repor
     return Request{row0, ok ? row1 - row0 : 0, len};
 }
 
-__device__ __forceinline__ int blocks_of(const Params &p, const Request &q) {
-    return (q.rows * p.G + p.block - 1) / p.block;
+__device__ __forceinline__ int blocks_of(const Params &p, int rows) {
+    return rows <= p.block_rows ? (rows > 0 ? 1 : 0) : (rows + p.block_rows - 1) / p.block_rows;
 }
 
-// tokens that block b of a request's lines can see
+// tokens that the rows of block b can see
 __device__ __forceinline__ int tokens_of(const Params &p, const Request &q, int b) {
-    if (p.a.mask) return q.len + q.rows;
-    const int last = min(q.rows * p.G, (b + 1) * p.block) - 1;
-    return q.len + last / p.G + 1;
+    return q.len + (p.a.mask ? q.rows : min(q.rows, (b + 1) * p.block_rows));
 }
 
 __device__ __forceinline__ int tiles_of(const Params &p, const Request &q, int b) {
-    return (tokens_of(p, q, b) + p.tile - 1) / p.tile;
+    return (int)(((unsigned)tokens_of(p, q, b) + (1u << p.tile_log2) - 1) >> p.tile_log2);
 }
 
 __device__ __forceinline__ long long request_tiles(const Params &p, const Request &q) {
-    const int n = blocks_of(p, q);
+    const int n = blocks_of(p, q.rows);
     long long t = 0;
     for (int b = 0; b < n; ++b) t += tiles_of(p, q, b);
-    return t * p.a.H;
+    return t * (p.a.H * p.subs);
 }
 
 // One CTA's piece of a unit.
 struct Piece {
-    int r, b, h;
+    int r, head;     // request; unit's place among the request's heads: h subs + sub
     int t0, t1;      // its tiles
     int tiles;       // the unit's tiles
-    int row0, rows, len;
-    int line0, lines;
+    int row0;        // the request's first row
+    int rows, len;   // of the request
+    int first, n;    // the unit's rows: first row and how many
     int tokens;      // the unit's tokens
     int slot;        // partial to leave it in, or -1: the unit is whole
 };
 
 // The CTA's share of the line and the place where it starts.  Every thread of
-// the CTA calls this once; `sh` is shared scratch of 2 + 2 (threads / 32) words.
+// the CTA calls this once; `sh` is shared scratch of 2 + threads / 32 words.
 struct Share {
-    long long lo, hi, total;
-    int ctas;            // CTAs that have a share
+    int lo, hi;
+    int each, more;      // tiles of a CTA's share; the first `more` CTAs have one more
     int r;               // request of tile lo
-    long long r_begin;   // its first tile
+    int r_begin;         // its first tile
 };
 
 __device__ inline Share share_of(const Params &p, long long *sh) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
-    const int R = p.a.R, per = (R + (int)blockDim.x - 1) / (int)blockDim.x;
+    const int R = p.a.R, per = R <= (int)blockDim.x ? 1 : (R + (int)blockDim.x - 1) / (int)blockDim.x;
     const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
     long long mine = 0;
     for (int r = r0; r < r1; ++r) mine += request_tiles(p, request_of(p, r, blockIdx.x == 0));
@@ -109,25 +121,28 @@ __device__ inline Share share_of(const Params &p, long long *sh) {
     __syncthreads();
     long long before = 0, total = 0;
     for (int w = 0; w < nwarps; ++w) {
-        if (w < warp) before += sh[2 + w];
-        total += sh[2 + w];
+        const long long x = sh[2 + w];
+        if (w < warp) before += x;
+        total += x;
     }
-    Share s;
-    s.total = total;
-    s.ctas = (int)min((long long)gridDim.x, total);
-    s.lo = s.hi = 0;
-    s.r = 0;
-    s.r_begin = 0;
-    if ((int)blockIdx.x < s.ctas) {
-        s.lo = total * blockIdx.x / s.ctas;
-        s.hi = total * (blockIdx.x + 1) / s.ctas;
+    Share s{0, 0, 1, 0, 0, 0};
+    if (total > 0x7fffffffll) {  // months of work: not a case to count in 64 bits for
+        if (tid == 0 && blockIdx.x == 0) set_err(p.a.err, DSPARK_ERR_UNSUPPORTED);
+        total = 0;
+    }
+    const int t = (int)total, ctas = min((int)gridDim.x, t), c = blockIdx.x;
+    if (c < ctas) {
+        s.each = t / ctas;
+        s.more = t - s.each * ctas;
+        s.lo = c * s.each + min(c, s.more);
+        s.hi = s.lo + s.each + (c < s.more ? 1 : 0);
         long long begin = before + inc - mine;
         if (begin <= s.lo && s.lo < begin + mine) {
             int r = r0;
-            for (;;) {
-                const long long t = request_tiles(p, request_of(p, r, false));
-                if (s.lo < begin + t) break;
-                begin += t;
+            for (; r1 - r0 > 1;) {
+                const long long n = request_tiles(p, request_of(p, r, false));
+                if (s.lo < begin + n) break;
+                begin += n;
                 ++r;
             }
             sh[0] = r;
@@ -136,7 +151,7 @@ __device__ inline Share share_of(const Params &p, long long *sh) {
     }
     __syncthreads();
     s.r = (int)sh[0];
-    s.r_begin = sh[1];
+    s.r_begin = (int)sh[1];
     return s;
 }
 
@@ -144,8 +159,9 @@ __device__ inline Share share_of(const Params &p, long long *sh) {
 struct Walk {
     const Params &p;
     Share s;
-    long long at;      // next tile of the line
+    int at;            // next tile of the line
     int r, b, h, t;    // its place
+    int tiles, blocks; // of the unit, of the request
     Request q;
     bool first;
 
@@ -153,45 +169,46 @@ struct Walk {
         if (s.lo >= s.hi) return;
         r = s.r;
         q = request_of(p, r, false);
-        long long left = s.lo - s.r_begin;
+        blocks = blocks_of(p, q.rows);
+        int left = s.lo - s.r_begin;
         for (;; ++b) {
-            const long long line = (long long)tiles_of(p, q, b) * p.a.H;
+            tiles = tiles_of(p, q, b);
+            const int line = tiles * p.a.H * p.subs;
             if (left < line) break;
             left -= line;
         }
-        const int tiles = tiles_of(p, q, b);
-        h = (int)(left / tiles);
-        t = (int)(left % tiles);
+        h = (unsigned)left / (unsigned)tiles;
+        t = left - h * tiles;
     }
 
     __device__ __forceinline__ bool next(Piece &out) {
         if (at >= s.hi) return false;
-        const int tiles = tiles_of(p, q, b);
         out.r = r;
-        out.b = b;
-        out.h = h;
+        out.head = h;
         out.t0 = t;
-        out.t1 = (int)min((long long)tiles, t + (s.hi - at));
+        out.t1 = min(tiles, t + (s.hi - at));
         out.tiles = tiles;
         out.row0 = q.row0;
         out.rows = q.rows;
         out.len = q.len;
-        out.line0 = b * p.block;
-        out.lines = min(p.block, q.rows * p.G - out.line0);
+        out.first = b * p.block_rows;
+        out.n = min(p.block_rows, q.rows - out.first);
         out.tokens = tokens_of(p, q, b);
         out.slot = out.t0 == 0 && out.t1 == tiles ? -1 : 2 * (int)blockIdx.x + (first ? 0 : 1);
         first = false;
         at += out.t1 - t;
         if (at < s.hi) {  // the unit is done: the next head, block or request
             t = 0;
-            if (++h == p.a.H) {
+            if (++h == p.a.H * p.subs) {
                 h = 0;
-                if (++b == blocks_of(p, q)) {
+                if (++b == blocks) {
                     b = 0;
                     do {
                         q = request_of(p, ++r, false);
                     } while (q.rows == 0);
+                    blocks = blocks_of(p, q.rows);
                 }
+                tiles = tiles_of(p, q, b);
             }
         }
         return true;
@@ -199,10 +216,12 @@ struct Walk {
 
     // what the second launch needs of a piece that starts a unit and does not end it
     __device__ __forceinline__ Join join_of(const Piece &x) const {
-        const long long end = s.hi - x.t1 + x.tiles;  // the piece is the share's last one
-        int c = blockIdx.x;
-        while (s.total * (c + 1) / s.ctas < end) ++c;
-        return Join{c - (int)blockIdx.x + 1, x.slot, x.row0, x.h, x.line0, x.lines};
+        const unsigned last = (unsigned)(s.hi - x.t1 + x.tiles) - 1;  // the piece is the share's last one
+        const unsigned big = (unsigned)s.more * (s.each + 1);
+        const unsigned c = last < big ? last / (unsigned)(s.each + 1) : s.more + (last - big) / (unsigned)s.each;
+        const int sub = p.subs == 1 ? 0 : x.head % p.subs, h0 = p.subs == 1 ? x.head : x.head / p.subs;
+        return Join{(int)c - (int)blockIdx.x + 1, x.slot, x.row0 + x.first, h0 * p.G + sub * p.heads,
+                    min(p.heads, p.G - sub * p.heads), x.n * p.heads};
     }
 };
 
@@ -214,11 +233,11 @@ __device__ __forceinline__ void store_out(const Params &p, size_t at, float v) {
 // ln of the sum of exponentials from the maximum of s log2(e) and the weights' sum
 __device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f ? (m + __log2f(l)) * kLn2 : (l == l ? -INFINITY : l); }
 
-size_t workspace_bytes(int grid, int block, int D);
+size_t workspace_bytes(int grid, int lines, int stride);
 void carve(Params &p, void *ws, int grid);
 // the tensor-core kernel: one CTA per SM
 bool tc_supported(const dspark_tree_attention_args &a);
-int tc_block(const dspark_tree_attention_args &a);
+void tc_shape(const dspark_tree_attention_args &a, int *block_rows, int *lines, int *stride);
 cudaError_t launch_tc(Params p, int grid, cudaStream_t s);
 cudaError_t launch_join(const Params &p, int grid, cudaStream_t s);
 

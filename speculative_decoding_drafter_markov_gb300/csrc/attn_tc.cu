@@ -2,21 +2,24 @@
 // tensor cores (bf16, D a multiple of 8 up to 128, pages of a multiple of 8 tokens).
 //
 // A unit's lines (rows x query heads of a group) fill one or two 128-row MMA
-// operands.  Per tile of 128 tokens and operand:
+// operands.  Per operand and tile of 128 tokens:
 //     S = Q K^T   (Q, K in shared memory, S in tensor memory, fp32)
 //     P = 2^(S scale log2(e) - m)   rounded to bf16 over S's columns
 //     O += P V    (P in tensor memory, V in shared memory as the MN-major operand)
-// Two streams, each with its own S, O and four softmax warps, keep the tensor
-// pipe and the softmax busy in turn: with two operands a stream per operand, both
-// over every tile; with one, the streams take the even and the odd tiles and are
-// added at the end like two partials.  Warp 8 copies keys and values by TMA, a
-// box per page piece, through one ring of slots in the order of their use; warp 9
-// copies Q and issues the MMAs.  The maximum m is only moved, and O rescaled in
-// tensor memory, when a tile exceeds it by 2^8 (any reference gives the same
-// result; P stays below 2^8 and fp32 sums far from overflow).
+// Two streams, each with its own S and O and four softmax warps, run side by side:
+// with two operands a stream per operand, both over every tile; with one, the
+// streams take the even and the odd tiles and are added at the end like two
+// partials.  The softmax hands P over in halves, so that the first half's product
+// runs while the second half is formed.  The maximum m is only moved, and O
+// rescaled in tensor memory, when a tile exceeds it by 2^8 (any reference gives
+// the same result; P stays below 2^8 and the fp32 sums far from overflow).
+//
+// Warps 0-7 softmax, 8 and 10 copy keys and values by TMA, a box per page piece,
+// through one ring of slots in the order of their use, 9 copies Q and issues the
+// MMAs, 11 walks the CTA's share of the work and hands out its pieces.
 //
 // Bound by HBM while lines are few: a tile of D = 128 is 64 KB, 2,800 clocks of an
-// SM's share of the bandwidth, against about 1,050 of MMA per operand.
+// SM's share of the bandwidth, against 1,056 of MMA per operand.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -28,48 +31,100 @@ namespace attn {
 
 namespace {
 
-constexpr int kThreads = 320, kTile = 128;
+constexpr int kThreads = 384, kTileLog2 = 7, kTile = 1 << kTileLog2;
 constexpr float kSlack = 8.f;  // log2 by which a tile may exceed the reference
+constexpr int kQueue = 4;      // pieces handed out ahead
 
 // DP: D padded to the copied width, NQ: operands a unit may have
 template <int DP_, int NQ_>
 struct Shape {
     static constexpr int DP = DP_, NQ = NQ_;
-    static constexpr int kHalves = DP / 64;
-    static constexpr int kHalf = 128 * 128;  // 128 rows of 64 bf16
-    static constexpr int kSlot = kHalves * kHalf;
+    static constexpr int kCols = DP / 64;        // a row is copied in blocks of 64 columns
+    static constexpr int kBlock = 128 * 128;     // 128 rows of 64 bf16
+    static constexpr int kSlot = kCols * kBlock;
     static constexpr int NS = DP == 128 ? 7 - NQ : 12;  // ring slots: what 227 KB hold beside Q
     static constexpr int kOffRing = NQ * kSlot;
-    static constexpr int kOffMl = kOffRing + NS * kSlot;        // float2 [2][128]
-    static constexpr int kOffBar = kOffMl + 2 * 128 * 8;        // barriers
-    static constexpr int kBars = 2 * NS + 9;
-    static constexpr int kOffBad = kOffBar + 8 * kBars;         // uint32 [3][8]
-    static constexpr int kOffMisc = kOffBad + 96;               // tmem slot, abort flag
-    static constexpr int kOffScan = kOffMisc + 8;               // long long [2 + 10]
-    static constexpr int kSmem = kOffScan + 96;
+    static constexpr int kOffMl = kOffRing + NS * kSlot;    // float2 [2][128]
+    static constexpr int kOffPiece = kOffMl + 2 * 128 * 8;  // Piece [kQueue], 64 bytes each
+    static constexpr int kOffScan = kOffPiece + 64 * kQueue;  // long long [2 + 12]
+    static constexpr int kOffBar = kOffScan + 8 * 14;
+    static constexpr int kBars = 2 * NS + 11 + 2 * kQueue;
+    static constexpr int kOffBad = kOffBar + 8 * kBars;     // uint32 [3][8]
+    static constexpr int kOffMisc = kOffBad + 96;           // tmem slot, abort flag
+    static constexpr int kSmem = kOffMisc + 8;
 };
+static_assert(sizeof(Piece) <= 64, "a piece's place in the queue");
 
 struct TcParams {
     Params p;
-    int lines;  // of one operand: a whole number of rows
-    int box;    // tokens of a TMA box: a power of two that divides a page
+    int op_rows;  // rows of one operand
+    int box;      // tokens of a TMA box: a power of two that divides a page
 };
 
-// A softmax warp's waits, by its first lane.  After one has run out the warp
-// walks on to the end without waiting: the CTA's barriers stay paired, and the
-// rows are unspecified (the error word says so).
+// A role's bounded waits.  The first that runs out ends the role (every role
+// comes to the CTA's last barrier; the error word tells).  Hundreds of short
+// waits make up a piece, so the limit is counted in SM clocks, which cost less to
+// read than the wall clock, and only after a run of tries.
+constexpr long long kWaitClocks = 4000000000ll;  // about 2 s
 struct Waiter {
     volatile int *abort_flag;
     int32_t *err;
-    int lane;
-    bool dead;
-    __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity) {
-        if (lane == 0 && !dead) dead = !tc::mbar_wait(bar, parity, abort_flag, err);
-        __syncwarp();
+    __device__ __forceinline__ bool one(uint64_t *bar, uint32_t parity) const {
+        if (tc::mbar_try_wait(bar, parity)) return true;
+        return slow(bar, parity);
+    }
+    __device__ __noinline__ bool slow(uint64_t *bar, uint32_t parity) const {
+        const long long t0 = clock64();
+        for (;;) {
+#pragma unroll 1
+            for (int i = 0; i < 64; ++i)
+                if (tc::mbar_try_wait(bar, parity)) return true;
+            if (*abort_flag) return false;
+            if (clock64() - t0 > kWaitClocks) break;
+        }
+        *abort_flag = 1;
+        set_err(err, DSPARK_ERR_TIMEOUT);
+        return false;
+    }
+    // by a whole warp, its first lane looking
+    __device__ __forceinline__ bool warp(uint64_t *bar, uint32_t parity) const {
+        int ok = 1;
+        if ((threadIdx.x & 31) == 0) ok = one(bar, parity) ? 1 : 0;
+        return __shfl_sync(0xffffffffu, ok, 0) != 0;
     }
 };
 
-// 32 mask bits of a line from bit position pos on (its words, beyond `rows` clear)
+// The queue of pieces: each reader takes a copy and gives the place back.
+struct Queue {
+    const Piece *items;
+    uint64_t *full, *empty;
+    uint32_t n;
+    __device__ __forceinline__ bool read_one(const Waiter &w, Piece &x) {
+        const int i = n % kQueue;
+        if (!w.one(&full[i], (n / kQueue) & 1u)) return false;
+        x = *reinterpret_cast<const Piece *>(reinterpret_cast<const char *>(items) + 64 * i);
+        tc::mbar_arrive(&empty[i]);
+        ++n;
+        return x.r >= 0;
+    }
+    __device__ __forceinline__ bool read_warp(const Waiter &w, Piece &x) {
+        const int i = n % kQueue;
+        if (!w.warp(&full[i], (n / kQueue) & 1u)) return false;
+        x = *reinterpret_cast<const Piece *>(reinterpret_cast<const char *>(items) + 64 * i);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&empty[i]);
+        ++n;
+        return x.r >= 0;
+    }
+};
+constexpr int kReaders = 11;  // two copy warps, the MMA warp, eight softmax warps
+
+// where a piece's tiles stand in the ring, counted from the piece's first slot:
+// K0 K1 V0 K2 V1 K3 .., or with two operands K0 V0 K1 V1 ..
+__device__ __forceinline__ uint32_t key_place(int t, bool dual) { return dual ? 2 * t : t < 2 ? t : 2 * t - 1; }
+__device__ __forceinline__ uint32_t value_place(int t, int n, bool dual) { return dual ? 2 * t + 1 : t + min(t + 2, n); }
+
+// 32 mask bits of a row from bit position pos on (its words; beyond `rows` clear)
 __device__ __forceinline__ uint32_t mask_bits(const uint32_t *words, int n_words, int pos, int rows) {
     const int i = pos >> 5;
     const uint32_t lo = i < n_words ? words[i] : 0u, hi = i + 1 < n_words ? words[i + 1] : 0u;
@@ -81,7 +136,7 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t *words, int n_words
 }
 
 // which of the 32 tokens rel0 .. rel0 + 31 (counted from the first row of the
-// cycle; negative: the cache) line `j` sees
+// cycle; negative: the cache) row j sees
 __device__ __forceinline__ uint32_t seen_bits(const uint32_t *words, int n_words, int rel0, int rows, int j) {
     if (rel0 + 31 < 0) return 0xffffffffu;
     if (!words) {
@@ -92,6 +147,27 @@ __device__ __forceinline__ uint32_t seen_bits(const uint32_t *words, int n_words
     return (mask_bits(words, n_words, 0, rows) << -rel0) | ((1u << -rel0) - 1);
 }
 
+// 4 x 4 transposition among the four lanes of a quad: a[i] of lane j <-> a[j] of lane i
+__device__ __forceinline__ void transpose_quad(uint32_t (&a)[4], int j) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const uint32_t r = __shfl_xor_sync(0xffffffffu, j & 1 ? a[i] : a[i + 1], 1);
+        if (j & 1) a[i] = r;
+        else a[i + 1] = r;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t r = __shfl_xor_sync(0xffffffffu, j & 2 ? a[i] : a[i + 2], 2);
+        if (j & 2) a[i] = r;
+        else a[i + 2] = r;
+    }
+}
+
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 two = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&two);
+}
+
 template <typename C>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_attention_tc(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -99,10 +175,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem[];
     const Params &p = tp.p;
     const dspark_tree_attention_args &a = p.a;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
-    uint64_t *empty = full + C::NS;
-    uint64_t *s_full = empty + C::NS, *p_ready = s_full + 2, *o_done = p_ready + 2, *q_full = o_done + 2, *o_free = q_full + 1,
-             *drain = o_free + 1;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kOffBar), *empty = full + C::NS;
+    uint64_t *s_full = empty + C::NS, *p_ready = s_full + 2;  // [stream]; [stream][half]
+    uint64_t *q_full = p_ready + 4, *o_free = q_full + 1, *both = o_free + 1,
+             *drain = both + 1, *o_last = drain + 1;
+    uint64_t *queue_full = o_last + 1, *queue_empty = queue_full + kQueue;
+    Piece *pieces = reinterpret_cast<Piece *>(smem + C::kOffPiece);
     uint32_t *bad = reinterpret_cast<uint32_t *>(smem + C::kOffBad);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
@@ -113,158 +191,184 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tid == 0) set_err(a.err, DSPARK_ERR_UNSUPPORTED);
         return;
     }
-    if (tid == 0) {
-        for (int i = 0; i < C::NS; ++i) {
-            tc::mbar_init(&full[i], 1);
-            tc::mbar_init(&empty[i], 1);
-        }
-        for (int w = 0; w < 2; ++w) {
-            tc::mbar_init(&s_full[w], 1);
-            tc::mbar_init(&p_ready[w], 4);
-            tc::mbar_init(&o_done[w], 1);
-        }
-        tc::mbar_init(q_full, 1);
-        tc::mbar_init(o_free, 8);
-        tc::mbar_init(drain, 1);
-        *abort_flag = 0;
-        tc::fence_mbar_init();
-        p.join[blockIdx.x].pieces = 0;
-    }
-    if (tid < 24) bad[tid] = 0;
     if (warp == 9) {
         tc::tmem_alloc(tmem_slot, 512);
         tc::tmem_relinquish();
         tc::tc_fence_before();
+    } else if (tid == 0) {
+        for (int i = 0; i < C::NS; ++i) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&empty[i], 1);
+        }
+        tc::mbar_init(&s_full[0], 1);
+        tc::mbar_init(&s_full[1], 1);
+        for (int i = 0; i < 4; ++i) tc::mbar_init(&p_ready[i], 4);
+        tc::mbar_init(q_full, 1);
+        tc::mbar_init(o_free, 8);
+        tc::mbar_init(both, 8);
+        tc::mbar_init(drain, 1);
+        tc::mbar_init(o_last, 1);
+        for (int i = 0; i < kQueue; ++i) {
+            tc::mbar_init(&queue_full[i], 1);
+            tc::mbar_init(&queue_empty[i], kReaders);
+        }
+        *abort_flag = 0;
+        tc::fence_mbar_init();
+    } else if (warp == 1) {
+        if (lane < 24) bad[lane] = 0;
+        if (lane == 31) p.join[blockIdx.x].pieces = 0;
+    } else if (warp == 8 && lane == 0) {
+        tc::prefetch_tmap(&tmQ);
+        tc::prefetch_tmap(&tmK);
+        tc::prefetch_tmap(&tmV);
     }
     const Share share = share_of(p, reinterpret_cast<long long *>(smem + C::kOffScan));  // synchronises the CTA
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    Walk walk(p, share);
+    const Waiter wait{abort_flag, a.err};
+    Queue queue{pieces, queue_full, queue_empty, 0};
+    uint32_t next = 0, mine = 0;  // copy warps: the slot after the last copy; bit k: slot next - 1 - k was this warp's
     Piece x;
 
-    if (warp == 8) {
-        // ------------------------------------------------------------ keys and values
-        uint32_t pos = 0;
-        bool ok = true;
+    if (warp == 11) {
+        // ------------------------------------------------------------ the walk
         if (lane == 0) {
-            tc::prefetch_tmap(&tmK);
-            tc::prefetch_tmap(&tmV);
+            Walk walk(p, share);
+            for (uint32_t n = 0;; ++n) {
+                const bool more = walk.next(x);
+                if (!more) x.r = -1;
+                const int i = n % kQueue;
+                if (!wait.one(&queue_empty[i], ((n / kQueue) & 1u) ^ 1u)) break;
+                *reinterpret_cast<Piece *>(reinterpret_cast<char *>(pieces) + 64 * i) = x;
+                tc::mbar_arrive(&queue_full[i]);
+                if (!more) break;
+                if (x.t0 == 0 && x.t1 < x.tiles) p.join[blockIdx.x] = walk.join_of(x);
+            }
         }
-        while (ok && walk.next(x)) {
-            const int32_t *table = a.table + (size_t)x.r * a.max_pages;
+        __syncwarp();
+    } else if (warp == 8 || warp == 10) {
+        // ------------------------------------------------------------ keys; values
+        const bool values = warp == 10;
+        const CUtensorMap *map = values ? &tmV : &tmK;
+        uint32_t base = 0;  // slots before the piece
+        // a lane copies one block of columns of one box
+        const int bx = lane / C::kCols, col = lane % C::kCols;
+        while (queue.read_warp(wait, x)) {
+            const bool dual = C::NQ == 2 && x.n > tp.op_rows;
             const int n = x.t1 - x.t0;
-            auto load = [&](const CUtensorMap *map, int t) {
-                const int tok0 = t * kTile, tokens = min(kTile, x.tokens - tok0);
-                const int boxes = (tokens + tp.box - 1) / tp.box;
-                // a lane copies one half of one box
-                const int bx = lane / C::kHalves, half = lane % C::kHalves;
-                int pg = 0, off = 0;
+            const int32_t *table = a.table + (size_t)x.r * a.max_pages;
+            const int last_tok = x.tokens - 1;
+            auto page_at = [&](int t) { return table[min(t * kTile + bx * tp.box, last_tok) / a.page]; };
+            int pg = page_at(x.t0);
+            bool ok = true;
+            for (int t = 0; t < n; ++t) {
+                const int tok0 = (x.t0 + t) * kTile, tok = tok0 + bx * tp.box;
+                const int boxes = (min(kTile, x.tokens - tok0) + tp.box - 1) / tp.box;
+                const uint32_t pos = base + (values ? value_place(t, n, dual) : key_place(t, dual));
+                const int slot = pos % C::NS;
+                int go = 1;
+                if (lane == 0) {
+                    go = wait.one(&empty[slot], ((pos / C::NS) & 1u) ^ 1u) ? 1 : 0;
+                    if (go) tc::mbar_expect_tx(&full[slot], (uint32_t)(boxes * tp.box * 128 * C::kCols));
+                }
+                ok = __shfl_sync(0xffffffffu, go, 0) != 0;
+                if (!ok) break;
+                mine = (pos + 1 - next < 32 ? mine << (pos + 1 - next) : 0u) | 1u;
+                next = pos + 1;
                 if (bx < boxes) {
-                    const int tok = tok0 + bx * tp.box;
-                    pg = table[tok / a.page];
-                    off = tok % a.page;
                     if (pg < 0 || pg >= a.n_pages) {
                         set_err(a.err, DSPARK_ERR_RANGE);
                         pg = 0;
                     }
+                    tc::tma_load_3d(smem + C::kOffRing + slot * C::kSlot + col * C::kBlock + bx * tp.box * 128, map,
+                                    &full[slot], 64 * col, tok % a.page, pg * a.H + x.head);
                 }
-                const int slot = pos % C::NS;
-                int go = 1;
-                if (lane == 0) {
-                    go = tc::mbar_wait(&empty[slot], ((pos / C::NS) & 1u) ^ 1u, abort_flag, a.err) ? 1 : 0;
-                    if (go) tc::mbar_expect_tx(&full[slot], (uint32_t)(boxes * tp.box * 128 * C::kHalves));
-                }
-                if (!__shfl_sync(0xffffffffu, go, 0)) return false;
-                if (bx < boxes)
-                    tc::tma_load_3d(smem + C::kOffRing + slot * C::kSlot + half * C::kHalf + bx * tp.box * 128, map, &full[slot],
-                                    64 * half, off, pg * a.H + x.h);
                 __syncwarp();
-                ++pos;
-                return true;
-            };
-            if (C::NQ == 2 && x.lines > tp.lines) {
-                for (int t = x.t0; ok && t < x.t1; ++t) ok = load(&tmK, t) && load(&tmV, t);
-            } else {
-                ok = load(&tmK, x.t0) && (n == 1 || load(&tmK, x.t0 + 1));
-                for (int t = x.t0; ok && t < x.t1; ++t) ok = load(&tmV, t) && (t + 2 >= x.t1 || load(&tmK, t + 2));
+                if (t + 1 < n) pg = page_at(x.t0 + t + 1);
             }
+            if (!ok) break;
+            base += 2 * n;
         }
-        if (lane == 0)  // nothing is left in flight
-            for (uint32_t g = pos < (uint32_t)C::NS ? 0 : pos - C::NS; g < pos; ++g)
-                tc::mbar_wait_drain(&full[g % C::NS], (g / C::NS) & 1u, a.err);
         __syncwarp();
     } else if (warp == 9) {
         // ------------------------------------------------------------ Q and the MMAs
         if (lane == 0) {
-            constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, 128);
+            constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, kTile);
             constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, C::DP) | tc::kIdescBMnMajor;
-            tc::prefetch_tmap(&tmQ);
             const uint32_t sbase = tc::smem_u32(smem);
+            const uint32_t q_lo = tc::desc_lo_k128(sbase), k_lo = tc::desc_lo_k128(sbase + C::kOffRing),
+                           v_lo = tc::desc_lo_mn128(sbase + C::kOffRing, C::kBlock);
+            uint32_t q_loads = 0, done = 0, p_phase[2] = {0, 0};
+            int slot = 0, kslot = 0, vslot = 0;
+            uint32_t phase = 0;  // of the next slot
             auto load_q = [&](const Piece &y) {
-                const int ops = C::NQ == 2 && y.lines > tp.lines ? 2 : 1;
-                tc::mbar_expect_tx(q_full, (uint32_t)(ops * tp.lines * 128 * C::kHalves));
+                const int ops = C::NQ == 2 && y.n > tp.op_rows ? 2 : 1;
+                tc::mbar_expect_tx(q_full, (uint32_t)(ops * tp.op_rows * p.G * 128 * C::kCols));
                 for (int o = 0; o < ops; ++o)
-                    for (int half = 0; half < C::kHalves; ++half)
-                        tc::tma_load_3d(smem + o * C::kSlot + half * C::kHalf, &tmQ, q_full, 64 * half, y.h * p.G,
-                                        y.row0 + (y.line0 + o * tp.lines) / p.G);
+                    for (int col = 0; col < C::kCols; ++col)
+                        tc::tma_load_3d(smem + o * C::kSlot + col * C::kBlock, &tmQ, q_full, 64 * col, y.head * p.G,
+                                        y.row0 + y.first + o * tp.op_rows);
+                ++q_loads;
             };
-            uint32_t pos = 0, pieces = 0, p_count[2] = {0, 0};
-            int kslot = 0, vslot = 0;
-            bool more = walk.next(x), ok = true;
-            uint32_t q_loads = 0;
-            if (more) load_q(x), ++q_loads;
+            auto next_slot = [&](int &mine) {
+                mine = slot;
+                const bool got = wait.one(&full[slot], phase);
+                if (++slot == C::NS) slot = 0, phase ^= 1u;
+                return got;
+            };
+            bool more = queue.read_one(wait, x), ok = true;
+            if (more) load_q(x);
             while (ok && more) {
-                const bool dual = C::NQ == 2 && x.lines > tp.lines;
-                const int n = x.t1 - x.t0, steps = dual ? 2 * n : n;
-                auto next_slot = [&](int &slot) {
-                    slot = pos % C::NS;
-                    const bool got = tc::mbar_wait(&full[slot], (pos / C::NS) & 1u, abort_flag, a.err);
-                    ++pos;
-                    return got;
-                };
-                auto scores = [&](int i) {
-                    const int w = i & 1;
+                const bool dual = C::NQ == 2 && x.n > tp.op_rows;
+                const int steps = (x.t1 - x.t0) << (dual ? 1 : 0);
+                // a tile's keys and values serve one step, or with two operands the
+                // steps of both streams
+                auto scores = [&](int w) {
                     if ((!dual || w == 0) && !next_slot(kslot)) return false;
                     tc::tc_fence_after();
-                    const uint64_t ad = tc::smem_desc_k128(sbase + (dual && w ? C::kSlot : 0));
-                    const uint64_t bd = tc::smem_desc_k128(sbase + C::kOffRing + kslot * C::kSlot);
+                    const uint32_t al = q_lo + (dual && w ? C::kSlot >> 4 : 0), bl = k_lo + kslot * (C::kSlot >> 4);
 #pragma unroll
                     for (int kk = 0; kk < C::DP / 16; ++kk) {
-                        const uint64_t step = (uint64_t)(((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4);
-                        tc::umma_bf16(tmem + 128 * w, ad + step, bd + step, idesc_s, kk > 0 ? 1u : 0u);
+                        const uint32_t step = ((kk >> 2) * C::kBlock + (kk & 3) * 32) >> 4;
+                        tc::umma_bf16_lo(tmem + 128 * w, al + step, bl + step, idesc_s, kk > 0 ? 1u : 0u);
                     }
                     tc::umma_commit(&s_full[w]);
                     if (!dual || w == 1) tc::umma_commit(&empty[kslot]);
                     return true;
                 };
-                ok = tc::mbar_wait(q_full, pieces & 1u, abort_flag, a.err);
-                ok = ok && scores(0) && (steps == 1 || scores(1));
-                for (int i = 0; ok && i < steps; ++i) {
-                    const int w = i & 1;
-                    ok = tc::mbar_wait(&p_ready[w], p_count[w]++ & 1u, abort_flag, a.err);
-                    if (ok && i == 0 && pieces > 0) ok = tc::mbar_wait(o_free, (pieces - 1) & 1u, abort_flag, a.err);
-                    if (!ok) break;
-                    if (i == steps - 1) {  // every S of the piece is done: Q may go
-                        more = walk.next(x);
-                        if (more) load_q(x), ++q_loads;
-                    }
-                    if ((!dual || w == 0) && !next_slot(vslot)) {
-                        ok = false;
-                        break;
-                    }
-                    tc::tc_fence_after();
-                    const uint64_t bd = tc::smem_desc_mn128(sbase + C::kOffRing + vslot * C::kSlot, C::kHalf);
+                auto values = [&](int i, int w) {
 #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk)
-                        tc::umma_bf16_ta(tmem + 256 + 128 * w, tmem + 128 * w + 8 * kk, bd + (uint64_t)((kk * 2048) >> 4),
-                                         idesc_o, i >= 2 || kk > 0 ? 1u : 0u);
-                    tc::umma_commit(&o_done[w]);
+                    for (int half = 0; half < 2; ++half) {
+                        if (!wait.one(&p_ready[2 * w + half], p_phase[w])) return false;
+                        if (half == 0) {
+                            if (i == 0 && done > 0 && !wait.one(o_free, (done - 1) & 1u)) return false;
+                            if ((!dual || w == 0) && !next_slot(vslot)) return false;
+                        }
+                        tc::tc_fence_after();
+                        const uint32_t bl = v_lo + vslot * (C::kSlot >> 4);
+#pragma unroll
+                        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                            tc::umma_bf16_ta_lo(tmem + 256 + 128 * w, tmem + 128 * w + 8 * kk, bl + ((kk * 2048) >> 4), idesc_o,
+                                                i >= 2 || kk > 0 ? 1u : 0u);
+                    }
+                    p_phase[w] ^= 1u;
                     if (!dual || w == 1) tc::umma_commit(&empty[vslot]);
-                    if (i + 2 < steps) ok = scores(i + 2);
+                    if (i + 1 == steps) tc::umma_commit(o_last);
+                    return true;
+                };
+                ok = wait.one(q_full, (q_loads - 1) & 1u) && scores(0) && (steps == 1 || scores(1));
+                for (int i = 0; ok && i < steps; i += 2) {
+                    ok = values(i, 0) && (i + 2 >= steps || scores(0));
+                    if (ok && i + 1 < steps) ok = values(i + 1, 1) && (i + 3 >= steps || scores(1));
                 }
-                ++pieces;
+                ++done;
+                // every S of the piece is done (its P was waited for): Q may go
+                if (ok) {
+                    more = queue.read_one(wait, x);
+                    if (more) load_q(x);
+                }
             }
-            if (!ok) {
+            if (!ok || *abort_flag) {
                 // given up: let what was issued finish before memory is released
                 if (q_loads) tc::mbar_wait_drain(q_full, (q_loads - 1) & 1u, a.err);
                 tc::umma_commit(drain);
@@ -276,48 +380,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ softmax
         const int w = warp >> 2, q = warp & 3, row = 32 * q + lane;
         const uint32_t quad = (uint32_t)(32 * q) << 16;
-        const uint32_t s_tmem = tmem + quad + 128 * w;
         float2 *ml = reinterpret_cast<float2 *>(smem + C::kOffMl);
-        Waiter wait{abort_flag, a.err, lane, false};
-        uint32_t s_count = 0, done0 = 0, done1 = 0, base = 0, pieces = 0;
+        uint32_t count = 0;  // tiles of this stream so far
+        uint32_t base = 0, done = 0;
+        const uint32_t s_tmem = tmem + quad + 128 * w, o_tmem = tmem + quad + 256 + 128 * w;
         const float scale = fmaxf(fabsf(p.scale_log2), 1e-37f);
-        while (walk.next(x)) {
-            const bool dual = C::NQ == 2 && x.lines > tp.lines;
+        const bool flip = p.scale_log2 < 0.f;
+        while (queue.read_warp(wait, x)) {
+            const bool dual = C::NQ == 2 && x.n > tp.op_rows;
             const int n = x.t1 - x.t0;
-            const int lines = dual ? (w ? x.lines - tp.lines : tp.lines) : x.lines;
+            const int row_first = x.first + (dual && w ? tp.op_rows : 0);
+            const int lines = (dual ? (w ? x.n - tp.op_rows : tp.op_rows) : x.n) * p.G;
             const int steps = dual ? n : (n + 1 - w) >> 1;
-            const int line = x.line0 + (dual && w ? tp.lines : 0) + row;
             const bool active = 32 * q < lines, live = row < lines;
-            const int j = line / p.G;
+            const int jj = row / p.G, j = row_first + jj;
             // rows of the cycle before `base_rel` are seen by every line of the unit
-            const int base_rel = a.mask ? 0 : x.line0 / p.G + 1;
+            const int base_rel = a.mask ? 0 : x.first + 1;
             const uint32_t *words = a.mask && live ? reinterpret_cast<const uint32_t *>(a.mask + (size_t)(x.row0 + j) * a.W) : nullptr;
-            uint32_t *flags = bad + 8 * (pieces % 3u);
+            uint32_t *flags = bad + 8 * (done % 3u);
             float m = -INFINITY, l = 0.f;
-            for (int k = 0; k < steps; ++k) {
-                const int t = dual ? x.t0 + k : x.t0 + 2 * k + w;
-                const int tok0 = t * kTile;
+            bool ok = true;
+            for (int u = 0; u < steps; ++u, ++count) {
+                const int tl = dual ? u : 2 * u + w;
+                const int tok0 = (x.t0 + tl) * kTile;
                 const bool tail = tok0 + kTile > x.len + base_rel;
                 if (tail && (!dual || w == 0)) {
                     // Values that some lines do not see must not reach them as 0 x inf:
                     // slots beyond the tokens are zeroed, infinities and NaN of the
                     // cycle's rows too, and those added back below where they are seen.
-                    const int tl = t - x.t0;
-                    const uint32_t pos = base + (uint32_t)(dual ? 2 * tl + 1 : tl + min(tl + 2, n));
+                    const uint32_t pos = base + value_place(tl, n, dual);
                     const int slot = pos % C::NS;
-                    wait(&full[slot], (pos / C::NS) & 1u);
-                    const int tok = tok0 + row, rel = tok - x.len - base_rel;
+                    ok = wait.warp(&full[slot], (pos / C::NS) & 1u);
+                    if (!ok) break;
+                    const int tok = tok0 + row, rel = tok - x.len - base_rel;  // a thread a token
                     if (tok >= x.tokens || rel >= 0) {
                         bool found = false;
 #pragma unroll 1
-                        for (int c = 0; c < 8 * C::kHalves; ++c) {
-                            uint4 *at = reinterpret_cast<uint4 *>(smem + C::kOffRing + slot * C::kSlot + (c >> 3) * C::kHalf +
-                                                                  row * 128 + ((c + lane) & 7) * 16);
+                        for (int c = 0; c < 8 * C::kCols; ++c) {
+                            uint4 *at = reinterpret_cast<uint4 *>(smem + C::kOffRing + slot * C::kSlot + (c >> 3) * C::kBlock +
+                                                                  row * 128 + ((c ^ lane) & 7) * 16);
                             if (tok >= x.tokens) {
                                 *at = make_uint4(0u, 0u, 0u, 0u);
                                 continue;
                             }
-                            uint4 v = *at;
+                            const uint4 v = *at;
                             uint32_t e[4] = {v.x, v.y, v.z, v.w};
                             bool hit = false;
 #pragma unroll
@@ -334,177 +440,216 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::fence_proxy_async_smem();
                     }
                 }
-                wait(&s_full[w], s_count++ & 1u);
+                ok = wait.warp(&s_full[w], count & 1u);
+                if (!ok) break;
                 tc::tc_fence_after();
-                if (active) {
-                    float s[128];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tc::tmem_ld32(s_tmem + 32 * c, s + 32 * c);
+                // half a tile's scores, what the line does not see at -inf
+                auto half_scores = [&](int half, float (&s)[64]) {
+                    tc::tmem_ld32(s_tmem + 64 * half, s);
+                    tc::tmem_ld32(s_tmem + 64 * half + 32, s + 32);
                     tc::tmem_wait_ld();
-                    if (p.scale_log2 < 0.f) {
+                    if (flip) {
 #pragma unroll
-                        for (int i = 0; i < 128; ++i) s[i] = -s[i];
+                        for (int i = 0; i < 64; ++i) s[i] = -s[i];
                     }
                     if (tail) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int rel0 = tok0 + 32 * c - x.len;
+                        for (int c = 0; c < 2; ++c) {
                             // lines beyond the unit's see nothing; what they hold is not read
-                            const uint32_t see = live ? seen_bits(words, 2 * a.W, rel0, x.rows, j) : 0u;
+                            const uint32_t see = live ? seen_bits(words, 2 * a.W, tok0 + 64 * half + 32 * c - x.len, x.rows, j) : 0u;
 #pragma unroll
                             for (int i = 0; i < 32; ++i) s[32 * c + i] = (see >> i) & 1u ? s[32 * c + i] : -INFINITY;
                         }
                     }
+                };
+                auto half_max = [&](const float (&s)[64]) {
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < 128; i += 4)
+                    for (int i = 0; i < 64; i += 4)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], s[i + c]);
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-                    if (k == 0) {
+                    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                };
+                float s[64], ref = 0.f;
+                if (active) {
+                    // the maximum of both halves before either's weights; the second is
+                    // read again from tensor memory, which costs less than 64 registers
+                    half_scores(1, s);
+                    float top = half_max(s);
+                    half_scores(0, s);
+                    top = fmaxf(top, half_max(s)) * scale;
+                    if (u == 0) {
                         m = top;
                     } else if (__any_sync(0xffffffffu, top > m + kSlack)) {
                         const float to = top > m + kSlack ? top : m;
                         const float f = to == -INFINITY ? 1.f : ex2(m - to);
                         m = to;
                         l *= f;
-                        wait(&o_done[w], ((w ? done1 : done0) + k - 1) & 1u);
+                        // the product before has been added when its values' slot is free
+                        const int tb = dual ? tl - 1 : tl - 2;
+                        const uint32_t pos = base + value_place(tb, n, dual);
+                        ok = wait.warp(&empty[pos % C::NS], (pos / C::NS) & 1u);
                         tc::tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < C::DP; c += 32) {
                             float o[32];
-                            tc::tmem_ld32(tmem + quad + 256 + 128 * w + c, o);
+                            tc::tmem_ld32(o_tmem + c, o);
                             tc::tmem_wait_ld();
                             uint32_t r[32];
 #pragma unroll
                             for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(o[i] * f);
-                            tc::tmem_st32(tmem + quad + 256 + 128 * w + c, r);
+                            tc::tmem_st32(o_tmem + c, r);
                         }
                     }
-                    const float ref = m == -INFINITY ? 0.f : m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    ref = m == -INFINITY ? 0.f : m;
+                }
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                for (int half = 0; half < 2; ++half) {
+                    if (active) {
+                        if (half == 1) half_scores(1, s);
+                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
                         uint32_t r[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const float p0 = ex2(fmaf(s[64 * c + 2 * i], scale, -ref));
-                            const float p1 = ex2(fmaf(s[64 * c + 2 * i + 1], scale, -ref));
+                            const float p0 = ex2(fmaf(s[2 * i], scale, -ref));
+                            const float p1 = ex2(fmaf(s[2 * i + 1], scale, -ref));
                             sum[i & 3] += p0 + p1;
-                            const __nv_bfloat162 two = __floats2bfloat162_rn(p0, p1);
-                            r[i] = *reinterpret_cast<const uint32_t *>(&two);
+                            r[i] = pack(p0, p1);
                         }
-                        tc::tmem_st32(s_tmem + 32 * c, r);
+                        tc::tmem_st32(s_tmem + 32 * half, r);
+                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        tc::tmem_wait_st();
+                        tc::tc_fence_before();
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tc::tmem_wait_st();
-                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&p_ready[2 * w + half]);
                 }
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&p_ready[w]);
             }
+            if (!ok) break;
 
             // ---------------------------------------------------------- the piece's end
-            const bool two = !dual && n > 1;  // both streams hold a part of the same lines
-            if (two) ml[128 * w + row] = make_float2(m, l);
-            if (tid < 8) bad[8 * ((pieces + 1) % 3u) + tid] = 0;
-            tc::named_bar_sync(1, 256);
-            float M = m, f0 = 1.f, f1 = 0.f;
+            // with one operand both streams hold a part of every line
+            if (done > 0 && !wait.warp(both, 1u)) break;  // the last piece's ml was read
+            ml[128 * w + row] = make_float2(m, l);  // of no tile: -inf, 0
+            if (tid < 8) bad[8 * ((done + 1) % 3u) + tid] = 0;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(both);
+            if (!wait.warp(both, 0u)) break;
+            float f0 = 1.f, f1 = 0.f;
             if (!dual) {
-                const float2 s0 = two ? ml[row] : make_float2(m, l), s1 = two ? ml[128 + row] : make_float2(-INFINITY, 0.f);
-                if (two) {
-                    M = fmaxf(s0.x, s1.x);
-                    const float ref = M == -INFINITY ? 0.f : M;
-                    f0 = ex2(s0.x - ref);
-                    f1 = ex2(s1.x - ref);
-                    l = fmaf(f0, s0.y, f1 * s1.y);
-                }  // else the only tile was stream 0's, and its warps finish the lines alone
+                const float2 s0 = ml[row], s1 = ml[128 + row];
+                m = fmaxf(s0.x, s1.x);
+                const float ref = m == -INFINITY ? 0.f : m;
+                f0 = ex2(s0.x - ref);
+                f1 = ex2(s1.x - ref);
+                l = fmaf(f0, s0.y, f1 * s1.y);
             }
-            const uint32_t steps0 = dual ? n : (n + 1) >> 1, steps1 = dual ? n : n >> 1;
-            if (!dual || w == 0) wait(&o_done[0], (done0 + steps0 - 1) & 1u);
-            if (steps1 > 0 && (!dual || w == 1)) wait(&o_done[1], (done1 + steps1 - 1) & 1u);
-            tc::tc_fence_after();
-            if (two) tc::named_bar_sync(1, 256);  // ml has been read
             uint32_t any_bad = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) any_bad |= flags[i];
-            if (active && (dual || two || w == 0)) {
-                const int unit_line = line - x.line0;
-                const float inv = x.slot < 0 ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-                const size_t orow = (size_t)(x.row0 + j) * a.Hq + x.h * p.G + line % p.G;
-                const size_t prow = (size_t)(x.slot < 0 ? 0 : x.slot) * p.block + unit_line;
-                // with two streams of the same lines each takes half of the columns
-                const int c0 = two ? w * (C::DP / 2) : 0, c1 = two ? c0 + C::DP / 2 : C::DP;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(both);
+            if (!wait.warp(o_last, done & 1u)) break;
+            tc::tc_fence_after();
+            if (active) {
+                const bool whole = x.slot < 0;
+                const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+                f0 *= inv;
+                f1 *= inv;
+                // with two streams of the same lines each finishes half of the columns
+                const int c0 = dual ? 0 : w * (C::DP / 2), c1 = dual ? C::DP : c0 + C::DP / 2;
+                const size_t prow0 = (size_t)(whole ? 0 : x.slot) * p.lines + (row_first - x.first) * p.G;
+                const int j4 = lane & 3;
 #pragma unroll 1
-                for (int c = c0; c < c1; c += 32) {
-                    float o[32];
-                    tc::tmem_ld32(tmem + quad + 256 + (dual ? 128 * w : 0) + c, o);
-                    if (two) {
-                        float o1[32];
-                        tc::tmem_ld32(tmem + quad + 384 + c, o1);
-                        tc::tmem_wait_ld();
+                for (int rb = 0; rb < 32; rb += 16) {
+                    if (32 * q + rb >= lines) break;
+                    const float fa[2] = {__shfl_sync(0xffffffffu, f0, rb + (lane >> 2)), __shfl_sync(0xffffffffu, f0, rb + 8 + (lane >> 2))};
+                    const float fb[2] = {__shfl_sync(0xffffffffu, f1, rb + (lane >> 2)), __shfl_sync(0xffffffffu, f1, rb + 8 + (lane >> 2))};
+#pragma unroll 1
+                    for (int c = c0; c < c1; c += 32) {
+                        const uint32_t from = tmem + quad + ((uint32_t)rb << 16) + 256 + c;
+                        float o[16];
+                        tc::tmem_ld_frag32(from + (dual ? 128 * w : 0), o);
+                        if (dual || n == 1) {  // one tile: the second stream's O is not this piece's
+                            tc::tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = fmaf(f0, o[i], f1 * o1[i]);
-                    } else {
-                        tc::tmem_wait_ld();
-                    }
-                    if (any_bad && live) {
-                        for (int b = 0; b < 256; ++b) {
-                            if (!((flags[b >> 5] >> (b & 31)) & 1u)) continue;
-                            const int rel = b + base_rel, tok = x.len + rel;
-                            if (!(seen_bits(words, 2 * a.W, rel, x.rows, j) & 1u)) continue;
-                            int pg = a.table[(size_t)x.r * a.max_pages + tok / a.page];
-                            if (pg < 0 || pg >= a.n_pages) pg = 0;
-                            const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v_cache) +
-                                                     (((size_t)pg * a.H + x.h) * a.page + tok % a.page) * a.D + c;
+                            for (int i = 0; i < 16; ++i) o[i] *= fa[(i >> 1) & 1];
+                        } else {
+                            float o1[16];
+                            tc::tmem_ld_frag32(from + 128, o1);
+                            tc::tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                if (c + i >= a.D) break;
-                                const float e = __bfloat162float(v[i]);
-                                if (!(fabsf(e) < INFINITY)) o[i] += e;
-                            }
+                            for (int i = 0; i < 16; ++i) o[i] = fmaf(fa[(i >> 1) & 1], o[i], fb[(i >> 1) & 1] * o1[i]);
                         }
-                    }
-                    if (!live) continue;
-                    if (x.slot < 0) {
-                        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + orow * a.D + c;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            if (c + i >= a.D) break;
-                            uint32_t r[4];
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const int ln = 32 * q + rb + 8 * hf + (lane >> 2);  // the line of these elements
+                            const bool in = ln < lines;
+                            const int g = ln % p.G, jr = row_first + ln / p.G;
+                            if (any_bad && in) {
+                                const uint32_t *mine = a.mask ? reinterpret_cast<const uint32_t *>(a.mask + (size_t)(x.row0 + jr) * a.W) : nullptr;
+                                for (int b = 0; b < 256; ++b) {
+                                    if (!((flags[b >> 5] >> (b & 31)) & 1u)) continue;
+                                    const int rel = b + base_rel, tok = x.len + rel;
+                                    if (!(seen_bits(mine, 2 * a.W, rel, x.rows, jr) & 1u)) continue;
+                                    int pg = a.table[(size_t)x.r * a.max_pages + tok / a.page];
+                                    if (pg < 0 || pg >= a.n_pages) pg = 0;
+                                    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v_cache) +
+                                                             (((size_t)pg * a.H + x.head) * a.page + tok % a.page) * a.D;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const __nv_bfloat162 v = __floats2bfloat162_rn(o[i + 2 * e] * inv, o[i + 2 * e + 1] * inv);
-                                r[e] = *reinterpret_cast<const uint32_t *>(&v);
+                                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                                        for (int e = 0; e < 2; ++e) {
+                                            const int d = c + 8 * k + 2 * j4 + e;
+                                            const float val = d < a.D ? __bfloat162float(v[d]) : 0.f;
+                                            if (!(fabsf(val) < INFINITY)) o[4 * k + 2 * hf + e] += val;
+                                        }
+                                }
                             }
-                            *reinterpret_cast<uint4 *>(out + i) = make_uint4(r[0], r[1], r[2], r[3]);
-                        }
-                    } else {
-                        float *out = p.part_o + prow * a.D + c;
+                            if (whole) {
+                                uint32_t r[4];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            if (c + i >= a.D) break;
-                            *reinterpret_cast<float4 *>(out + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                                for (int k = 0; k < 4; ++k) r[k] = pack(o[4 * k + 2 * hf], o[4 * k + 2 * hf + 1]);
+                                transpose_quad(r, j4);  // now columns c + 8 j4 .. + 7
+                                const int d = c + 8 * j4;
+                                if (in && d < a.D) {
+                                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) +
+                                                         ((size_t)(x.row0 + jr) * a.Hq + x.head * p.G + g) * a.D + d;
+                                    *reinterpret_cast<uint4 *>(out) = make_uint4(r[0], r[1], r[2], r[3]);
+                                }
+                            } else if (in) {
+                                float *out = p.part_o + (prow0 + ln) * p.stride + c + 4 * j4;
+#pragma unroll
+                                for (int k = 0; k < 4; k += 2)
+                                    *reinterpret_cast<float4 *>(out + 8 * k) =
+                                        make_float4(o[4 * k + 2 * hf], o[4 * k + 2 * hf + 1], o[4 * k + 4 + 2 * hf], o[4 * k + 5 + 2 * hf]);
+                            }
                         }
                     }
                 }
                 if (live && (dual || w == 0)) {
-                    if (x.slot >= 0) p.part_ml[prow] = make_float2(M, l);
-                    else if (a.lse) a.lse[orow] = lse_of(M, l);
+                    if (!whole) p.part_ml[prow0 + row] = make_float2(m, l);
+                    else if (a.lse) a.lse[(size_t)(x.row0 + j) * a.Hq + x.head * p.G + row % p.G] = lse_of(m, l);
                 }
             }
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(o_free);
-            if (tid == 0 && x.t0 == 0 && x.t1 < x.tiles) p.join[blockIdx.x] = walk.join_of(x);
-            done0 += steps0;
-            done1 += steps1;
             base += 2 * (uint32_t)n;
-            ++pieces;
+            ++done;
         }
         tc::tc_fence_before();
     }
     __syncthreads();
+    if (*abort_flag) {
+        // A role gave up (else the MMAs have waited for every copy): let the copies
+        // land before the CTA's memory goes.  One whose slot was used again is taken
+        // for one in flight, and costs the limit of a wait.
+        if (lane == 0)
+            for (uint32_t k = 0; k < (uint32_t)C::NS; ++k)
+                if ((mine >> k) & 1u) tc::mbar_wait_drain(&full[(next - 1 - k) % C::NS], ((next - 1 - k) / C::NS) & 1u, a.err);
+        __syncthreads();
+    }
     if (warp == 9) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, 512);
@@ -522,17 +667,12 @@ bool encode_cache(CUtensorMap *m, const void *base, const dspark_tree_attention_
 template <typename C>
 cudaError_t launch_as(const TcParams &tp, int grid, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                       cudaStream_t s) {
+    static_assert(C::kSmem <= 232448, "shared memory of a CTA");
     auto kern = tree_attention_tc<C>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     kern<<<grid, kThreads, C::kSmem, s>>>(q, k, v, tp);
     return cudaGetLastError();
-}
-
-// lines of one operand: whole rows of a group's query heads
-int lines_of(const dspark_tree_attention_args &a) {
-    const int G = a.Hq / a.H;
-    return 128 / G * G;
 }
 
 }  // namespace
@@ -541,30 +681,34 @@ bool tc_supported(const dspark_tree_attention_args &a) {
     auto al16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
     return a.dtype == DSPARK_BF16 && a.D % 8 == 0 && a.D <= 128 && a.page % 8 == 0 && a.Hq / a.H <= 128 && al16(a.q) &&
            al16(a.k_cache) && al16(a.v_cache) && al16(a.out) && a.q_row % 8 == 0 && a.q_head % 8 == 0 && a.q_row > 0 &&
-           a.q_head > 0 && a.q_row < (1ll << 38) && tc_kernels_enabled() && tc_available();
+           a.q_head > 0 && a.q_row < (1ll << 38) && a.q_head < (1ll << 38) && tc_kernels_enabled() && tc_available();
 }
 
-int tc_block(const dspark_tree_attention_args &a) {
-    const long long most = (long long)a.max_rows * (a.Hq / a.H);
-    return lines_of(a) * (most > lines_of(a) ? 2 : 1);
+// One operand while the host's hint says that a request's lines fit it, else two:
+// a unit of two reads its keys once for twice the lines.
+void tc_shape(const dspark_tree_attention_args &a, int *block_rows, int *lines, int *stride) {
+    const int G = a.Hq / a.H, one = 128 / G;
+    *block_rows = a.max_rows > one ? 2 * one : one;
+    *lines = *block_rows * G;
+    *stride = a.D > 64 ? 128 : 64;
 }
 
 cudaError_t launch_tc(Params p, int grid, cudaStream_t s) {
     const dspark_tree_attention_args &a = p.a;
     TcParams tp{};
-    tp.lines = lines_of(a);
-    p.tile = kTile;
+    tp.op_rows = 128 / p.G;
+    p.tile_log2 = kTileLog2;
     tp.p = p;
     tp.box = a.page & -a.page;
     if (tp.box > kTile) tp.box = kTile;
     CUtensorMap q, k, v;
     const uint64_t dims[3] = {(uint64_t)a.D, (uint64_t)a.Hq, (uint64_t)a.N};
     const uint64_t strides[2] = {(uint64_t)a.q_head * 2, (uint64_t)a.q_row * 2};
-    const uint32_t bx[3] = {64, (uint32_t)p.G, (uint32_t)(tp.lines / p.G)};
+    const uint32_t bx[3] = {64, (uint32_t)p.G, (uint32_t)tp.op_rows};
     if (!encode_bf16_map3(&q, a.q, dims, strides, bx) || !encode_cache(&k, a.k_cache, a, tp.box) ||
         !encode_cache(&v, a.v_cache, a, tp.box))
         return cudaErrorInvalidValue;
-    const bool two = p.block > tp.lines;
+    const bool two = p.block_rows > tp.op_rows;
     if (a.D > 64)
         return two ? launch_as<Shape<128, 2>>(tp, grid, q, k, v, s) : launch_as<Shape<128, 1>>(tp, grid, q, k, v, s);
     return two ? launch_as<Shape<64, 2>>(tp, grid, q, k, v, s) : launch_as<Shape<64, 1>>(tp, grid, q, k, v, s);

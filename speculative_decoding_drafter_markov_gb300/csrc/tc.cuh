@@ -263,19 +263,6 @@ __device__ __forceinline__ uint64_t smem_desc_k128(uint32_t saddr) {
     return d;
 }
 
-// Shared-memory matrix descriptor: MN-major operand in the 128-byte swizzle
-// layout (rows of 64 MN-consecutive bf16 per K index, 8-row groups 1024 bytes
-// apart, the next 64 MN elements `mn_stride` bytes further).
-__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr, uint32_t mn_stride) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);            // start address
-    d |= (uint64_t)((mn_stride >> 4) & 0x3FFFu) << 16;  // leading byte offset: along MN
-    d |= (uint64_t)(1024u >> 4) << 32;                  // stride byte offset: 8-row groups along K
-    d |= (uint64_t)1u << 46;                            // descriptor version
-    d |= (uint64_t)2u << 61;                            // 128-byte swizzle
-    return d;
-}
-
 // Instruction descriptor of kind::f16: bf16 A and B (K-major), fp32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -292,14 +279,34 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t adesc, uint6
         : "memory");
 }
 
-// the same with A in tensor memory: lane = row, two consecutive K entries per column
-__device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// The same with descriptors given by their low words (the high word is the same
+// for every 128-byte swizzled operand, and one word halves the issuing thread's
+// register traffic), and with A in tensor memory: lane = row, two consecutive K
+// entries per column.
+constexpr uint32_t kDescHi128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo_k128(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | (1u << 16); }
+// MN-major: rows of 64 MN-consecutive bf16 per K index, 8-row groups 1024 bytes
+// apart, the next 64 MN elements `mn_stride` bytes further
+__device__ __forceinline__ uint32_t desc_lo_mn128(uint32_t saddr, uint32_t mn_stride) {
+    return ((saddr >> 4) & 0x3FFFu) | (((mn_stride >> 4) & 0x3FFFu) << 16);
+}
+__device__ __forceinline__ void umma_bf16_lo(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\t"
+        "mov.b64 ad, {%1, %5};\n\tmov.b64 bd, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(alo), "r"(blo), "r"(idesc), "r"(accumulate), "n"(kDescHi128)
+        : "memory");
+}
+__device__ __forceinline__ void umma_bf16_ta_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t idesc,
+                                                uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 bd;\n\t"
+        "mov.b64 bd, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(blo), "r"(idesc), "r"(accumulate), "n"(kDescHi128)
         : "memory");
 }
 
@@ -335,7 +342,23 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// the same way back
+// 16 lanes x 32 consecutive 32-bit columns as fragments: in v[4 k .. 4 k + 3] thread
+// i gets columns 8 k + 2 (i % 4) + {0, 1} of lane base + i / 4, then of lane base + 8 + i / 4.
+__device__ __forceinline__ void tmem_ld_frag32(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// back from one thread per lane, 32 consecutive columns
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
