@@ -380,6 +380,7 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws,
     p.block_rows = kLines / p.heads;
     p.lines = p.block_rows * p.heads;
     p.tile_log2 = kTileLog2;
+    p.unit_cost = 1;
     p.stride = a.D;
     const int es = a.dtype == DSPARK_BF16 ? 2 : 4;
     p.vec = a.D % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.k_cache) | reinterpret_cast<uintptr_t>(a.v_cache)) & (4 * es - 1)) == 0;

@@ -7,7 +7,9 @@
 // tiles.  The tiles of all units stand in one line -- by request, block, head --
 // and each CTA takes an equal, consecutive share of the line, whatever the
 // lengths of the requests are: a long cache is spread over many CTAs, many short
-// ones are packed into one, and no length reaches the host.  A CTA leaves a unit
+// ones are packed into one, and no length reaches the host.  Before its tiles a
+// unit has `unit_cost` empty places in the line, the tiles' worth of its start and
+// end, so that CTAs with many short units get fewer tiles.  A CTA leaves a unit
 // that it did not do whole as a partial (unnormalised sums, maximum and sum of
 // the weights); a second launch joins the partials of each unit.
 #pragma once
@@ -32,6 +34,7 @@ struct Params {
     int block_rows;   // rows of a unit
     int lines;        // block_rows * heads
     int tile_log2;    // tokens of a tile
+    int unit_cost;    // places of a unit in the line beside its tiles
     int stride;       // floats of a partial's line
     int mixed;        // partials in the order of the tensor-core fragments (see `plain_column`)
     int vec;          // CUDA-core kernel: 16-byte loads are possible
@@ -77,10 +80,10 @@ __device__ __forceinline__ int tiles_of(const Params &p, const Request &q, int b
     return (int)(((unsigned)tokens_of(p, q, b) + (1u << p.tile_log2) - 1) >> p.tile_log2);
 }
 
-__device__ __forceinline__ long long request_tiles(const Params &p, const Request &q) {
+__device__ __forceinline__ long long request_places(const Params &p, const Request &q) {
     const int n = blocks_of(p, q.rows);
     long long t = 0;
-    for (int b = 0; b < n; ++b) t += tiles_of(p, q, b);
+    for (int b = 0; b < n; ++b) t += tiles_of(p, q, b) + p.unit_cost;
     return t * (p.a.H * p.subs);
 }
 
@@ -100,9 +103,9 @@ struct Piece {
 // the CTA calls this once; `sh` is shared scratch of 2 + threads / 32 words.
 struct Share {
     int lo, hi;
-    int each, more;      // tiles of a CTA's share; the first `more` CTAs have one more
-    int r;               // request of tile lo
-    int r_begin;         // its first tile
+    int each, more;      // places of a CTA's share; the first `more` CTAs have one more
+    int r;               // request of place lo
+    int r_begin;         // its first place
 };
 
 __device__ inline Share share_of(const Params &p, long long *sh) {
@@ -110,7 +113,7 @@ __device__ inline Share share_of(const Params &p, long long *sh) {
     const int R = p.a.R, per = R <= (int)blockDim.x ? 1 : (R + (int)blockDim.x - 1) / (int)blockDim.x;
     const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
     long long mine = 0;
-    for (int r = r0; r < r1; ++r) mine += request_tiles(p, request_of(p, r, blockIdx.x == 0));
+    for (int r = r0; r < r1; ++r) mine += request_places(p, request_of(p, r, blockIdx.x == 0));
     long long inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -140,7 +143,7 @@ __device__ inline Share share_of(const Params &p, long long *sh) {
         if (begin <= s.lo && s.lo < begin + mine) {
             int r = r0;
             for (; r1 - r0 > 1;) {
-                const long long n = request_tiles(p, request_of(p, r, false));
+                const long long n = request_places(p, request_of(p, r, false));
                 if (s.lo < begin + n) break;
                 begin += n;
                 ++r;
@@ -159,8 +162,9 @@ __device__ inline Share share_of(const Params &p, long long *sh) {
 struct Walk {
     const Params &p;
     Share s;
-    int at;            // next tile of the line
-    int r, b, h, t;    // its place
+    int at;            // next place of the line
+    int r, b, h;       // its unit
+    int begin;         // the unit's first place
     int tiles, blocks; // of the unit, of the request
     Request q;
     bool first;
@@ -173,20 +177,21 @@ struct Walk {
         int left = s.lo - s.r_begin;
         for (;; ++b) {
             tiles = tiles_of(p, q, b);
-            const int line = tiles * p.a.H * p.subs;
+            const int line = (tiles + p.unit_cost) * p.a.H * p.subs;
             if (left < line) break;
             left -= line;
         }
-        h = (unsigned)left / (unsigned)tiles;
-        t = left - h * tiles;
+        h = (unsigned)left / (unsigned)(tiles + p.unit_cost);
+        begin = s.lo - (left - h * (tiles + p.unit_cost));
     }
 
     __device__ __forceinline__ bool next(Piece &out) {
-        if (at >= s.hi) return false;
+        if (s.hi <= begin + p.unit_cost || at >= s.hi) return false;  // no tile of the unit is left here
+        const int skip = begin + p.unit_cost;
+        out.t0 = max(0, at - skip);
+        out.t1 = min(tiles, s.hi - skip);
         out.r = r;
         out.head = h;
-        out.t0 = t;
-        out.t1 = min(tiles, t + (s.hi - at));
         out.tiles = tiles;
         out.row0 = q.row0;
         out.rows = q.rows;
@@ -196,9 +201,9 @@ struct Walk {
         out.tokens = tokens_of(p, q, b);
         out.slot = out.t0 == 0 && out.t1 == tiles ? -1 : 2 * (int)blockIdx.x + (first ? 0 : 1);
         first = false;
-        at += out.t1 - t;
+        at = skip + out.t1;
         if (at < s.hi) {  // the unit is done: the next head, block or request
-            t = 0;
+            begin = at;
             if (++h == p.a.H * p.subs) {
                 h = 0;
                 if (++b == blocks) {
@@ -216,7 +221,7 @@ struct Walk {
 
     // what the second launch needs of a piece that starts a unit and does not end it
     __device__ __forceinline__ Join join_of(const Piece &x) const {
-        const unsigned last = (unsigned)(s.hi - x.t1 + x.tiles) - 1;  // the piece is the share's last one
+        const unsigned last = (unsigned)(s.hi - x.t1 + x.tiles) - 1;  // the piece ends the share
         const unsigned big = (unsigned)s.more * (s.each + 1);
         const unsigned c = last < big ? last / (unsigned)(s.each + 1) : s.more + (last - big) / (unsigned)s.each;
         const int sub = p.subs == 1 ? 0 : x.head % p.subs, h0 = p.subs == 1 ? x.head : x.head / p.subs;

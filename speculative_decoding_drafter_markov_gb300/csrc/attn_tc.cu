@@ -34,6 +34,7 @@ namespace {
 constexpr int kThreads = 384, kTileLog2 = 7, kTile = 1 << kTileLog2;
 constexpr float kSlack = 8.f;  // log2 by which a tile may exceed the reference
 constexpr int kQueue = 4;      // pieces handed out ahead
+constexpr int kUnitCost = 2;   // tiles' worth of a unit's start and end
 
 // DP: D padded to the copied width, NQ: operands a unit may have
 template <int DP_, int NQ_>
@@ -58,6 +59,7 @@ static_assert(sizeof(Piece) <= 64, "a piece's place in the queue");
 struct TcParams {
     Params p;
     int op_rows;  // rows of one operand
+    int inv_group;  // ceil(2^16 / G): line * inv_group >> 16 = line / G below 256
     int box;      // tokens of a TMA box: a power of two that divides a page
 };
 
@@ -384,8 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t count = 0;  // tiles of this stream so far
         uint32_t base = 0, done = 0;
         const uint32_t s_tmem = tmem + quad + 128 * w, o_tmem = tmem + quad + 256 + 128 * w;
-        const float scale = fmaxf(fabsf(p.scale_log2), 1e-37f);
-        const bool flip = p.scale_log2 < 0.f;
+        const float scale = fmaxf(p.scale_log2, 1e-37f);  // 0 would make -inf x 0 of what is not seen
         while (queue.read_warp(wait, x)) {
             const bool dual = C::NQ == 2 && x.n > tp.op_rows;
             const int n = x.t1 - x.t0;
@@ -415,25 +416,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int tok = tok0 + row, rel = tok - x.len - base_rel;  // a thread a token
                     if (tok >= x.tokens || rel >= 0) {
                         bool found = false;
+                        unsigned char *from = smem + C::kOffRing + slot * C::kSlot + row * 128;
 #pragma unroll 1
-                        for (int c = 0; c < 8 * C::kCols; ++c) {
-                            uint4 *at = reinterpret_cast<uint4 *>(smem + C::kOffRing + slot * C::kSlot + (c >> 3) * C::kBlock +
-                                                                  row * 128 + ((c ^ lane) & 7) * 16);
+                        for (int b = 0; b < C::kCols; ++b, from += C::kBlock) {
+                            // eight 16-byte pieces, each lane from another one on (the banks)
                             if (tok >= x.tokens) {
-                                *at = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(from + ((c ^ lane) & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                                 continue;
                             }
-                            const uint4 v = *at;
-                            uint32_t e[4] = {v.x, v.y, v.z, v.w};
-                            bool hit = false;
+                            uint4 v[8];
+                            uint32_t hits = 0;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if ((e[i] & 0x7f80u) == 0x7f80u) e[i] &= 0xffff0000u, hit = true;
-                                if ((e[i] & 0x7f800000u) == 0x7f800000u) e[i] &= 0xffffu, hit = true;
+                            for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const uint4 *>(from + ((c ^ lane) & 7) * 16);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const uint32_t e[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)  // an exponent of ones carries into the sign's place
+                                    hits |= ((e[i] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;
                             }
-                            if (hit) {
-                                *at = make_uint4(e[0], e[1], e[2], e[3]);
-                                found = true;
+                            if (hits == 0) continue;
+                            found = true;
+#pragma unroll 1
+                            for (int i = 0; i < 64; ++i) {
+                                unsigned short *at = reinterpret_cast<unsigned short *>(from) + i;
+                                if ((*at & 0x7f80u) == 0x7f80u) *at = 0;
                             }
                         }
                         if (found && rel < 256) atomicOr(&flags[rel >> 5], 1u << (rel & 31));
@@ -443,70 +451,60 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = wait.warp(&s_full[w], count & 1u);
                 if (!ok) break;
                 tc::tc_fence_after();
-                // half a tile's scores, what the line does not see at -inf
-                auto half_scores = [&](int half, float (&s)[64]) {
-                    tc::tmem_ld32(s_tmem + 64 * half, s);
-                    tc::tmem_ld32(s_tmem + 64 * half + 32, s + 32);
-                    tc::tmem_wait_ld();
-                    if (flip) {
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) s[i] = -s[i];
-                    }
-                    if (tail) {
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            // lines beyond the unit's see nothing; what they hold is not read
-                            const uint32_t see = live ? seen_bits(words, 2 * a.W, tok0 + 64 * half + 32 * c - x.len, x.rows, j) : 0u;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) s[32 * c + i] = (see >> i) & 1u ? s[32 * c + i] : -INFINITY;
-                        }
-                    }
-                };
-                auto half_max = [&](const float (&s)[64]) {
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int i = 0; i < 64; i += 4)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], s[i + c]);
-                    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                };
-                float s[64], ref = 0.f;
-                if (active) {
-                    // the maximum of both halves before either's weights; the second is
-                    // read again from tensor memory, which costs less than 64 registers
-                    half_scores(1, s);
-                    float top = half_max(s);
-                    half_scores(0, s);
-                    top = fmaxf(top, half_max(s)) * scale;
-                    if (u == 0) {
-                        m = top;
-                    } else if (__any_sync(0xffffffffu, top > m + kSlack)) {
-                        const float to = top > m + kSlack ? top : m;
-                        const float f = to == -INFINITY ? 1.f : ex2(m - to);
-                        m = to;
-                        l *= f;
-                        // the product before has been added when its values' slot is free
-                        const int tb = dual ? tl - 1 : tl - 2;
-                        const uint32_t pos = base + value_place(tb, n, dual);
-                        ok = wait.warp(&empty[pos % C::NS], (pos / C::NS) & 1u);
-                        tc::tc_fence_after();
+                // Three passes of one code: the maximum of the second half, that of the
+                // first and its weights, the weights of the second.  The weights need the
+                // maximum of both, and a half read again from tensor memory costs less
+                // than 64 registers.
+                float ref = 0.f, top = -INFINITY;
 #pragma unroll 1
-                        for (int c = 0; c < C::DP; c += 32) {
-                            float o[32];
-                            tc::tmem_ld32(o_tmem + c, o);
-                            tc::tmem_wait_ld();
-                            uint32_t r[32];
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(o[i] * f);
-                            tc::tmem_st32(o_tmem + c, r);
-                        }
-                    }
-                    ref = m == -INFINITY ? 0.f : m;
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
+                for (int pass = 0; pass < 3; ++pass) {
+                    const int half = pass == 1 ? 0 : 1;
                     if (active) {
-                        if (half == 1) half_scores(1, s);
+                        float s[64];
+                        tc::tmem_ld32(s_tmem + 64 * half, s);
+                        tc::tmem_ld32(s_tmem + 64 * half + 32, s + 32);
+                        tc::tmem_wait_ld();
+                        if (tail) {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                // lines beyond the unit's see nothing; what they hold is not read
+                                const uint32_t see = live ? seen_bits(words, 2 * a.W, tok0 + 64 * half + 32 * c - x.len, x.rows, j) : 0u;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) s[32 * c + i] = see & (1u << i) ? s[32 * c + i] : -INFINITY;
+                            }
+                        }
+                        if (pass < 2) {
+                            float mx[4] = {top, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                            for (int i = 0; i < 64; i += 4)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], s[i + c]);
+                            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                            if (pass == 0) continue;
+                            top *= scale;
+                            if (u == 0) {
+                                m = top;
+                            } else if (__any_sync(0xffffffffu, top > m + kSlack)) {
+                                const float to = top > m + kSlack ? top : m;
+                                const float f = to == -INFINITY ? 1.f : ex2(m - to);
+                                m = to;
+                                l *= f;
+                                // the product before has been added when its values' slot is free
+                                const uint32_t pos = base + value_place(dual ? tl - 1 : tl - 2, n, dual);
+                                ok = wait.warp(&empty[pos % C::NS], (pos / C::NS) & 1u);
+                                tc::tc_fence_after();
+#pragma unroll 1
+                                for (int c = 0; c < C::DP; c += 16) {
+                                    uint32_t o[16];
+                                    tc::tmem_ld16(o_tmem + c, o);
+                                    tc::tmem_wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                    tc::tmem_st16(o_tmem + c, o);
+                                }
+                            }
+                            ref = m == -INFINITY ? 0.f : m;
+                        }
                         float sum[4] = {0.f, 0.f, 0.f, 0.f};
                         uint32_t r[32];
 #pragma unroll
@@ -520,6 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                         tc::tmem_wait_st();
                         tc::tc_fence_before();
+                    } else if (pass == 0) {
+                        continue;
                     }
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&p_ready[2 * w + half]);
@@ -559,39 +559,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // with two streams of the same lines each finishes half of the columns
                 const int c0 = dual ? 0 : w * (C::DP / 2), c1 = dual ? C::DP : c0 + C::DP / 2;
                 const size_t prow0 = (size_t)(whole ? 0 : x.slot) * p.lines + (row_first - x.first) * p.G;
+                const bool add = !dual && n > 1;  // one tile: the second stream's O is not this piece's
                 const int j4 = lane & 3;
 #pragma unroll 1
                 for (int rb = 0; rb < 32; rb += 16) {
                     if (32 * q + rb >= lines) break;
-                    const float fa[2] = {__shfl_sync(0xffffffffu, f0, rb + (lane >> 2)), __shfl_sync(0xffffffffu, f0, rb + 8 + (lane >> 2))};
-                    const float fb[2] = {__shfl_sync(0xffffffffu, f1, rb + (lane >> 2)), __shfl_sync(0xffffffffu, f1, rb + 8 + (lane >> 2))};
+                    // the two lines of this lane's elements: factors, place of the output
+                    float fa[2], fb[2];
+                    bool in[2];
+                    int jr[2];
+                    __nv_bfloat16 *out[2];
+                    float *part[2];
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int at = rb + 8 * hf + (lane >> 2), ln = 32 * q + at;
+                        fa[hf] = __shfl_sync(0xffffffffu, f0, at);
+                        fb[hf] = __shfl_sync(0xffffffffu, f1, at);
+                        in[hf] = ln < lines;
+                        const int row_in = (ln * tp.inv_group) >> 16, g = ln - row_in * p.G;  // ln / G
+                        jr[hf] = row_first + row_in;
+                        out[hf] = static_cast<__nv_bfloat16 *>(a.out) + ((size_t)(x.row0 + jr[hf]) * a.Hq + x.head * p.G + g) * a.D + 8 * j4;
+                        part[hf] = p.part_o + (prow0 + ln) * p.stride + 4 * j4;
+                    }
 #pragma unroll 1
                     for (int c = c0; c < c1; c += 32) {
                         const uint32_t from = tmem + quad + ((uint32_t)rb << 16) + 256 + c;
-                        float o[16];
+                        float o[16], o1[16];
                         tc::tmem_ld_frag32(from + (dual ? 128 * w : 0), o);
-                        if (dual || n == 1) {  // one tile: the second stream's O is not this piece's
-                            tc::tmem_wait_ld();
+                        if (add) tc::tmem_ld_frag32(from + 128, o1);
+                        tc::tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] *= fa[(i >> 1) & 1];
-                        } else {
-                            float o1[16];
-                            tc::tmem_ld_frag32(from + 128, o1);
-                            tc::tmem_wait_ld();
+                        for (int i = 0; i < 16; ++i) o[i] *= fa[(i >> 1) & 1];
+                        if (add) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = fmaf(fa[(i >> 1) & 1], o[i], fb[(i >> 1) & 1] * o1[i]);
+                            for (int i = 0; i < 16; ++i) o[i] = fmaf(fb[(i >> 1) & 1], o1[i], o[i]);
                         }
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            const int ln = 32 * q + rb + 8 * hf + (lane >> 2);  // the line of these elements
-                            const bool in = ln < lines;
-                            const int g = ln % p.G, jr = row_first + ln / p.G;
-                            if (any_bad && in) {
-                                const uint32_t *mine = a.mask ? reinterpret_cast<const uint32_t *>(a.mask + (size_t)(x.row0 + jr) * a.W) : nullptr;
+                        if (any_bad) {
+#pragma unroll 1
+                            for (int hf = 0; hf < 2; ++hf) {
+                                if (!in[hf]) continue;
+                                const uint32_t *mine = a.mask ? reinterpret_cast<const uint32_t *>(a.mask + (size_t)(x.row0 + jr[hf]) * a.W) : nullptr;
+#pragma unroll 1
                                 for (int b = 0; b < 256; ++b) {
                                     if (!((flags[b >> 5] >> (b & 31)) & 1u)) continue;
                                     const int rel = b + base_rel, tok = x.len + rel;
-                                    if (!(seen_bits(mine, 2 * a.W, rel, x.rows, jr) & 1u)) continue;
+                                    if (!(seen_bits(mine, 2 * a.W, rel, x.rows, jr[hf]) & 1u)) continue;
                                     int pg = a.table[(size_t)x.r * a.max_pages + tok / a.page];
                                     if (pg < 0 || pg >= a.n_pages) pg = 0;
                                     const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v_cache) +
@@ -602,26 +614,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         for (int e = 0; e < 2; ++e) {
                                             const int d = c + 8 * k + 2 * j4 + e;
                                             const float val = d < a.D ? __bfloat162float(v[d]) : 0.f;
-                                            if (!(fabsf(val) < INFINITY)) o[4 * k + 2 * hf + e] += val;
+                                            if (fabsf(val) < INFINITY) continue;
+                                            if (hf == 0) o[4 * k + e] += val;
+                                            else o[4 * k + 2 + e] += val;
                                         }
                                 }
                             }
+                            __syncwarp();
+                        }
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
                             if (whole) {
                                 uint32_t r[4];
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) r[k] = pack(o[4 * k + 2 * hf], o[4 * k + 2 * hf + 1]);
                                 transpose_quad(r, j4);  // now columns c + 8 j4 .. + 7
-                                const int d = c + 8 * j4;
-                                if (in && d < a.D) {
-                                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) +
-                                                         ((size_t)(x.row0 + jr) * a.Hq + x.head * p.G + g) * a.D + d;
-                                    *reinterpret_cast<uint4 *>(out) = make_uint4(r[0], r[1], r[2], r[3]);
-                                }
-                            } else if (in) {
-                                float *out = p.part_o + (prow0 + ln) * p.stride + c + 4 * j4;
+                                if (in[hf] && c + 8 * j4 < a.D)
+                                    *reinterpret_cast<uint4 *>(out[hf] + c) = make_uint4(r[0], r[1], r[2], r[3]);
+                            } else if (in[hf]) {
 #pragma unroll
                                 for (int k = 0; k < 4; k += 2)
-                                    *reinterpret_cast<float4 *>(out + 8 * k) =
+                                    *reinterpret_cast<float4 *>(part[hf] + c + 8 * k) =
                                         make_float4(o[4 * k + 2 * hf], o[4 * k + 2 * hf + 1], o[4 * k + 4 + 2 * hf], o[4 * k + 5 + 2 * hf]);
                             }
                         }
@@ -679,7 +692,7 @@ cudaError_t launch_as(const TcParams &tp, int grid, const CUtensorMap &q, const 
 
 bool tc_supported(const dspark_tree_attention_args &a) {
     auto al16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
-    return a.dtype == DSPARK_BF16 && a.D % 8 == 0 && a.D <= 128 && a.page % 8 == 0 && a.Hq / a.H <= 128 && al16(a.q) &&
+    return a.dtype == DSPARK_BF16 && a.scale >= 0.f && a.D % 8 == 0 && a.D <= 128 && a.page % 8 == 0 && a.Hq / a.H <= 128 && al16(a.q) &&
            al16(a.k_cache) && al16(a.v_cache) && al16(a.out) && a.q_row % 8 == 0 && a.q_head % 8 == 0 && a.q_row > 0 &&
            a.q_head > 0 && a.q_row < (1ll << 38) && a.q_head < (1ll << 38) && tc_kernels_enabled() && tc_available();
 }
@@ -697,7 +710,9 @@ cudaError_t launch_tc(Params p, int grid, cudaStream_t s) {
     const dspark_tree_attention_args &a = p.a;
     TcParams tp{};
     tp.op_rows = 128 / p.G;
+    tp.inv_group = (65536 + p.G - 1) / p.G;
     p.tile_log2 = kTileLog2;
+    p.unit_cost = kUnitCost;
     tp.p = p;
     tp.box = a.page & -a.page;
     if (tp.box > kTile) tp.box = kTile;
