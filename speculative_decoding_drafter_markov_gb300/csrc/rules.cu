@@ -5,22 +5,36 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tc.cuh"
 
 namespace dspark {
 
 namespace {
 
 // One CTA takes one request, one slice of the vocabulary and a run of the
-// request's rows.  It counts the request's text once, into a word per entry of
-// its slice in shared memory, and then passes over the slice of each row: the
-// counts are shared by the rows, and what a row continues is added before its
-// pass (and what only the row before continued taken out: a chain only adds).
-// Beside the logits' one read and one write there is the text, read once per
-// slice from L2; a 16-byte piece whose entries are all forbidden is not read.
-// Bound by HBM at the large end.
+// request's rows.  Few entries of a vocabulary stand in a text or a bias list, so
+// the work is split in two:
+// * the grammar covers every entry of a row: 16-byte pieces with forbidden entries
+//   at -inf (a piece that is forbidden whole is not read; in place, one that is
+//   allowed whole is not touched);
+// * the text is counted into a word per entry of the slice in shared memory, shared
+//   by the rows, the entries that any other rule can touch are listed, and these
+//   are computed for every row, a thread each.  Drafted tokens are marked in the
+//   words; a row counts those that it continues.
+// Each warp has a part of the slice to itself after the counting: a list of its own,
+// and two places in shared memory through which the rows' parts go, a bulk copy in
+// while the row before is worked on.  The listed entries are computed there (as
+// 2-byte reads and writes of global memory they took as long as half of the copy)
+// and the grammar on the way out; no warp waits for another.  In place there is
+// no copy to join, and the listed entries are scattered.
+// Bound by HBM: the logits' one read and one write.  The text is read once per
+// slice, from L2, which is why a slice is large.
 constexpr int kRulesThreads = 256;
-constexpr int kBiasList = 256;  // bias entries of a slice kept in shared memory
-constexpr uint32_t kPromptBit = 1u << 31, kBiasBit = 1u << 30, kCountMask = kBiasBit - 1;
+constexpr int kBiasList = 256;   // bias entries of a slice kept in shared memory
+constexpr int kWarps = kRulesThreads / 32;
+constexpr int kPart = 2048;      // bytes of a row that a warp stages: its part of a slice
+constexpr int kSliceBytes = kPart * kWarps;
+constexpr uint32_t kPromptBit = 1u << 31, kBiasBit = 1u << 30, kDraftBit = 1u << 29, kCountMask = kDraftBit - 1;
 
 struct Bias {
     const int *id;      // the slice's entries in shared memory, in their order,
@@ -32,64 +46,56 @@ struct RowRules {
     float rep, inv_rep, freq, pres;
 };
 
-__device__ __noinline__ float biased(float z, int v, Bias b) {
-    for (int i = 0; i < b.n; ++i)
-        if (b.id[i] == v) z += b.val[i];
-    return z;
-}
-
 __device__ __forceinline__ float apply(float z, uint32_t word, int v, const RowRules &k, const Bias &b) {
     const uint32_t c = word & kCountMask;
     if (word & (kPromptBit | kCountMask)) z *= z > 0.f ? k.inv_rep : k.rep;
     z = fmaf(-k.freq, (float)c, z);
     if (c) z -= k.pres;
-    if (word & kBiasBit) z = biased(z, v, b);
+    if (word & kBiasBit)
+        for (int i = 0; i < b.n; ++i)
+            if (b.id[i] == v) z += b.val[i];
     return z;
 }
-
-// 16 bytes of logits
-template <typename T>
-struct Piece;
-template <>
-struct Piece<float> {
-    static constexpr int N = 4;
-    __device__ static __forceinline__ void get(const uint4 &v, float (&z)[N]) {
-        z[0] = __uint_as_float(v.x), z[1] = __uint_as_float(v.y), z[2] = __uint_as_float(v.z), z[3] = __uint_as_float(v.w);
-    }
-    __device__ static __forceinline__ uint4 put(const float (&z)[N]) {
-        return make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]), __float_as_uint(z[3]));
-    }
-};
-template <>
-struct Piece<__nv_bfloat16> {
-    static constexpr int N = 8;
-    __device__ static __forceinline__ void get(const uint4 &v, float (&z)[N]) {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[2 * i] = __uint_as_float(w[i] << 16), z[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-    __device__ static __forceinline__ uint4 put(const float (&z)[N]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 two = __floats2bfloat162_rn(z[2 * i], z[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&two);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-};
 
 __device__ __forceinline__ void put(float *p, float z) { *p = z; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float z) { *p = __float2bfloat16_rn(z); }
 
-// kVec: rows of T and out start on 16-byte boundaries
-template <typename T, bool kVec>
-__global__ void __launch_bounds__(kRulesThreads) logit_rules_kernel(const dspark_logit_rules_args a, int slice) {
-    extern __shared__ __align__(16) uint32_t word[];  // [slice]
+// a 16-byte piece with the entries whose bit is clear at -inf; keep[i]: the two bits
+// of i as masks of 16 bits each
+__device__ __forceinline__ uint4 forbid(uint4 v, uint32_t ok, const uint32_t *, float) {
+    const uint32_t inf = 0xff800000u;
+    return make_uint4(ok & 1 ? v.x : inf, ok & 2 ? v.y : inf, ok & 4 ? v.z : inf, ok & 8 ? v.w : inf);
+}
+__device__ __forceinline__ uint4 forbid(uint4 v, uint32_t ok, const uint32_t *keep, __nv_bfloat16) {
+    const uint32_t inf = 0xff80ff80u, m0 = keep[ok & 3], m1 = keep[(ok >> 2) & 3], m2 = keep[(ok >> 4) & 3], m3 = keep[ok >> 6];
+    return make_uint4((v.x & m0) | (inf & ~m0), (v.y & m1) | (inf & ~m1), (v.z & m2) | (inf & ~m2), (v.w & m3) | (inf & ~m3));
+}
+
+// `bits` bits of a grammar row from entry v on (kAligned: in one word)
+template <bool kAligned>
+__device__ __forceinline__ uint32_t allowed(const uint32_t *allow, int v, int bits) {
+    const int sh = v & 31;
+    uint32_t x = allow[v >> 5] >> sh;
+    if (!kAligned && sh + bits > 32) x |= allow[(v >> 5) + 1] << (32 - sh);
+    return x & ((1u << bits) - 1);
+}
+
+// kAligned: every row of T and out starts on a 16-byte boundary; else vec: T and out
+// lie alike to 16 bytes
+template <typename T, bool kAligned>
+__global__ void __launch_bounds__(kRulesThreads, 3) logit_rules_kernel(const dspark_logit_rules_args a, int slice, bool vec) {
+    extern __shared__ __align__(128) unsigned char stage[];  // [warp][2][kPart], then the slice's words
+    uint32_t *word = reinterpret_cast<uint32_t *>(stage + 2 * kSliceBytes);
+    __shared__ uint64_t landed[kWarps][2];
+    __shared__ int abort_word;
     __shared__ int bias_id[kBiasList];
     __shared__ float bias_val[kBiasList];
     __shared__ int bias_n;
-    const int tid = threadIdx.x, lane = tid & 31;
+    __shared__ uint32_t keep[4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (kAligned) vec = true;
+    if (tid < 4) keep[tid] = (tid & 1 ? 0xffffu : 0u) | (tid & 2 ? 0xffff0000u : 0u);
+    __syncthreads();
     const int r = blockIdx.y, v0 = blockIdx.x * slice, v1 = min(a.V, v0 + slice);
     // the request's numbers, all loads in flight together
     const int row0 = a.row_start[r], row_end = a.row_start[r + 1];
@@ -119,177 +125,276 @@ __global__ void __launch_bounds__(kRulesThreads) logit_rules_kernel(const dspark
     if (j0 == j1) return;
     k.inv_rep = 1.f / k.rep;
     const bool penal = k.rep != 1.f || k.freq != 0.f || k.pres != 0.f;
-    const bool counted = penal || b1 > b0;  // the entries' words are in use
+    const bool path = penal && a.tok;
     Bias bias{bias_id, bias_val, 0};
 
-    if (counted) {
-        for (int i = 4 * tid; i < slice; i += 4 * kRulesThreads) *reinterpret_cast<uint4 *>(word + i) = make_uint4(0u, 0u, 0u, 0u);
-        __syncthreads();
-        if (penal) {
-            const int32_t *text = a.hist + (size_t)r * a.max_hist;
-#pragma unroll 8
-            for (int i = tid; i < n; i += kRulesThreads) {
-                const int v = text[i];
-                if (v < 0 || v >= a.V) set_err(a.err, DSPARK_ERR_RANGE);
-                if (v >= v0 && v < v1) {
-                    if (i < np) atomicOr(&word[v - v0], kPromptBit);
-                    else atomicAdd(&word[v - v0], 1u);
-                }
-            }
-        }
-        if (b1 > b0 && tid < 32) {  // one warp, so that the list keeps the entries' order
-            int found = 0;
-            for (int i = b0; i < b1; i += 32) {
-                const int v = i + lane < b1 ? a.bias_id[i + lane] : v0;
-                if (v < 0 || v >= a.V) set_err(a.err, DSPARK_ERR_RANGE);
-                const bool in = i + lane < b1 && v >= v0 && v < v1;
-                const unsigned who = __ballot_sync(0xffffffffu, in);
-                const int at = found + __popc(who & ((1u << lane) - 1));
-                if (in) {
-                    atomicOr(&word[v - v0], kBiasBit);
-                    if (at < kBiasList) {
-                        bias_id[at] = v;
-                        bias_val[at] = a.bias_val[i + lane];
-                    }
-                }
-                found += __popc(who);
-            }
-            if (lane == 0) bias_n = found;
-        } else if (tid == 0) {
-            bias_n = 0;
-        }
-        __syncthreads();
-        bias.n = bias_n;
-        if (bias.n > kBiasList) bias = Bias{a.bias_id + b0, a.bias_val + b0, b1 - b0};
-    }
-
     const int words = (a.V + 31) / 32;
-    const bool path = penal && a.tok;
-    auto add = [&](int at, uint32_t by) {  // drafted row `at` joins or leaves the path
-        const int v = a.tok[row0 + at];
-        if (v < 0 || v >= a.V) set_err(a.err, DSPARK_ERR_RANGE);
-        if (v >= v0 && v < v1) atomicAdd(&word[v - v0], by);
+    const bool in_place = a.T == a.out;
+    auto grammar = [&](int row) -> const uint32_t * {
+        const int m = a.allow ? a.allow_row[row] : -1;
+        return m >= 0 && m < a.n_allow ? a.allow + (size_t)m * words : nullptr;
     };
-    for (int j = j0; j < j1; ++j) {
-        const int row = row0 + j;
-        if (path && !a.mask) {
-            // rows 1 .. j; those before j are in already, but for the run's first row
-            for (int at = j == j0 ? 1 : j; at <= j; ++at) {
-                if (at == 0) continue;
-                const int v = a.tok[row0 + at];
-                if (v >= v0 && v < v1) {  // the same for all threads: few rows touch a slice
-                    __syncthreads();
-                    if (tid == 0) add(at, 1u);
-                    __syncthreads();
-                } else if (tid == 0 && (v < 0 || v >= a.V)) {
-                    set_err(a.err, DSPARK_ERR_RANGE);
-                }
-            }
-        } else if (path) {
-            const uint64_t *now = a.mask + (size_t)row * a.W, *was = now - a.W;
-            for (int at = tid; at < (rows + kRulesThreads - 1) / kRulesThreads * kRulesThreads; at += kRulesThreads) {
-                int change = 0;
-                if (at > 0 && at < rows) {
-                    change = (int)((now[at >> 6] >> (at & 63)) & 1);
-                    if (j > j0) change -= (int)((was[at >> 6] >> (at & 63)) & 1);
-                }
-                __syncthreads();  // the row before is done
-                if (change) add(at, (uint32_t)change);
-            }
-            __syncthreads();
+    constexpr int E = 16 / (int)sizeof(T);
+    constexpr uint32_t kAll = (1u << E) - 1;
+    // the pieces [va, vb) of a row's entries [lo, hi) lie on 16-byte boundaries of memory;
+    // what is left before and after them goes entry by entry
+    auto pieces = [&](const T *src, int lo, int hi, int &va, int &vb) {
+        if (kAligned) {
+            va = lo;
+            vb = hi;
+            return;
         }
-        const uint32_t *allow = nullptr;
-        if (a.allow) {
-            const int m = a.allow_row[row];
-            if (m >= a.n_allow) {
-                if (tid == 0) set_err(a.err, DSPARK_ERR_RANGE);
-            } else if (m >= 0) {
-                allow = a.allow + (size_t)m * words;
-            }
-        }
+        va = vb = hi;
+        if (!vec) return;
+        const int lead = (int)((16 - (reinterpret_cast<uintptr_t>(src + lo) & 15)) & 15) / (int)sizeof(T);
+        va = min(hi, lo + lead);
+        vb = va + (hi - va) / E * E;
+    };
+    auto copy_row = [&](int row) {
+        if (tid == 0 && a.allow && a.allow_row[row] >= a.n_allow) set_err(a.err, DSPARK_ERR_RANGE);
+        const uint32_t *allow = grammar(row);
         const T *src = static_cast<const T *>(a.T) + (size_t)row * a.V;
         T *dst = static_cast<T *>(a.out) + (size_t)row * a.V;
-        if (kVec) {
-            constexpr int E = Piece<T>::N, U = 4;
-            constexpr uint32_t kAll = (1u << E) - 1;
-            for (int vb = v0 + E * tid; vb < v1; vb += U * E * kRulesThreads) {
+        if (!in_place || allow) {
+            constexpr int U = 4;
+            int va, vb;
+            pieces(src, v0, v1, va, vb);
+            for (int first = va + E * tid; first < vb; first += U * E * kRulesThreads) {
                 uint32_t ok[U];
                 uint4 raw[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int v = vb + u * E * kRulesThreads;
-                    ok[u] = v < v1 ? kAll : 0u;
-                    if (allow && v < v1) ok[u] = (allow[v >> 5] >> (v & 31)) & kAll;
+                    const int v = first + u * E * kRulesThreads;
+                    ok[u] = kAll;
+                    if (allow && v < vb) ok[u] = allowed<kAligned>(allow, v, E);
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int v = vb + u * E * kRulesThreads;
+                    const int v = first + u * E * kRulesThreads;
                     raw[u] = make_uint4(0u, 0u, 0u, 0u);
-                    if (ok[u]) raw[u] = __ldcs(reinterpret_cast<const uint4 *>(src + v));
+                    if (v < vb && ok[u] && !(in_place && ok[u] == kAll)) raw[u] = __ldcs(reinterpret_cast<const uint4 *>(src + v));
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int v = vb + u * E * kRulesThreads;
-                    if (v >= v1) break;
-                    uint4 res = raw[u];
-                    uint32_t w[E], any = 0;
-                    if (counted) {
-#pragma unroll
-                        for (int i = 0; i < E; i += 4) {
-                            const uint4 q = *reinterpret_cast<const uint4 *>(word + (v - v0) + i);
-                            w[i] = q.x, w[i + 1] = q.y, w[i + 2] = q.z, w[i + 3] = q.w;
-                            any |= q.x | q.y | q.z | q.w;
-                        }
-                    }
-                    if (any || ok[u] != kAll) {
-                        float z[E];
-                        Piece<T>::get(res, z);
-                        if (any) {
-#pragma unroll
-                            for (int i = 0; i < E; ++i)
-                                if (w[i]) z[i] = apply(z[i], w[i], v + i, k, bias);
-                        }
-#pragma unroll
-                        for (int i = 0; i < E; ++i)
-                            if (!((ok[u] >> i) & 1)) z[i] = -INFINITY;
-                        res = Piece<T>::put(z);
-                    }
-                    __stcs(reinterpret_cast<uint4 *>(dst + v), res);
+                    const int v = first + u * E * kRulesThreads;
+                    if (v >= vb || (in_place && ok[u] == kAll)) continue;
+                    if (allow) raw[u] = forbid(raw[u], ok[u], keep, T());
+                    __stcs(reinterpret_cast<uint4 *>(dst + v), raw[u]);
                 }
             }
-        } else {
-            constexpr int U = 8;
-            for (int vb = v0 + tid; vb < v1; vb += U * kRulesThreads) {
-                float z[U];
-                bool ok[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int v = vb + u * kRulesThreads;
-                    z[u] = v < v1 ? to_f32(src[v]) : 0.f;
-                    ok[u] = !allow || v >= v1 || ((allow[v >> 5] >> (v & 31)) & 1);
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int v = vb + u * kRulesThreads;
-                    if (v >= v1) break;
-                    if (counted) {
-                        const uint32_t w = word[v - v0];
-                        if (w) z[u] = apply(z[u], w, v, k, bias);
-                    }
-                    put(dst + v, ok[u] ? z[u] : -INFINITY);
-                }
+            for (int i = tid; !kAligned && i < (va - v0) + (v1 - vb); i += kRulesThreads) {
+                const int v = i < va - v0 ? v0 + i : vb + i - (va - v0);
+                dst[v] = !allow || allowed<true>(allow, v, 1) ? src[v] : T(-INFINITY);
             }
         }
+    };
+    if (!penal && b1 == b0) {
+        for (int j = j0; j < j1; ++j) copy_row(row0 + j);
+        return;
+    }
+
+    // this warp's part of the slice
+    const bool staged = vec && !in_place;
+    const int part = slice / kWarps, lo = min(v1, v0 + warp * part), hi = min(v1, lo + part);
+    unsigned char *places = stage + warp * 2 * kPart;
+    auto load = [&](int j) {
+        const T *src = static_cast<const T *>(a.T) + (size_t)(row0 + j) * a.V;
+        int va, vb;
+        pieces(src, lo, hi, va, vb);
+        const int b = (j - j0) & 1;
+        const uint32_t bytes = (uint32_t)(vb - va) * (uint32_t)sizeof(T);
+        tc::mbar_expect_tx(&landed[warp][b], bytes);
+        if (bytes) tc::bulk_load(places + b * kPart, src + va, bytes, &landed[warp][b]);
+    };
+    if (lane == 0) {
+        tc::mbar_init(&landed[warp][0], 1);
+        tc::mbar_init(&landed[warp][1], 1);
+        tc::fence_mbar_init();
+        if (staged) {
+            load(j0);
+            if (j0 + 1 < j1) load(j0 + 1);
+        }
+    }
+    if (tid == 0) abort_word = bias_n = 0;
+    // the grammar's bits of a row are read a row ahead, the first during the counting
+    constexpr int kMine = kPart / 16 / 32;  // a lane's pieces
+    auto grammar_bits = [&](int j, uint32_t (&ok)[kMine]) {
+        const uint32_t *allow = grammar(row0 + j);
+        const T *src = static_cast<const T *>(a.T) + (size_t)(row0 + j) * a.V;
+        int va, vb;
+        pieces(src, lo, hi, va, vb);
+#pragma unroll
+        for (int u = 0; u < kMine; ++u) {
+            const int v = va + E * (lane + 32 * u);
+            ok[u] = allow && v < vb ? allowed<kAligned>(allow, v, E) : kAll;
+        }
+        return allow;
+    };
+    uint32_t ok[kMine];
+    const uint32_t *allow = staged ? grammar_bits(j0, ok) : nullptr;
+    // the first tokens of the text are on their way while the words are cleared
+    constexpr int kAhead = 8;
+    const int32_t *text = a.hist + (size_t)r * a.max_hist;
+    if (!penal) n = 0;
+    int ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) ahead[i] = tid + i * kRulesThreads < n ? text[tid + i * kRulesThreads] : 0;
+    for (int i = 4 * tid; i < slice; i += 4 * kRulesThreads) *reinterpret_cast<uint4 *>(word + i) = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+    auto count = [&](int i, int v) {
+        if ((unsigned)v >= (unsigned)a.V) set_err(a.err, DSPARK_ERR_RANGE);
+        if (v >= v0 && v < v1) {
+            if (i < np) atomicOr(&word[v - v0], kPromptBit);
+            else atomicAdd(&word[v - v0], 1u);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (tid + i * kRulesThreads < n) count(tid + i * kRulesThreads, ahead[i]);
+#pragma unroll 8
+    for (int i = kAhead * kRulesThreads + tid; i < n; i += kRulesThreads) count(i, text[i]);
+    if (path)  // whatever a row of the run may continue
+        for (int at = 1 + tid; at < rows; at += kRulesThreads) {
+            const int v = a.tok[row0 + at];
+            if ((unsigned)v >= (unsigned)a.V) set_err(a.err, DSPARK_ERR_RANGE);
+            if (v >= v0 && v < v1) atomicOr(&word[v - v0], kDraftBit);
+        }
+    if (b1 > b0 && tid < 32) {  // one warp, so that the list keeps the entries' order
+        int found = 0;
+        for (int i = b0; i < b1; i += 32) {
+            const int v = i + lane < b1 ? a.bias_id[i + lane] : v0;
+            if ((unsigned)v >= (unsigned)a.V) set_err(a.err, DSPARK_ERR_RANGE);
+            const bool in = i + lane < b1 && v >= v0 && v < v1;
+            const unsigned who = __ballot_sync(0xffffffffu, in);
+            const int at = found + __popc(who & ((1u << lane) - 1));
+            if (in) {
+                atomicOr(&word[v - v0], kBiasBit);
+                if (at < kBiasList) {
+                    bias_id[at] = v;
+                    bias_val[at] = a.bias_val[i + lane];
+                }
+            }
+            found += __popc(who);
+        }
+        if (lane == 0) bias_n = found;
+    }
+    __syncthreads();
+    bias.n = bias_n;
+    if (bias.n > kBiasList) bias = Bias{a.bias_id + b0, a.bias_val + b0, b1 - b0};
+    // The warp's list of touched entries {word, place}, over its words: a lane takes
+    // `part / 32` of them into registers.  With more entries than fit there the words
+    // stay, and are searched for every row.
+    constexpr int kLaneWords = kPart / (int)sizeof(T) / 32;
+    uint32_t *mine = word + warp * part;
+    uint2 *list = reinterpret_cast<uint2 *>(mine);
+    int listed = 0;
+    {
+        uint32_t w[kLaneWords];
+        int n_own = 0;
+#pragma unroll
+        for (int i = 0; i < kLaneWords; ++i) {
+            w[i] = 32 * i < part ? mine[32 * i + lane] : 0u;
+            n_own += w[i] != 0;
+        }
+        int at = n_own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, at, d);
+            if (lane >= d) at += y;
+        }
+        listed = __shfl_sync(0xffffffffu, at, 31);
+        at -= n_own;
+        if (listed <= part / 2) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kLaneWords; ++i)
+                if (w[i]) list[at++] = make_uint2(w[i], (uint32_t)(32 * i + lane));
+            __syncwarp();
+        }
+    }
+    const bool by_list = listed <= part / 2;
+    // f(place in the part, word) for the touched entries, a lane each
+    auto touched = [&](auto f) {
+        if (by_list) {
+            for (int i = lane; i < listed; i += 32) f((int)list[i].y, list[i].x);
+        } else {
+            for (int i = lane; i < part; i += 32)
+                if (mine[i]) f(i, mine[i]);
+        }
+    };
+
+    // entry v of row j, whose word is w
+    auto value = [&](int j, int v, uint32_t w, float z) {
+        if (w & kDraftBit) {  // drafted in the request: how often on this row's path
+            const uint64_t *mine = a.mask ? a.mask + (size_t)(row0 + j) * a.W : nullptr;
+            for (int at = 1; at < (mine ? rows : j + 1); ++at)
+                if (a.tok[row0 + at] == v && (!mine || ((mine[at >> 6] >> (at & 63)) & 1))) ++w;
+        }
+        return apply(z, w, v, k, bias);
+    };
+    auto scatter = [&](int j, int v, uint32_t w, const uint32_t *allow, const T *src, T *dst) {
+        if (!allow || allowed<true>(allow, v, 1)) put(dst + v, value(j, v, w, to_f32(src[v])));
+    };
+
+    if (!staged) {
+        for (int j = j0; j < j1; ++j) copy_row(row0 + j);
+        __syncthreads();  // another thread's pieces are written
+        for (int j = j0; j < j1; ++j) {
+            const uint32_t *allow = grammar(row0 + j);
+            const T *src = static_cast<const T *>(a.T) + (size_t)(row0 + j) * a.V;
+            T *dst = static_cast<T *>(a.out) + (size_t)(row0 + j) * a.V;
+            touched([&](int i, uint32_t w) { scatter(j, lo + i, w, allow, src, dst); });
+        }
+        return;
+    }
+
+    volatile int *abort_flag = &abort_word;
+    for (int j = j0; j < j1; ++j) {
+        const int b = (j - j0) & 1;
+        uint32_t ok_next[kMine];
+        const uint32_t *allow_next = j + 1 < j1 ? grammar_bits(j + 1, ok_next) : nullptr;
+        if (tid == 0 && a.allow && a.allow_row[row0 + j] >= a.n_allow) set_err(a.err, DSPARK_ERR_RANGE);
+        const T *src = static_cast<const T *>(a.T) + (size_t)(row0 + j) * a.V;
+        T *dst = static_cast<T *>(a.out) + (size_t)(row0 + j) * a.V;
+        int va, vb;
+        pieces(src, lo, hi, va, vb);
+        T *row = reinterpret_cast<T *>(places + b * kPart) - va;  // entry v at row[v]
+        for (int i = lane; !kAligned && i < (va - lo) + (hi - vb); i += 32) {
+            const int v = i < va - lo ? lo + i : vb + i - (va - lo);
+            dst[v] = !allow || allowed<true>(allow, v, 1) ? src[v] : T(-INFINITY);
+        }
+        // a wait that runs out is reported; the rows are then unspecified
+        if (lane == 0) tc::mbar_wait(&landed[warp][b], ((j - j0) >> 1) & 1, abort_flag, a.err);
+        __syncwarp();
+        touched([&](int i, uint32_t w) {
+            const int v = lo + i;
+            if (!kAligned && (v < va || v >= vb)) scatter(j, v, w, allow, src, dst);
+            else put(row + v, value(j, v, w, to_f32(row[v])));
+        });
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < kMine; ++u) {
+            const int v = va + E * (lane + 32 * u);
+            if (v >= vb) break;
+            uint4 q = *reinterpret_cast<const uint4 *>(row + v);
+            if (ok[u] != kAll) q = forbid(q, ok[u], keep, T());
+            __stcs(reinterpret_cast<uint4 *>(dst + v), q);
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && j + 2 < j1) load(j + 2);
+        allow = allow_next;
+#pragma unroll
+        for (int u = 0; u < kMine; ++u) ok[u] = ok_next[u];
     }
 }
 
 template <typename T>
 cudaError_t launch_as(const dspark_logit_rules_args &a, cudaStream_t s) {
-    // Slices as large as leave every SM three CTAs (a slice's words take 4 bytes
-    // an entry, and the text is read once per slice); where requests are few the
+    // Slices as large as leave every SM three CTAs; where requests are few the
     // rows are spread too, at the price of counting the text for each run.
     const long long want = 3ll * sm_count();
-    int slice = 8192;
+    int slice = kSliceBytes / (int)sizeof(T);
     while (slice > 1024 && (long long)a.R * ((a.V + slice - 1) / slice) < want) slice /= 2;
     const int slices = (a.V + slice - 1) / slice;
     const long long per = (a.N + a.R - 1) / a.R;
@@ -297,10 +402,13 @@ cudaError_t launch_as(const dspark_logit_rules_args &a, cudaStream_t s) {
     if (runs > per) runs = per;
     if (runs < 1) runs = 1;
     const dim3 grid(slices, a.R, (unsigned)runs);
-    const size_t smem = sizeof(uint32_t) * slice;
-    const uintptr_t at = reinterpret_cast<uintptr_t>(a.T) | reinterpret_cast<uintptr_t>(a.out) | ((uintptr_t)a.V * sizeof(T));
-    if ((at & 15) == 0) logit_rules_kernel<T, true><<<grid, kRulesThreads, smem, s>>>(a, slice);
-    else logit_rules_kernel<T, false><<<grid, kRulesThreads, smem, s>>>(a, slice);
+    const size_t smem = 2 * kSliceBytes + sizeof(uint32_t) * (kSliceBytes / sizeof(T));
+    const uintptr_t t = reinterpret_cast<uintptr_t>(a.T), o = reinterpret_cast<uintptr_t>(a.out);
+    const bool aligned = ((t | o | (uintptr_t)a.V * sizeof(T)) & 15) == 0;
+    auto kern = aligned ? logit_rules_kernel<T, true> : logit_rules_kernel<T, false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, kRulesThreads, smem, s>>>(a, slice, ((t ^ o) & 15) == 0);
     return cudaGetLastError();
 }
 

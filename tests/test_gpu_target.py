@@ -545,6 +545,12 @@ def test_rules(dtype, R, most, V, tree):
     rules_check(s, got, want)
     same = dsp.logit_rules(keep, ints(s["start"]), **args, out=keep)  # in place
     assert same is keep and torch.equal(keep, got)
+    # rows that do not start on the boundaries of the output's
+    n = s["T"].numel()
+    odd = torch.empty(n + 1, dtype=dtype, device="cuda")[1:].view_as(s["T"])
+    assert torch.equal(dsp.logit_rules(s["T"], ints(s["start"]), **args, out=odd), got)
+    odd.copy_(s["T"])
+    assert torch.equal(dsp.logit_rules(odd, ints(s["start"]), **args), got)
 
 
 @pytest.mark.parametrize("off", [("hist",), ("prompt_len",), ("tok",), ("rep",), ("freq",), ("pres",), ("bias",), ("allow",),
@@ -567,6 +573,16 @@ def test_rules_long_bias_lists_and_texts():
     s["bias_id"], s["bias_val"] = rng.integers(0, 700, 905), rng.uniform(-1, 1, 905)
     out, size = rules_expect(s)
     rules_check(s, dsp.logit_rules(s["T"], ints(s["start"]), **rules_args(s)), (out, size * 4))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [4096, 6001])
+def test_rules_texts_of_many_tokens(dtype, V):
+    """More said tokens in a slice than the kernel lists."""
+    s = rules_case(3, 4, V, dtype, seed=V, hist=9000)
+    s["hist_len"][:2] = 9000
+    s["prompt_len"][:2] = 4000
+    rules_check(s, dsp.logit_rules(s["T"], ints(s["start"]), **rules_args(s)), rules_expect(s))
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
