@@ -1,4 +1,5 @@
-"""ctypes binding of libdspark.so (include/dspark.h).
+"""Python binding of libdspark.so (include/dspark.h): ctypes, and for the target-pass
+operators the module built from csrc/bind.cpp.
 
 Argument marshalling only: every step of the hot path runs in the library's CUDA
 kernels.  PyTorch provides device memory (outputs and the scratch workspace are
@@ -8,6 +9,8 @@ library cannot be built or loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -479,51 +482,23 @@ def train_losses(zd, zt, xs, s, gamma, *, a_ce=0.1, a_tv=0.9, a_conf=1.0, want_r
 
 # --------------------------------------------------------------------- the target's pass
 # These run once per layer or per cycle on small inputs too, where the host's
-# share counts: every tensor is checked once, in one expression where it is right.
-_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# share counts; csrc/bind.cpp checks the tensors and makes the outputs.
+_bind = None
 
 
-def _want(name, t, dtype, shape):
-    """Address of a contiguous GPU tensor of this element type and shape (None: any)."""
-    if t.is_cuda and t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape):
-        return t.data_ptr()
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    return _ptr(t).value
-
-
-def _maybe(name, t, dtype, shape):
-    return None if t is None else _want(name, t, dtype, shape)
-
-
-def _heads(name, t, dtype, shape):
-    """Address, row stride and head stride of a [N, H, D] view whose D elements are adjacent."""
-    if not t.is_cuda:
-        raise ValueError("dspark tensors must live on the GPU")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    row, head, one = t.stride()
-    if one != 1 and shape[2] > 1:
-        raise ValueError(f"the elements of a head of {name} must be adjacent")
-    return t.data_ptr(), row, head
-
-
-def _queue(stream, device):
-    """Handle of the stream to work on: the one given, or the device's current one."""
-    return _raw_stream(device) if stream is None else stream.cuda_stream
-
-
-def _empty(stream, device, *shapes):
-    """Tensors made for `stream`, so that they may be used and freed on it."""
-    if stream is None:
-        return [torch.empty(n, dtype=d, device=device) for n, d in shapes]
-    with torch.cuda.stream(stream):
-        return [torch.empty(n, dtype=d, device=device) for n, d in shapes]
+def _target():
+    """The module of the target-pass calls, loaded beside the library."""
+    global _bind
+    if _bind is None:
+        load()
+        with _lock:
+            if _bind is None:
+                loader = importlib.machinery.ExtensionFileLoader("_dspark_bind", _build.BIND)
+                module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_dspark_bind", loader))
+                loader.exec_module(module)
+                module.set_errors(DSparkError, torch.OutOfMemoryError)
+                _bind = module
+    return _bind
 
 
 def page_map(lens, rows, table, held, free, n_free, *, page, N, parents=None, max_rows=None, out=None, err=None,
@@ -535,59 +510,20 @@ def page_map(lens, rows, table, held, free, n_free, *, page, N, parents=None, ma
     Returns {"held", "n_free", "row_start", "slot", "pos"} and, for trees,
     "mask" [N, ceil(max_rows / 64)] int64.  The new held and n_free are other
     tensors than the ones passed in: hand them to the next call."""
-    L = _lib or load()
-    R, max_pages = table.shape
-    device = table.get_device()
-    W = n_parents = 0
-    if parents is not None:
-        if max_rows is None or max_rows < 1:
-            raise ValueError("trees need max_rows")
-        W, n_parents = (max_rows + 63) // 64, parents.numel()
-    if out is None:
-        shapes = [(R, _I32), (1, _I32), (R + 1, _I32), (N, _I32), (N, _I32)]
-        if W:
-            shapes.append(((N, W), _I64))
-        out = dict(zip(("held", "n_free", "row_start", "slot", "pos", "mask"), _empty(stream, table.device, *shapes)))
-    per = (R,)
-    a = PageMapArgs(R, page, free.numel(), max_pages, N, n_parents, W, _want("lens", lens, _I32, per),
-                    _want("rows", rows, _I32, per), _maybe("parents", parents, _I32, None), _want("held", held, _I32, per),
-                    _want("n_free", n_free, _I32, (1,)), _want("table", table, _I32, None), _want("free", free, _I32, None),
-                    _want("held", out["held"], _I32, per), _want("n_free", out["n_free"], _I32, (1,)),
-                    _want("row_start", out["row_start"], _I32, (R + 1,)), _want("slot", out["slot"], _I32, (N,)),
-                    _want("pos", out["pos"], _I32, (N,)), _want("mask", out["mask"], _I64, (N, W)) if W else None,
-                    _maybe("err", err, _I32, None))
-    _check(L.dspark_page_map(a, _queue(stream, device)))
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return page_map(lens, rows, table, held, free, n_free, page=page, N=N, parents=parents, max_rows=max_rows,
+                            out=out, err=err)
+    return (_bind or _target()).page_map(lens, rows, table, held, free, n_free, page, N, parents, max_rows, out, err)
 
 
 def cache_store(k, v, slot, k_cache, v_cache, *, err=None, stream=None):
     """Write the rows' keys and values k, v [N, H, D] (views of a fused projection
     are fine) into the slots slot [N] int32 of the caches [n_pages, H, page, D]."""
-    L = _lib or load()
-    shape = n_pages, H, page, D = k_cache.shape
-    N = k.shape[0]
-    dt = k_cache.dtype
-    kp, k_row, k_head = _heads("k", k, dt, (N, H, D))
-    vp, v_row, v_head = _heads("v", v, dt, (N, H, D))
-    a = CacheStoreArgs(N, H, D, page, n_pages, _dtype_code(k_cache), kp, vp, k_row, k_head, v_row, v_head,
-                       _want("slot", slot, _I32, (N,)), _want("k_cache", k_cache, dt, None),
-                       _want("v_cache", v_cache, dt, shape), _maybe("err", err, _I32, None))
-    _check(L.dspark_cache_store(a, _queue(stream, k_cache.get_device())))
-
-
-def _tree_attention_struct(q, k_cache, v_cache, table, lens, row_start, mask, scale, max_rows, out, lse, err):
-    shape = n_pages, H, page, D = k_cache.shape
-    N, Hq = q.shape[:2]
-    R, max_pages = table.shape
-    dt = k_cache.dtype
-    qp, q_row, q_head = _heads("q", q, dt, (N, Hq, D))
-    W = 0 if mask is None else mask.shape[1]
-    return TreeAttentionArgs(R, N, Hq, H, D, page, n_pages, max_pages, _dtype_code(k_cache), W, max_rows,
-                             D ** -0.5 if scale is None else scale, qp, q_row, q_head, _want("k_cache", k_cache, dt, None),
-                             _want("v_cache", v_cache, dt, shape), _want("table", table, _I32, None),
-                             _want("lens", lens, _I32, (R,)), _want("row_start", row_start, _I32, (R + 1,)),
-                             _maybe("mask", mask, _I64, (N, W)), _maybe("out", out, dt, (N, Hq, D)),
-                             _maybe("lse", lse, _F32, (N, Hq)), _maybe("err", err, _I32, None))
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return cache_store(k, v, slot, k_cache, v_cache, err=err)
+    return (_bind or _target()).cache_store(k, v, slot, k_cache, v_cache, err)
 
 
 def tree_attention(q, k_cache, v_cache, table, lens, row_start, *, mask=None, scale=None, max_rows=1, out=None, ws=None,
@@ -595,27 +531,20 @@ def tree_attention(q, k_cache, v_cache, table, lens, row_start, *, mask=None, sc
     """Attention of the drafted rows q [N, Hq, D] over the cache and over their
     ancestors among the rows (include/dspark.h): table, row_start and mask as
     page_map gives them (mask None: chains), lens [R] the tokens before the
-    rows.  Returns {"out": [N, Hq, D], "lse": [N, Hq] fp32}; an `out` passed in
-    may leave "lse" out."""
-    L = _lib or load()
-    if out is None:
-        o, lse = _empty(stream, q.device, (q.shape, q.dtype), (q.shape[:2], _F32))
-        out = {"out": o, "lse": lse}
-    a = _tree_attention_struct(q, k_cache, v_cache, table, lens, row_start, mask, scale, max_rows, out["out"],
-                               out.get("lse"), err)
-    nbytes = L.dspark_tree_attention_workspace_size(a) or 256
-    if ws is None:
-        ws, = _empty(stream, q.device, (nbytes, torch.uint8))
-    else:
-        ws = _workspace(nbytes, q.device, ws)
-    _check(L.dspark_tree_attention(a, ws.data_ptr(), _queue(stream, q.get_device())))
-    return out
+    rows, scale 1 / sqrt(D) unless given.  Returns {"out": [N, Hq, D],
+    "lse": [N, Hq] fp32}; an `out` passed in may leave "lse" out."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return tree_attention(q, k_cache, v_cache, table, lens, row_start, mask=mask, scale=scale, max_rows=max_rows,
+                                  out=out, ws=ws, err=err)
+    return (_bind or _target()).tree_attention(q, k_cache, v_cache, table, lens, row_start, mask, scale, max_rows, out, ws,
+                                               err)
 
 
 def tree_attention_workspace_size(q, k_cache, v_cache, table, lens, row_start, *, mask=None, max_rows=1):
     """Scratch bytes dspark_tree_attention needs for this shape."""
-    a = _tree_attention_struct(q, k_cache, v_cache, table, lens, row_start, mask, None, max_rows, None, None, None)
-    return load().dspark_tree_attention_workspace_size(a)
+    return _target().tree_attention_workspace_size(q, k_cache, v_cache, table, lens, row_start, mask, None, max_rows, None,
+                                                   None, None)
 
 
 def logit_rules(T, row_start, *, tok=None, mask=None, hist=None, hist_len=None, prompt_len=None, rep=None, freq=None,
@@ -626,24 +555,10 @@ def logit_rules(T, row_start, *, tok=None, mask=None, hist=None, hist_len=None, 
     tok [N] the rows' tokens and mask their trees; rep, freq, pres [R] fp32;
     bias_start [R + 1], bias_id, bias_val; allow [n, ceil(V / 32)] int32 bits and
     allow_row [N].  Every rule may be None.  Returns out (T itself is fine)."""
-    L = _lib or load()
-    N, V = T.shape
-    R = row_start.numel() - 1
-    if out is None:
-        out, = _empty(stream, T.device, (T.shape, T.dtype))
-    W = 0 if mask is None else mask.shape[1]
-    n_bias = 0 if bias_id is None else bias_id.numel()
-    n_allow = 0 if allow is None else allow.shape[0]
-    max_hist = 0 if hist is None else hist.shape[1]
-    per, row = (R,), (N,)
-    a = LogitRulesArgs(R, N, V, _dtype_code(T), max_hist, n_bias, n_allow, W, _want("T", T, T.dtype, None),
-                       _want("row_start", row_start, _I32, None), _maybe("tok", tok, _I32, row),
-                       _maybe("mask", mask, _I64, (N, W)), _maybe("hist", hist, _I32, (R, max_hist)),
-                       _maybe("hist_len", hist_len, _I32, per), _maybe("prompt_len", prompt_len, _I32, per),
-                       _maybe("rep", rep, _F32, per), _maybe("freq", freq, _F32, per), _maybe("pres", pres, _F32, per),
-                       _maybe("bias_start", bias_start, _I32, (R + 1,)), _maybe("bias_id", bias_id, _I32, None),
-                       _maybe("bias_val", bias_val, _F32, (n_bias,)),
-                       _maybe("allow", allow, _I32, (n_allow, (V + 31) // 32)), _maybe("allow_row", allow_row, _I32, row),
-                       _want("out", out, T.dtype, (N, V)), _maybe("err", err, _I32, None))
-    _check(L.dspark_logit_rules(a, _queue(stream, T.get_device())))
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return logit_rules(T, row_start, tok=tok, mask=mask, hist=hist, hist_len=hist_len, prompt_len=prompt_len, rep=rep,
+                               freq=freq, pres=pres, bias_start=bias_start, bias_id=bias_id, bias_val=bias_val, allow=allow,
+                               allow_row=allow_row, out=out, err=err)
+    return (_bind or _target()).logit_rules(T, row_start, tok, mask, hist, hist_len, prompt_len, rep, freq, pres, bias_start,
+                                            bias_id, bias_val, allow, allow_row, out, err)

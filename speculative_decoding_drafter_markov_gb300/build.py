@@ -2,7 +2,9 @@
 
 Each translation unit compiles in parallel with nvcc; the objects link into
 one shared library whose exported symbols are exactly the C ABI of
-include/dspark.h.  Outputs go to speculative_decoding_drafter_markov_gb300/_build/.
+include/dspark.h.  Beside it g++ compiles the Python calls of the target-pass
+operators (bind.cpp, against the installed PyTorch's headers) into a module that
+links to the library.  Outputs go to speculative_decoding_drafter_markov_gb300/_build/.
 """
 from __future__ import annotations
 
@@ -11,12 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libdspark.so")
+BIND = os.path.join(OUT, "_dspark_bind.so")
 SOURCES = ["abi.cu", "attn.cu", "attn_tc.cu", "diag.cu", "draft.cu", "draft_tc.cu", "gemm_tc.cu", "paged.cu", "rules.cu",
            "sched.cu", "sts.cu", "train_loss.cu", "verify.cu", "verify_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -38,11 +42,37 @@ def _deps():
     return files
 
 
+def _build_bind(obj: str) -> None:
+    """Compile bind.cpp; the module is linked once the library is there."""
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in (inc, os.path.join(inc, "torch", "csrc", "api", "include"),
+                                sysconfig.get_paths()["include"], "/usr/local/cuda/include")),
+           "-c", os.path.join(CSRC, "bind.cpp"), "-o", obj]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on bind.cpp:\n{res.stderr}")
+
+
+def _link_bind(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BIND + f".{os.getpid()}.tmp"
+    cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", OUT, "-l:libdspark.so", "-Wl,-rpath,$ORIGIN",
+           "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{res.stderr}")
+    os.replace(tmp, BIND)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OUT, exist_ok=True)
-    if not force and os.path.exists(LIB):
+    if not force and os.path.exists(LIB) and os.path.exists(BIND):
         newest = max(os.path.getmtime(f) for f in _deps())
-        if os.path.getmtime(LIB) >= newest:
+        if min(os.path.getmtime(LIB), os.path.getmtime(BIND)) >= newest:
             return LIB
     nvcc = _nvcc()
 
@@ -59,13 +89,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(res.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    bind = os.path.join(OUT, "bind.o")
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        python_side = ex.submit(_build_bind, bind)
         objs = list(ex.map(compile_one, SOURCES))
+        python_side.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     res = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stderr}")
     os.replace(tmp, LIB)
+    _link_bind(bind)
     return LIB
 
 
