@@ -40,15 +40,19 @@ inline size_t smem_bytes(int D) {
 template <typename T, int kDV>  // kDV: float4 columns per lane, ceil(D / 128)
 __global__ void __launch_bounds__(kThreads) tree_attention_simt(const __grid_constant__ Params p) {
     extern __shared__ __align__(16) float sh[];
-    __shared__ long long scratch[2 + kThreads / 32];
+    __shared__ Share shared_share;
     const dspark_tree_attention_args &a = p.a;
     const int D = a.D, DP = padded(D), KS = DP + 4;
     float *sq = sh, *sk = sq + kLines * DP, *sv = sk + kTile * KS, *sp = sv + kTile * DP;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int line = tid >> 3, tx = tid & 7;  // scores: this thread's line and its tokens tx + 8 i
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Share share = share_of(p, scratch);
-    Walk walk(p, share);
+    if (warp == 0) {
+        const Share s = share_of(p);
+        if (lane == 0) shared_share = s;
+    }
+    __syncthreads();
+    Walk walk(p, shared_share);
     if (tid == 0) p.join[blockIdx.x].pieces = 0;
     Piece x;
     while (walk.next(x)) {

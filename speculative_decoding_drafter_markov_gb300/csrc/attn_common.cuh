@@ -99,8 +99,8 @@ struct Piece {
     int slot;        // partial to leave it in, or -1: the unit is whole
 };
 
-// The CTA's share of the line and the place where it starts.  Every thread of
-// the CTA calls this once; `sh` is shared scratch of 2 + threads / 32 words.
+// The CTA's share of the line and the place where it starts, found by one warp (all
+// its lanes come here and get it): a run of requests per lane, no barrier.
 struct Share {
     int lo, hi;
     int each, more;      // places of a CTA's share; the first `more` CTAs have one more
@@ -108,11 +108,11 @@ struct Share {
     int r_begin;         // its first place
 };
 
-__device__ inline Share share_of(const Params &p, long long *sh) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
-    const int R = p.a.R, per = R <= (int)blockDim.x ? 1 : (R + (int)blockDim.x - 1) / (int)blockDim.x;
-    const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
+__device__ inline Share share_of(const Params &p) {
+    const int lane = threadIdx.x & 31, R = p.a.R;
+    const int per = (R + 31) / 32, r0 = min(R, lane * per), r1 = min(R, r0 + per);
     long long mine = 0;
+#pragma unroll 4
     for (int r = r0; r < r1; ++r) mine += request_places(p, request_of(p, r, blockIdx.x == 0));
     long long inc = mine;
 #pragma unroll
@@ -120,41 +120,29 @@ __device__ inline Share share_of(const Params &p, long long *sh) {
         const long long y = __shfl_up_sync(0xffffffffu, inc, d);
         if (lane >= d) inc += y;
     }
-    if (lane == 31) sh[2 + warp] = inc;
-    __syncthreads();
-    long long before = 0, total = 0;
-    for (int w = 0; w < nwarps; ++w) {
-        const long long x = sh[2 + w];
-        if (w < warp) before += x;
-        total += x;
-    }
+    long long total = __shfl_sync(0xffffffffu, inc, 31);
     Share s{0, 0, 1, 0, 0, 0};
     if (total > 0x7fffffffll) {  // months of work: not a case to count in 64 bits for
-        if (tid == 0 && blockIdx.x == 0) set_err(p.a.err, DSPARK_ERR_UNSUPPORTED);
+        if (lane == 0 && blockIdx.x == 0) set_err(p.a.err, DSPARK_ERR_UNSUPPORTED);
         total = 0;
     }
-    const int t = (int)total, ctas = min((int)gridDim.x, t), c = blockIdx.x;
-    if (c < ctas) {
-        s.each = t / ctas;
-        s.more = t - s.each * ctas;
-        s.lo = c * s.each + min(c, s.more);
-        s.hi = s.lo + s.each + (c < s.more ? 1 : 0);
-        long long begin = before + inc - mine;
-        if (begin <= s.lo && s.lo < begin + mine) {
-            int r = r0;
-            for (; r1 - r0 > 1;) {
-                const long long n = request_places(p, request_of(p, r, false));
-                if (s.lo < begin + n) break;
-                begin += n;
-                ++r;
-            }
-            sh[0] = r;
-            sh[1] = begin;
+    const unsigned t = (unsigned)total, c = blockIdx.x, ctas = min(gridDim.x, t);
+    if (c >= ctas) return s;
+    s.each = t / ctas;
+    s.more = t - s.each * ctas;
+    s.lo = c * s.each + min((int)c, s.more);
+    s.hi = s.lo + s.each + ((int)c < s.more ? 1 : 0);
+    int begin = (int)(inc - mine), r = r0;
+    const bool here = begin <= s.lo && s.lo < begin + (int)mine;
+    if (here)
+        for (; r1 - r0 > 1; ++r) {
+            const int n = (int)request_places(p, request_of(p, r, false));
+            if (s.lo < begin + n) break;
+            begin += n;
         }
-    }
-    __syncthreads();
-    s.r = (int)sh[0];
-    s.r_begin = (int)sh[1];
+    const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    s.r = __shfl_sync(0xffffffffu, r, from);
+    s.r_begin = __shfl_sync(0xffffffffu, begin, from);
     return s;
 }
 

@@ -47,8 +47,7 @@ struct Shape {
     static constexpr int kOffRing = NQ * kSlot;
     static constexpr int kOffMl = kOffRing + NS * kSlot;    // float2 [2][128]
     static constexpr int kOffPiece = kOffMl + 2 * 128 * 8;  // Piece [kQueue], 64 bytes each
-    static constexpr int kOffScan = kOffPiece + 64 * kQueue;  // long long [2 + 12]
-    static constexpr int kOffBar = kOffScan + 8 * 14;
+    static constexpr int kOffBar = kOffPiece + 64 * kQueue;
     static constexpr int kBars = 2 * NS + 11 + 2 * kQueue;
     static constexpr int kOffBad = kOffBar + 8 * kBars;     // uint32 [3][8]
     static constexpr int kOffMisc = kOffBad + 96;           // tmem slot, abort flag
@@ -224,7 +223,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::prefetch_tmap(&tmK);
         tc::prefetch_tmap(&tmV);
     }
-    const Share share = share_of(p, reinterpret_cast<long long *>(smem + C::kOffScan));  // synchronises the CTA
+    Share share{};
+    if (warp == 11) share = share_of(p);
+    __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const Waiter wait{abort_flag, a.err};
