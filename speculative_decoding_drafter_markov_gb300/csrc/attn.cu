@@ -1,6 +1,6 @@
-// attn.cu -- attention of drafted rows over a paged cache: the CUDA-core kernel
-// (fp32, and the bf16 shapes the tensor-core kernel does not take) and the join
-// of the pieces of a unit.
+// attn.cu -- attention of drafted rows over a paged cache: the general CUDA-core
+// kernel (the shapes that neither the tensor-core kernel nor the fp32 one takes),
+// the choice among the three and the join of the pieces of a unit.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -16,7 +16,7 @@ namespace {
 // tile are staged in shared memory as fp32 and shared by the lines.  A thread
 // scores one line against four tokens, then each warp adds its four lines'
 // weighted values, the lanes side by side over D.
-constexpr int kLines = 16, kTileLog2 = 5, kTile = 1 << kTileLog2, kThreads = 128;
+constexpr int kLines = kSimtLines, kTileLog2 = 5, kTile = 1 << kTileLog2, kThreads = 128;
 
 template <typename T>
 __device__ __forceinline__ float4 load4(const T *p);
@@ -383,9 +383,15 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws,
     p.subs = (p.G + p.heads - 1) / p.heads;
     p.block_rows = kLines / p.heads;
     p.lines = p.block_rows * p.heads;
+    p.stride = a.D;
+    if (f32_supported(a)) {
+        const int grid = f32_grid(a.D);
+        carve(p, ws, grid);
+        cudaError_t e = launch_f32(p, grid, s);
+        return e == cudaSuccess ? launch_join(p, grid, s) : e;
+    }
     p.tile_log2 = kTileLog2;
     p.unit_cost = 1;
-    p.stride = a.D;
     const int es = a.dtype == DSPARK_BF16 ? 2 : 4;
     p.vec = a.D % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.k_cache) | reinterpret_cast<uintptr_t>(a.v_cache)) & (4 * es - 1)) == 0;
     const int grid = simt_grid(a.D);

@@ -232,6 +232,11 @@ void carve(Params &p, void *ws, int grid);
 bool tc_supported(const dspark_tree_attention_args &a);
 void tc_shape(const dspark_tree_attention_args &a, int *block_rows, int *lines, int *stride);
 cudaError_t launch_tc(Params p, int grid, cudaStream_t s);
+// the fp32 kernel: units of kSimtLines lines, as the general CUDA-core kernel
+constexpr int kSimtLines = 16;
+bool f32_supported(const dspark_tree_attention_args &a);
+int f32_grid(int D);
+cudaError_t launch_f32(Params p, int grid, cudaStream_t s);
 cudaError_t launch_join(const Params &p, int grid, cudaStream_t s);
 
 }  // namespace attn

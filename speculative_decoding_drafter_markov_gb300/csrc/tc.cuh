@@ -205,6 +205,10 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src, uint32_t 
                  "l"(src), "r"(src_bytes), "l"(policy)
                  : "memory");
 }
+// the same with the default L2 policy
+__device__ __forceinline__ void cp_async16_zfill(void *dst, const void *src, uint32_t src_bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(src_bytes) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // wait until at most n of this thread's committed groups are still in flight
 template <int n>
