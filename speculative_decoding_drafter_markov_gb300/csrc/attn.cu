@@ -207,93 +207,111 @@ __global__ void __launch_bounds__(kThreads) tree_attention_simt(const __grid_con
 
 // ---------------------------------------------------------------- join
 // out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over a unit's partials.
-// At most one unit starts in a CTA and ends in a later one, so CTA (c, z) joins
-// lines z, z + kJoinSplit, .. of CTA c's unit.  A warp takes a line, or, where a
-// unit has many pieces (one long cache over the whole GPU), the four warps share
-// a line's pieces.  Bound by latency: a few dependent reads of partials that are
-// still in L2, eight pieces in flight.
-constexpr int kJoinWarps = 4, kJoinSplit = 8, kJoinMany = 8;
+// At most one unit starts in a CTA and ends in a later one, so CTAs (c, ..) join the
+// lines of CTA c's unit: a warp a line, or, where a unit has many pieces (one long
+// cache over the whole GPU), the four warps of a CTA share a line's pieces.  Bound by
+// latency: partials that are still in L2, eight under way before the weights are known.
+constexpr int kJoinWarps = 4, kJoinMany = 8, kAhead = 8;
 
-template <bool kFour>  // D a multiple of 4: four columns per lane and load
+// four (or, E = 1, one) adjacent floats per lane
+template <int E>
+struct Cells {
+    float v[E];
+    __device__ __forceinline__ void load(const float *p) {
+        if (E == 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(p);
+            v[0] = q.x, v[E > 1 ? 1 : 0] = q.y, v[E > 2 ? 2 : 0] = q.z, v[E > 3 ? 3 : 0] = q.w;
+        } else {
+            v[0] = *p;
+        }
+    }
+};
+
+// kCols: groups of 32 E columns that a line has
+template <int E, int kCols>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_attention_join(const __grid_constant__ Params p) {
-    constexpr int E = kFour ? 4 : 1, kMaxCols = 256 / (32 * E);
-    __shared__ float sum_o[kJoinWarps - 1][256];
+    __shared__ float sum_o[kJoinWarps - 1][32 * E * kCols];
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are written
     const Join n = p.join[blockIdx.x];
     if (n.pieces == 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.stride;
     const bool many = n.pieces > kJoinMany;
-    const int cols = (D + 32 * E - 1) / (32 * E);
     // partial i: the first one, then the first partials of the CTAs after it
     auto slot = [&](int i, int ln) { return (size_t)(i == 0 ? n.first : 2 * ((int)blockIdx.x + i)) * p.lines + ln; };
-    const int stride = many ? kJoinSplit : kJoinSplit * kJoinWarps;
-    const int unit_heads = p.heads;
-    for (int ln = many ? blockIdx.y : blockIdx.y * kJoinWarps + warp; ln < n.lines; ln += stride) {
-        const int jj = ln / unit_heads, g = ln % unit_heads;
+    const int step = many ? kJoinWarps : 1;  // pieces of this warp: own, own + step, ..
+    const int own = many ? warp : 0;
+    for (int ln = many ? blockIdx.y : blockIdx.y * kJoinWarps + warp; ln < n.lines; ln += many ? gridDim.y : gridDim.y * kJoinWarps) {
+        const int jj = ln / p.heads, g = ln - jj * p.heads;
         if (g >= n.heads) continue;
-        // weights of pieces lane, lane + 32, ..: every warp has them all
-        float M = -INFINITY;
-        for (int i = lane; i < n.pieces; i += 32) M = fmaxf(M, p.part_ml[slot(i, ln)].x);
+        float2 ml = lane < n.pieces ? p.part_ml[slot(lane, ln)] : make_float2(-INFINITY, 0.f);
+        Cells<E> next[kAhead][kCols];
+        auto fetch = [&](int i0) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int i = i0 + u * step;
+                const float *from = p.part_o + slot(i, ln) * D;
+#pragma unroll
+                for (int c = 0; c < kCols; ++c)
+                    if (i < n.pieces && E * (lane + 32 * c) < D) next[u][c].load(from + E * (lane + 32 * c));
+            }
+        };
+        fetch(own);
+        float M = ml.x;
+        for (int i = 32 + lane; i < n.pieces; i += 32) M = fmaxf(M, p.part_ml[slot(i, ln)].x);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
         const float ref = M == -INFINITY ? 0.f : M;
-        float o[kMaxCols][E], L = 0.f;
-#pragma unroll
-        for (int c = 0; c < kMaxCols; ++c)
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[c][e] = 0.f;
-        for (int i0 = 0; i0 < n.pieces; i0 += 32) {
-            float w = 0.f;
-            if (i0 + lane < n.pieces) {
-                const float2 ml = p.part_ml[slot(i0 + lane, ln)];
-                w = ex2(ml.x - ref);
-                L = fmaf(w, ml.y, L);
-            }
-            const int end = min(32, n.pieces - i0);
-#pragma unroll 8
-            for (int i = many ? warp : 0; i < end; i += many ? kJoinWarps : 1) {
-                const float wi = __shfl_sync(0xffffffffu, w, i);
-                const float *from = p.part_o + slot(i0 + i, ln) * D;
-#pragma unroll
-                for (int c = 0; c < kMaxCols; ++c) {
-                    const int d = E * (lane + 32 * c);
-                    if (c >= cols || d >= D) break;
-                    if (kFour) {
-                        const float4 v = *reinterpret_cast<const float4 *>(from + d);
-                        o[c][0] = fmaf(wi, v.x, o[c][0]);
-                        o[c][E > 1 ? 1 : 0] = fmaf(wi, v.y, o[c][E > 1 ? 1 : 0]);
-                        o[c][E > 2 ? 2 : 0] = fmaf(wi, v.z, o[c][E > 2 ? 2 : 0]);
-                        o[c][E > 3 ? 3 : 0] = fmaf(wi, v.w, o[c][E > 3 ? 3 : 0]);
-                    } else {
-                        o[c][0] = fmaf(wi, from[d], o[c][0]);
-                    }
-                }
-            }
+        float o[kCols][E], w = ex2(ml.x - ref), L = w * ml.y;
+        for (int i = 32 + lane; i < n.pieces; i += 32) {
+            const float2 x = p.part_ml[slot(i, ln)];
+            L = fmaf(ex2(x.x - ref), x.y, L);
         }
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[c][e] = 0.f;
+        int chunk = 0;  // w is the weight of piece chunk + lane
+        for (int i0 = own; i0 < n.pieces; i0 += kAhead * step) {
+            if (i0 != own) fetch(i0);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int i = i0 + u * step;
+                if (i >= n.pieces) break;
+                if (i >= chunk + 32) {
+                    chunk = i & ~31;
+                    w = chunk + lane < n.pieces ? ex2(p.part_ml[slot(chunk + lane, ln)].x - ref) : 0.f;
+                }
+                const float wi = __shfl_sync(0xffffffffu, w, i - chunk);
+#pragma unroll
+                for (int c = 0; c < kCols; ++c)
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if (E * (lane + 32 * c) < D) o[c][e] = fmaf(wi, next[u][c].v[e], o[c][e]);
+            }
+        }
         if (many) {
             __syncthreads();
             if (warp > 0) {
 #pragma unroll
-                for (int c = 0; c < kMaxCols; ++c)
+                for (int c = 0; c < kCols; ++c)
 #pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        if (E * (lane + 32 * c) + e < D) sum_o[warp - 1][E * (lane + 32 * c) + e] = o[c][e];
+                    for (int e = 0; e < E; ++e) sum_o[warp - 1][E * (lane + 32 * c) + e] = o[c][e];
             }
             __syncthreads();
             if (warp > 0) continue;
 #pragma unroll
-            for (int c = 0; c < kMaxCols; ++c)
+            for (int c = 0; c < kCols; ++c)
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    if (E * (lane + 32 * c) + e < D)
-                        for (int x = 0; x < kJoinWarps - 1; ++x) o[c][e] += sum_o[x][E * (lane + 32 * c) + e];
+#pragma unroll
+                    for (int x = 0; x < kJoinWarps - 1; ++x) o[c][e] += sum_o[x][E * (lane + 32 * c) + e];
         }
         const size_t at = (size_t)(n.row + jj) * p.a.Hq + n.head + g;
         const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-        for (int c = 0; c < kMaxCols; ++c)
+        for (int c = 0; c < kCols; ++c)
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const int place = E * (lane + 32 * c) + e, d = p.mixed ? plain_column(place) : place;
@@ -337,18 +355,22 @@ void carve(Params &p, void *ws, int grid) {
 }
 
 cudaError_t launch_join(const Params &p, int grid, cudaStream_t s) {
-    // its CTAs come up while the first launch runs, and wait there for its end
+    // a CTA for every line of a unit, as far as the host knows them; its CTAs come up
+    // while the first launch runs, and wait there for its end
+    const long long lines = (long long)p.a.max_rows * p.heads;
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid, kJoinSplit);
+    cfg.gridDim = dim3(grid, (unsigned)(lines < 1 ? 1 : lines < p.lines ? lines : p.lines));
+    if (cfg.gridDim.y > 32) cfg.gridDim.y = 32;
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = s;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    return p.stride % 4 == 0 ? cudaLaunchKernelEx(&cfg, tree_attention_join<true>, p)
-                          : cudaLaunchKernelEx(&cfg, tree_attention_join<false>, p);
+    if (p.stride % 4 == 0)
+        return p.stride <= 128 ? cudaLaunchKernelEx(&cfg, tree_attention_join<4, 1>, p) : cudaLaunchKernelEx(&cfg, tree_attention_join<4, 2>, p);
+    return p.stride <= 64 ? cudaLaunchKernelEx(&cfg, tree_attention_join<1, 2>, p) : cudaLaunchKernelEx(&cfg, tree_attention_join<1, 8>, p);
 }
 
 }  // namespace attn
@@ -385,7 +407,7 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws,
     p.lines = p.block_rows * p.heads;
     p.stride = a.D;
     if (f32_supported(a)) {
-        const int grid = f32_grid(a.D);
+        const int grid = f32_grid();
         carve(p, ws, grid);
         cudaError_t e = launch_f32(p, grid, s);
         return e == cudaSuccess ? launch_join(p, grid, s) : e;

@@ -235,7 +235,7 @@ cudaError_t launch_tc(Params p, int grid, cudaStream_t s);
 // the fp32 kernel: units of kSimtLines lines, as the general CUDA-core kernel
 constexpr int kSimtLines = 16;
 bool f32_supported(const dspark_tree_attention_args &a);
-int f32_grid(int D);
+int f32_grid();
 cudaError_t launch_f32(Params p, int grid, cudaStream_t s);
 cudaError_t launch_join(const Params &p, int grid, cudaStream_t s);
 
