@@ -506,17 +506,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             ref = m == -INFINITY ? 0.f : m;
                         }
-                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                        // two weights at a time: arguments and sums in pairs
+                        float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+                        const float2 by = {scale, scale}, off = {-ref, -ref};
                         uint32_t r[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const float p0 = ex2(fmaf(s[2 * i], scale, -ref));
-                            const float p1 = ex2(fmaf(s[2 * i + 1], scale, -ref));
-                            sum[i & 3] += p0 + p1;
-                            r[i] = pack(p0, p1);
+                            const float2 arg = fma2({s[2 * i], s[2 * i + 1]}, by, off);
+                            const float2 e = {ex2(arg.x), ex2(arg.y)};
+                            sum[i & 1] = add2(sum[i & 1], e);
+                            r[i] = pack(e.x, e.y);
                         }
                         tc::tmem_st32(s_tmem + 32 * half, r);
-                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        sum[0] = add2(sum[0], sum[1]);
+                        l += sum[0].x + sum[0].y;
                         tc::tmem_wait_st();
                         tc::tc_fence_before();
                     } else if (pass == 0) {
