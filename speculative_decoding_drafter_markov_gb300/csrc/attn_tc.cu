@@ -406,8 +406,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int tl = dual ? u : 2 * u + w;
                 const int tok0 = (x.t0 + tl) * kTile;
                 const bool tail = tok0 + kTile > x.len + base_rel;
+                ok = wait.warp(&s_full[w], count & 1u);
+                if (!ok) break;
+                tc::tc_fence_after();
                 if (tail && (!dual || w == 0)) {
-                    // Values that some lines do not see must not reach them as 0 x inf:
+                    // (S of the tile is there, so the copies into this slot before its values
+                    // are too.)  Values that some lines do not see must not reach them as 0 x inf:
                     // slots beyond the tokens are zeroed, infinities and NaN of the
                     // cycle's rows too, and those added back below where they are seen.
                     const uint32_t pos = base + value_place(tl, n, dual);
@@ -449,9 +453,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::fence_proxy_async_smem();
                     }
                 }
-                ok = wait.warp(&s_full[w], count & 1u);
-                if (!ok) break;
-                tc::tc_fence_after();
                 // Three passes of one code: the maximum of the second half, that of the
                 // first and its weights, the weights of the second.  The weights need the
                 // maximum of both, and a half read again from tensor memory costs less
