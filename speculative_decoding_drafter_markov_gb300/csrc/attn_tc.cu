@@ -9,9 +9,9 @@
 // Two streams, each with its own S and O and four softmax warps, run side by side:
 // with two operands a stream per operand, both over every tile; with one, the
 // streams take the even and the odd tiles and are added at the end like two
-// partials.  The softmax hands P over in halves, so that the first half's product
-// runs while the second half is formed.  The maximum m is only moved, and O
-// rescaled in tensor memory, when a tile exceeds it by 2^8 (any reference gives
+// partials.  The softmax works and hands P over in halves, so that the first half's
+// product runs while the second half is formed.  The maximum m is only moved, and O
+// rescaled in tensor memory, when a half exceeds it by 2^8 (any reference gives
 // the same result; P stays below 2^8 and the fp32 sums far from overflow).
 //
 // Warps 0-7 softmax, 8 and 10 copy keys and values by TMA, a box per page piece,
@@ -32,7 +32,7 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 384, kTileLog2 = 7, kTile = 1 << kTileLog2;
-constexpr float kSlack = 8.f;  // log2 by which a tile may exceed the reference
+constexpr float kSlack = 8.f;  // log2 by which half a tile may exceed the reference
 constexpr int kQueue = 4;      // pieces handed out ahead
 constexpr int kUnitCost = 2;   // tiles' worth of a unit's start and end
 
@@ -48,7 +48,7 @@ struct Shape {
     static constexpr int kOffMl = kOffRing + NS * kSlot;    // float2 [2][128]
     static constexpr int kOffPiece = kOffMl + 2 * 128 * 8;  // Piece [kQueue], 64 bytes each
     static constexpr int kOffBar = kOffPiece + 64 * kQueue;
-    static constexpr int kBars = 2 * NS + 11 + 2 * kQueue;
+    static constexpr int kBars = 2 * NS + 13 + 2 * kQueue;
     static constexpr int kOffBad = kOffBar + 8 * kBars;     // uint32 [3][8]
     static constexpr int kOffMisc = kOffBad + 96;           // tmem slot, abort flag
     static constexpr int kSmem = kOffMisc + 8;
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const dspark_tree_attention_args &a = p.a;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kOffBar), *empty = full + C::NS;
     uint64_t *s_full = empty + C::NS, *p_ready = s_full + 2;  // [stream]; [stream][half]
-    uint64_t *q_full = p_ready + 4, *o_free = q_full + 1, *both = o_free + 1,
+    uint64_t *half_done = p_ready + 4, *q_full = half_done + 2, *o_free = q_full + 1, *both = o_free + 1,
              *drain = both + 1, *o_last = drain + 1;
     uint64_t *queue_full = o_last + 1, *queue_empty = queue_full + kQueue;
     Piece *pieces = reinterpret_cast<Piece *>(smem + C::kOffPiece);
@@ -203,6 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::mbar_init(&s_full[0], 1);
         tc::mbar_init(&s_full[1], 1);
+        tc::mbar_init(&half_done[0], 1);
+        tc::mbar_init(&half_done[1], 1);
         for (int i = 0; i < 4; ++i) tc::mbar_init(&p_ready[i], 4);
         tc::mbar_init(q_full, 1);
         tc::mbar_init(o_free, 8);
@@ -351,8 +353,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t bl = v_lo + vslot * (C::kSlot >> 4);
 #pragma unroll
                         for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                            tc::umma_bf16_ta_lo(tmem + 256 + 128 * w, tmem + 128 * w + 8 * kk, bl + ((kk * 2048) >> 4), idesc_o,
+                            tc::umma_bf16_ta_lo(tmem + 256 + 128 * w, tmem + 128 * w + 64 * half + 8 * (kk & 3), bl + ((kk * 2048) >> 4), idesc_o,
                                                 i >= 2 || kk > 0 ? 1u : 0u);
+                        if (half == 0) tc::umma_commit(&half_done[w]);
                     }
                     p_phase[w] ^= 1u;
                     if (!dual || w == 1) tc::umma_commit(&empty[vslot]);
@@ -453,18 +456,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::fence_proxy_async_smem();
                     }
                 }
-                // Three passes of one code: the maximum of the second half, that of the
-                // first and its weights, the weights of the second.  The weights need the
-                // maximum of both, and a half read again from tensor memory costs less
-                // than 64 registers.
-                float ref = 0.f, top = -INFINITY;
 #pragma unroll 1
-                for (int pass = 0; pass < 3; ++pass) {
-                    const int half = pass == 1 ? 0 : 1;
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t s_half = s_tmem + 64 * half;
                     if (active) {
                         float s[64];
-                        tc::tmem_ld32(s_tmem + 64 * half, s);
-                        tc::tmem_ld32(s_tmem + 64 * half + 32, s + 32);
+                        tc::tmem_ld32(s_half, s);
+                        tc::tmem_ld32(s_half + 32, s + 32);
                         tc::tmem_wait_ld();
                         if (tail) {
 #pragma unroll
@@ -475,38 +473,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int i = 0; i < 32; ++i) s[32 * c + i] = see & (1u << i) ? s[32 * c + i] : -INFINITY;
                             }
                         }
-                        if (pass < 2) {
-                            float mx[4] = {top, -INFINITY, -INFINITY, -INFINITY};
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                            for (int i = 0; i < 64; i += 4)
+                        for (int i = 0; i < 64; i += 4)
 #pragma unroll
-                                for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], s[i + c]);
-                            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                            if (pass == 0) continue;
-                            top *= scale;
-                            if (u == 0) {
-                                m = top;
-                            } else if (__any_sync(0xffffffffu, top > m + kSlack)) {
-                                const float to = top > m + kSlack ? top : m;
-                                const float f = to == -INFINITY ? 1.f : ex2(m - to);
-                                m = to;
-                                l *= f;
-                                // the product before has been added when its values' slot is free
-                                const uint32_t pos = base + value_place(dual ? tl - 1 : tl - 2, n, dual);
-                                ok = wait.warp(&empty[pos % C::NS], (pos / C::NS) & 1u);
-                                tc::tc_fence_after();
+                            for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], s[i + c]);
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+                        if (u == 0 && half == 0) {
+                            m = top;
+                        } else if (__any_sync(0xffffffffu, top > m + kSlack)) {
+                            const float to = top > m + kSlack ? top : m;
+                            const float f = to == -INFINITY ? 1.f : ex2(m - to);
+                            m = to;
+                            l *= f;
+                            // the products so far are in O: those of the tile before were
+                            // issued before this tile's S, that of the first half says so
+                            if (half == 1) ok = wait.warp(&half_done[w], count & 1u);
+                            tc::tc_fence_after();
 #pragma unroll 1
-                                for (int c = 0; c < C::DP; c += 16) {
-                                    uint32_t o[16];
-                                    tc::tmem_ld16(o_tmem + c, o);
-                                    tc::tmem_wait_ld();
+                            for (int c = 0; c < C::DP; c += 16) {
+                                uint32_t o[16];
+                                tc::tmem_ld16(o_tmem + c, o);
+                                tc::tmem_wait_ld();
 #pragma unroll
-                                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                    tc::tmem_st16(o_tmem + c, o);
-                                }
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tc::tmem_st16(o_tmem + c, o);
                             }
-                            ref = m == -INFINITY ? 0.f : m;
                         }
+                        const float ref = m == -INFINITY ? 0.f : m;
                         // two weights at a time: arguments and sums in pairs
                         float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
                         const float2 by = {scale, scale}, off = {-ref, -ref};
@@ -518,17 +512,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             sum[i & 1] = add2(sum[i & 1], e);
                             r[i] = pack(e.x, e.y);
                         }
-                        tc::tmem_st32(s_tmem + 32 * half, r);
+                        tc::tmem_st32(s_half, r);
                         sum[0] = add2(sum[0], sum[1]);
                         l += sum[0].x + sum[0].y;
                         tc::tmem_wait_st();
                         tc::tc_fence_before();
-                    } else if (pass == 0) {
-                        continue;
                     }
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&p_ready[2 * w + half]);
                 }
+                if (!ok) break;
             }
             if (!ok) break;
 
