@@ -210,8 +210,9 @@ __global__ void __launch_bounds__(kThreads) tree_attention_simt(const __grid_con
 // At most one unit starts in a CTA and ends in a later one, so CTAs (c, ..) join the
 // lines of CTA c's unit: a warp a line, or, where a unit has many pieces (one long
 // cache over the whole GPU), the four warps of a CTA share a line's pieces.  Bound by
-// latency: partials that are still in L2, eight under way before the weights are known.
-constexpr int kJoinWarps = 4, kJoinMany = 8, kAhead = 8;
+// latency: partials that are still in L2, four under way before the weights are known
+// (eight take the registers of half of the CTAs: 2 us more for 256 lines).
+constexpr int kJoinWarps = 4, kJoinMany = 8, kAhead = 4;
 
 // four (or, E = 1, one) adjacent floats per lane
 template <int E>
@@ -229,7 +230,7 @@ struct Cells {
 
 // kCols: groups of 32 E columns that a line has
 template <int E, int kCols>
-__global__ void __launch_bounds__(32 * kJoinWarps) tree_attention_join(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(32 * kJoinWarps, 8) tree_attention_join(const __grid_constant__ Params p) {
     __shared__ float sum_o[kJoinWarps - 1][32 * E * kCols];
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are written
     const Join n = p.join[blockIdx.x];
@@ -363,7 +364,7 @@ cudaError_t launch_join(const Params &p, int grid, cudaStream_t s) {
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid, (unsigned)(lines < 1 ? 1 : lines < p.lines ? lines : p.lines));
-    if (cfg.gridDim.y > 32) cfg.gridDim.y = 32;
+    if (cfg.gridDim.y > 16) cfg.gridDim.y = 16;
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = s;
     cfg.attrs = &early;

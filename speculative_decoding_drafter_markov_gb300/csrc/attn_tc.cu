@@ -34,7 +34,7 @@ namespace {
 constexpr int kThreads = 384, kTileLog2 = 7, kTile = 1 << kTileLog2;
 constexpr float kSlack = 8.f;  // log2 by which half a tile may exceed the reference
 constexpr int kQueue = 4;      // pieces handed out ahead
-constexpr int kUnitCost = 2;   // tiles' worth of a unit's start and end
+constexpr int kUnitCost = 3;   // tiles' worth of a unit's start and end
 
 // DP: D padded to the copied width, NQ: operands a unit may have
 template <int DP_, int NQ_>

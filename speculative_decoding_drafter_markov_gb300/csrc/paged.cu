@@ -41,11 +41,20 @@ __device__ __forceinline__ int holder(const int *sum, int R, int k) {
     return lo;
 }
 
-__device__ __forceinline__ long long need_of(const dspark_page_map_args &a, int r) {
-    return ((long long)a.len[r] + a.rows[r] + a.page - 1) / a.page;
+// division by the page: a shift where it is a power of two
+struct Page {
+    unsigned size;
+    int shift;  // or -1
+    __device__ __forceinline__ unsigned of(unsigned t) const { return shift >= 0 ? t >> shift : t / size; }
+};
+
+// pages of a request; the sum of two non-negative 32-bit sizes fits 32 bits unsigned
+__device__ __forceinline__ unsigned need_of(const dspark_page_map_args &a, const Page &page, int r) {
+    const unsigned t = (unsigned)a.len[r] + (unsigned)a.rows[r], q = page.of(t);
+    return q + (t != q * page.size);
 }
 
-__global__ void __launch_bounds__(kMapThreads) page_map_kernel(const dspark_page_map_args a) {
+__global__ void __launch_bounds__(kMapThreads) page_map_kernel(const dspark_page_map_args a, const Page page) {
     extern __shared__ int sh[];
     const int R = a.R;
     const MapSums s{sh, sh + (R + 1), sh + 2 * (R + 1)};
@@ -60,7 +69,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const dspark_page
     long long v[3] = {0, 0, 0};
     bool bad = false;
     for (int r = r0; r < r1; ++r) {
-        const long long need = need_of(a, r);
+        const long long need = need_of(a, page, r);
         const int held = a.held[r];
         if (a.len[r] < 0 || a.rows[r] < 0 || held < 0 || held > a.max_pages || need > a.max_pages ||
             (a.mask && a.rows[r] > 64 * a.W))
@@ -99,7 +108,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const dspark_page
         s.rows[r] = (int)base[0];
         s.less[r] = (int)base[1];
         s.more[r] = (int)base[2];
-        const long long need = need_of(a, r);
+        const long long need = need_of(a, page, r);
         const int held = a.held[r];
         base[0] += a.rows[r];
         if (held > need) base[1] += held - need;
@@ -135,7 +144,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const dspark_page
     const int m = (int)total[1], taken = (int)total[2], after = before + m;
     auto given = [&](int k) {  // the k-th page given back
         const int r = holder(s.less, R, k);
-        return a.table[(size_t)r * a.max_pages + need_of(a, r) + (k - s.less[r])];
+        return a.table[(size_t)r * a.max_pages + need_of(a, page, r) + (k - s.less[r])];
     };
     auto page_of = [&](int k) {  // the k-th page taken
         return k < m ? given(k) : a.free_list[before - 1 - (k - m)];
@@ -144,7 +153,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const dspark_page
     if (first == 0) *a.n_free_out = after - taken;
     for (int r = first; r <= R; r += step) {
         a.row_start[r] = s.rows[r];
-        if (r < R) a.held_out[r] = (int)need_of(a, r);
+        if (r < R) a.held_out[r] = (int)need_of(a, page, r);
     }
     for (int k = first; k < m; k += step) a.free_list[after - 1 - k] = given(k);
     for (int k = first; k < taken; k += step) {
@@ -155,9 +164,9 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const dspark_page
         int slot = -1, pos = 0;
         if (i < s.rows[R]) {
             const int r = holder(s.rows, R, i), start = s.rows[r], j = i - start;
-            const int t = a.len[r] + j, pi = t / a.page, held = a.held[r];
+            const int t = a.len[r] + j, pi = (int)page.of(t), held = a.held[r];
             const int pg = pi < held ? a.table[(size_t)r * a.max_pages + pi] : page_of(s.more[r] + pi - held);
-            slot = pg * a.page + t % a.page;
+            slot = pg * a.page + (t - pi * a.page);
             pos = t;
             if (a.parents) {
                 // walk up: a parent is an earlier row, so the walk ends
@@ -193,39 +202,57 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const dspark_page
 }
 
 // ---------------------------------------------------------------- cache write
-// A copy of 2 N H D elements: bound by HBM (read once, written once).  A CTA
-// takes kStoreRows rows, its threads the 16-byte pieces of their keys and
-// values in order, so that reads and writes of a head are both adjacent.
+// A copy of 2 N H D elements: bound by HBM (read once, written once).  A thread has
+// one 16-byte piece of a row -- keys or values, head and columns are found once --
+// and takes it from kRows rows, all reads under way together; neighbouring threads
+// have neighbouring pieces.
 constexpr int kStoreThreads = 256;
-constexpr int kStoreRows = 4;
 
-template <typename Vec>
-__global__ void __launch_bounds__(kStoreThreads) cache_store_kernel(const dspark_cache_store_args a, int es) {
+template <typename Vec, int kRows>
+__global__ void __launch_bounds__(kStoreThreads) cache_store_kernel(const dspark_cache_store_args a, const Page page, int es) {
     const int vpe = (int)sizeof(Vec) / es;  // elements of a piece
     const int per_head = a.D / vpe, per_row = a.H * per_head;
-    const int row0 = blockIdx.x * kStoreRows;
-    const int rows = min(kStoreRows, a.N - row0);
-    const long long limit = (long long)a.n_pages * a.page;
-    for (int idx = threadIdx.x; idx < rows * 2 * per_row; idx += kStoreThreads) {
-        const int row = row0 + idx / (2 * per_row);
-        int rest = idx % (2 * per_row);
-        const bool is_v = rest >= per_row;
-        if (is_v) rest -= per_row;
-        const int h = rest / per_head, e = (rest % per_head) * vpe;
-        const int slot = a.slot[row];
-        if (slot < 0) continue;
-        if (slot >= limit) {
+    int piece = blockIdx.y * kStoreThreads + threadIdx.x;
+    if (piece >= 2 * per_row) return;
+    const bool values = piece >= per_row;
+    if (values) piece -= per_row;
+    const int h = piece / per_head, e = (piece - h * per_head) * vpe;
+    const char *src = static_cast<const char *>(values ? a.v : a.k) + (h * (values ? a.v_head : a.k_head) + e) * es;
+    char *dst = static_cast<char *>(values ? a.v_cache : a.k_cache) + e * es;
+    const long long row_bytes = (values ? a.v_row : a.k_row) * es;
+    const unsigned limit = (unsigned)min((long long)a.n_pages * a.page, 0x80000000ll);
+    const int row0 = blockIdx.x * kRows;
+    int slot[kRows];
+    Vec v[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) slot[i] = row0 + i < a.N ? a.slot[row0 + i] : -1;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        if (slot[i] >= 0 && (unsigned)slot[i] >= limit) {
             set_err(a.err, DSPARK_ERR_RANGE);
-            continue;
+            slot[i] = -1;
         }
-        const long long from = is_v ? row * a.v_row + h * a.v_head + e : row * a.k_row + h * a.k_head + e;
-        const int pg = slot / a.page, off = slot % a.page;
-        const long long to = (((long long)pg * a.H + h) * a.page + off) * a.D + e;
-        const char *src = static_cast<const char *>(is_v ? a.v : a.k) + from * es;
-        char *dst = static_cast<char *>(is_v ? a.v_cache : a.k_cache) + to * es;
-        *reinterpret_cast<Vec *>(dst) = __ldcs(reinterpret_cast<const Vec *>(src));
+        if (slot[i] >= 0) v[i] = __ldcs(reinterpret_cast<const Vec *>(src + (row0 + i) * row_bytes));
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        if (slot[i] < 0) continue;
+        const int pg = (int)page.of(slot[i]), off = slot[i] - pg * a.page;
+        *reinterpret_cast<Vec *>(dst + (((long long)pg * a.H + h) * a.page + off) * a.D * es) = v[i];
     }
 }
+
+template <typename Vec>
+cudaError_t store_as(const dspark_cache_store_args &a, const Page &page, int es, cudaStream_t s) {
+    const int pieces = 2 * a.H * (a.D / ((int)sizeof(Vec) / es)), y = (pieces + kStoreThreads - 1) / kStoreThreads;
+    // eight rows a thread where that leaves every SM a few CTAs, else one
+    const bool many = (long long)a.N * y >= 8ll * 4 * sm_count();
+    if (many) cache_store_kernel<Vec, 8><<<dim3((a.N + 7) / 8, y), kStoreThreads, 0, s>>>(a, page, es);
+    else cache_store_kernel<Vec, 1><<<dim3(a.N, y), kStoreThreads, 0, s>>>(a, page, es);
+    return cudaGetLastError();
+}
+
+Page page_of_size(int size) { return Page{(unsigned)size, (size & (size - 1)) == 0 ? __builtin_ctz((unsigned)size) : -1}; }
 
 }  // namespace
 
@@ -238,7 +265,7 @@ cudaError_t launch_page_map(const dspark_page_map_args &a, cudaStream_t s) {
     const int items = a.N > a.R + 1 ? a.N : a.R + 1;
     int blocks = (items + kMapThreads - 1) / kMapThreads;
     if (blocks > sm_count()) blocks = sm_count();
-    page_map_kernel<<<blocks, kMapThreads, smem, s>>>(a);
+    page_map_kernel<<<blocks, kMapThreads, smem, s>>>(a, page_of_size(a.page));
     return cudaGetLastError();
 }
 
@@ -247,11 +274,9 @@ cudaError_t launch_cache_store(const dspark_cache_store_args &a, cudaStream_t s)
     const uintptr_t all = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
                           reinterpret_cast<uintptr_t>(a.k_cache) | reinterpret_cast<uintptr_t>(a.v_cache) |
                           (uintptr_t)((a.k_row | a.k_head | a.v_row | a.v_head | a.D) * es);
-    const int blocks = (a.N + kStoreRows - 1) / kStoreRows;
-    if ((all & 15) == 0) cache_store_kernel<uint4><<<blocks, kStoreThreads, 0, s>>>(a, es);
-    else if (es == 4) cache_store_kernel<unsigned int><<<blocks, kStoreThreads, 0, s>>>(a, es);
-    else cache_store_kernel<unsigned short><<<blocks, kStoreThreads, 0, s>>>(a, es);
-    return cudaGetLastError();
+    const Page page = page_of_size(a.page);
+    if ((all & 15) == 0) return store_as<uint4>(a, page, es, s);
+    return es == 4 ? store_as<unsigned int>(a, page, es, s) : store_as<unsigned short>(a, page, es, s);
 }
 
 }  // namespace dspark
