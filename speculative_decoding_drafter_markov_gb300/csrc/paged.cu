@@ -24,7 +24,7 @@ namespace {
 //   nobody reads them (a row's slot takes its page by the same rule);
 // * held and n_free are not written (their new values go elsewhere).
 // Bound by latency: at R = 4 one CTA's chain of a load, a scan and a store.
-constexpr int kMapThreads = 512;
+constexpr int kMapThreads = 256;
 
 struct MapSums {
     int *rows, *less, *more;  // [R + 1] each, exclusive
@@ -58,62 +58,63 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const dspark_page
     extern __shared__ int sh[];
     const int R = a.R;
     const MapSums s{sh, sh + (R + 1), sh + 2 * (R + 1)};
-    __shared__ long long wsum[3][kMapThreads / 32];
+    __shared__ unsigned wsum[2][3][kMapThreads / 32];
     __shared__ int bad_any;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) bad_any = 0;
+    const int before = *a.n_free;
 
-    // a run of consecutive requests per thread, then a scan over the threads
-    const int per = (R + kMapThreads - 1) / kMapThreads;
-    const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
-    long long v[3] = {0, 0, 0};
+    // running sums, a request per thread at a time; sums beyond 2^31 - 1, of which no
+    // call is good, stay there
+    auto add = [](unsigned x, unsigned y) { return min(x + y, 0x7fffffffu); };
+    unsigned total[3] = {0, 0, 0};
     bool bad = false;
-    for (int r = r0; r < r1; ++r) {
-        const long long need = need_of(a, page, r);
-        const int held = a.held[r];
-        if (a.len[r] < 0 || a.rows[r] < 0 || held < 0 || held > a.max_pages || need > a.max_pages ||
-            (a.mask && a.rows[r] > 64 * a.W))
-            bad = true;
-        v[0] += a.rows[r];
-        if (held > need) v[1] += held - need;
-        else v[2] += need - held;
-    }
-    long long inc[3];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        long long x = v[i];
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, x, d);
-            if (lane >= d) x += y;
-        }
-        inc[i] = x;
-        if (lane == 31) wsum[i][warp] = x;
-    }
     __syncthreads();
-    if (bad) bad_any = 1;
-    long long base[3], total[3];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        long long b = 0, t = 0;
-        for (int w = 0; w < kMapThreads / 32; ++w) {
-            const long long x = wsum[i][w];
-            if (w < warp) b += x;
-            t += x;
+    for (int r0 = 0, turn = 0; r0 < R; r0 += kMapThreads, turn ^= 1) {
+        const int r = r0 + tid;
+        unsigned v[3] = {0, 0, 0};
+        if (r < R) {
+            const int len = a.len[r], rows = a.rows[r], held = a.held[r];
+            const unsigned need = need_of(a, page, r);
+            if (len < 0 || rows < 0 || held < 0 || held > a.max_pages || need > (unsigned)a.max_pages || (a.mask && rows > 64 * a.W)) {
+                bad = true;
+            } else {
+                v[0] = rows;
+                v[1] = max(0, held - (int)need);
+                v[2] = max(0, (int)need - held);
+            }
         }
-        base[i] = b + inc[i] - v[i];
-        total[i] = t;
+        unsigned inc[3] = {v[0], v[1], v[2]};
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                const unsigned y = __shfl_up_sync(0xffffffffu, inc[i], d);
+                if (lane >= d) inc[i] = add(inc[i], y);
+            }
+        if (lane == 31)
+#pragma unroll
+            for (int i = 0; i < 3; ++i) wsum[turn][i][warp] = inc[i];
+        __syncthreads();
+        unsigned base[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            unsigned b = total[i];
+#pragma unroll
+            for (int w = 0; w < kMapThreads / 32; ++w) {
+                const unsigned x = wsum[turn][i][w];
+                if (w < warp) b = add(b, x);
+                total[i] = add(total[i], x);
+            }
+            base[i] = b + inc[i] - v[i];
+        }
+        if (r < R) {
+            s.rows[r] = (int)base[0];
+            s.less[r] = (int)base[1];
+            s.more[r] = (int)base[2];
+        }
     }
-    for (int r = r0; r < r1; ++r) {
-        s.rows[r] = (int)base[0];
-        s.less[r] = (int)base[1];
-        s.more[r] = (int)base[2];
-        const long long need = need_of(a, page, r);
-        const int held = a.held[r];
-        base[0] += a.rows[r];
-        if (held > need) base[1] += held - need;
-        else base[2] += need - held;
-    }
+    if (bad) bad_any = 1;
     if (tid == 0) {
         s.rows[R] = (int)total[0];
         s.less[R] = (int)total[1];
@@ -121,9 +122,8 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const dspark_page
     }
     __syncthreads();
 
-    const int before = *a.n_free;
-    const bool fail = bad_any || total[0] > a.N || (a.parents && total[0] > a.n_parents) || before < 0 ||
-                      before + total[1] > a.n_pages || total[2] > before + total[1];
+    const bool fail = bad_any || total[0] > (unsigned)a.N || (a.parents && total[0] > (unsigned)a.n_parents) || before < 0 ||
+                      (unsigned)before + total[1] > (unsigned)a.n_pages || total[2] > (unsigned)before + total[1];
     const int first = blockIdx.x * kMapThreads + tid, step = gridDim.x * kMapThreads;
     if (fail) {
         if (first == 0) {
@@ -264,7 +264,7 @@ cudaError_t launch_page_map(const dspark_page_map_args &a, cudaStream_t s) {
     }
     const int items = a.N > a.R + 1 ? a.N : a.R + 1;
     int blocks = (items + kMapThreads - 1) / kMapThreads;
-    if (blocks > sm_count()) blocks = sm_count();
+    if (blocks > 4 * sm_count()) blocks = 4 * sm_count();
     page_map_kernel<<<blocks, kMapThreads, smem, s>>>(a, page_of_size(a.page));
     return cudaGetLastError();
 }
