@@ -59,7 +59,7 @@ __device__ __forceinline__ void feed_lse(float &m, float &S, const float *x, int
         S *= ex2((m - cm) * kLog2e);
         m = cm;
     }
-    const float mL = m * kLog2e;
+    const float mL = m == -INFINITY ? 0.f : m * kLog2e;  // nothing but forbidden tokens so far: terms of 0
     float acc = 0.f;
 #pragma unroll
     for (int j = 0; j < n; ++j) acc += ex2(fmaf(x[j], kLog2e, -mL));
