@@ -15,7 +15,7 @@
 #pragma once
 
 #include "common.cuh"
-#include "kernels.h"
+#include "target.h"
 
 namespace dspark {
 namespace attn {

@@ -13,7 +13,7 @@
 #include <cuda_runtime.h>
 
 #include "attn_common.cuh"
-#include "tc.cuh"
+#include "attn_tc.cuh"
 
 namespace dspark {
 namespace attn {

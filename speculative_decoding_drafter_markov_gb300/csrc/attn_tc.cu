@@ -21,10 +21,13 @@
 // Bound by HBM while lines are few: a tile of D = 128 is 64 KB, 2,800 clocks of an
 // SM's share of the bandwidth, against 1,056 of MMA per operand.
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
+#include <mutex>
+
 #include "attn_common.cuh"
-#include "tc.cuh"
+#include "attn_tc.cuh"
 
 namespace dspark {
 namespace attn {
@@ -665,6 +668,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, 512);
     }
+}
+
+// A bf16 tensor of three dimensions (elements, the first adjacent; strides of the
+// other two in bytes) in boxes of 64 elements of the first, 128-byte swizzle; zeros
+// beyond the tensor.
+bool encode_bf16_map3(CUtensorMap *m, const void *base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
+                      const uint32_t (&box)[3]) {
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    });
+    if (!encode) return false;
+    const cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
+    const cuuint64_t st[2] = {strides[0], strides[1]};
+    const cuuint32_t b[3] = {box[0], box[1], box[2]};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), d, st, b, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // a map of the cache as [n_pages H][page][D], boxes of 64 columns x box tokens

@@ -873,22 +873,6 @@ bool encode_u_map(CUtensorMap *m, const void *U, int R, int gamma, int V, int MV
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// a bf16 tensor of three dimensions (elements, the first adjacent; strides of the
-// other two in bytes), boxes of 64 elements of the first, 128-byte swizzle; zeros
-// beyond the tensor
-bool encode_bf16_map3(CUtensorMap *m, const void *base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
-                      const uint32_t (&box)[3]) {
-    auto encode = encode_fn();
-    if (!encode) return false;
-    const cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
-    const cuuint64_t st[2] = {strides[0], strides[1]};
-    const cuuint32_t b[3] = {box[0], box[1], box[2]};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), d, st, b, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool tc_kernels_enabled() {
     static const bool on = [] {
         const char *v = getenv("DSPARK_DRAFT_KERNEL");

@@ -79,8 +79,6 @@ bool tc_available();
 bool tc_kernels_enabled();
 bool encode_w2t_map(CUtensorMap *m, const void *W2t, int V, int r, int BN);
 bool encode_kmajor_map(CUtensorMap *m, const void *base, int rows, int K, int ld, int box_rows);
-bool encode_bf16_map3(CUtensorMap *m, const void *base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
-                      const uint32_t (&box)[3]);
 bool encode_u_map(CUtensorMap *m, const void *U, int R, int gamma, int V, int MV);
 void tc_grid_shape(int R, int V, int MV, int BN, int *nparts, int *n_mtiles);
 
@@ -147,13 +145,6 @@ cudaError_t launch_verify_phase2_tc(const dspark_verify_args &a, VerifyWs &w, cu
 // ----- acceptance diagnostics and training losses ------------------------------------
 cudaError_t launch_accept_stats(const dspark_accept_stats_args &a, cudaStream_t s);
 cudaError_t launch_train_losses(const dspark_train_loss_args &a, cudaStream_t s);
-
-// ----- the target's pass: paged cache, attention of drafted rows, logit rules ---------
-cudaError_t launch_page_map(const dspark_page_map_args &a, cudaStream_t s);
-cudaError_t launch_cache_store(const dspark_cache_store_args &a, cudaStream_t s);
-size_t tree_attention_ws_bytes(const dspark_tree_attention_args &a);
-cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws, cudaStream_t s);
-cudaError_t launch_logit_rules(const dspark_logit_rules_args &a, cudaStream_t s);
 
 // ----- philox check ------------------------------------------------------------------
 cudaError_t launch_philox(const uint32_t *ctr, uint64_t seed, int n, uint32_t *out, cudaStream_t s);

@@ -5,7 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
-#include "kernels.h"
+#include "target.h"
 
 namespace dspark {
 

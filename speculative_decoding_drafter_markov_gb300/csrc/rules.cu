@@ -4,7 +4,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
-#include "kernels.h"
+#include "target.h"
 #include "tc.cuh"
 
 namespace dspark {
