@@ -46,6 +46,7 @@ __global__ void __launch_bounds__(kThreads) tree_attention_simt(const __grid_con
     float *sq = sh, *sk = sq + kLines * DP, *sv = sk + kTile * KS, *sp = sv + kTile * DP;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int line = tid >> 3, tx = tid & 7;  // scores: this thread's line and its tokens tx + 8 i
+    after_predecessor();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0) {
         const Share s = share_of(p);
@@ -232,7 +233,7 @@ struct Cells {
 template <int E, int kCols>
 __global__ void __launch_bounds__(32 * kJoinWarps, 8) tree_attention_join(const __grid_constant__ Params p) {
     __shared__ float sum_o[kJoinWarps - 1][32 * E * kCols];
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are written
+    after_predecessor();  // the partials are written
     const Join n = p.join[blockIdx.x];
     if (n.pieces == 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.stride;
@@ -329,8 +330,7 @@ cudaError_t launch_as(const Params &p, int grid, size_t smem, cudaStream_t s) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    kern<<<grid, kThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_close(kern, grid, kThreads, smem, s, p);
 }
 
 // CTAs of the CUDA-core kernel that fit an SM's shared memory (capped by its threads)
@@ -356,22 +356,14 @@ void carve(Params &p, void *ws, int grid) {
 }
 
 cudaError_t launch_join(const Params &p, int grid, cudaStream_t s) {
-    // a CTA for every line of a unit, as far as the host knows them; its CTAs come up
-    // while the first launch runs, and wait there for its end
+    // a CTA for every line of a unit, as far as the host knows them; the first launch lets
+    // them come up while it runs
     const long long lines = (long long)p.a.max_rows * p.heads;
-    cudaLaunchAttribute early{};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid, (unsigned)(lines < 1 ? 1 : lines < p.lines ? lines : p.lines));
-    if (cfg.gridDim.y > 16) cfg.gridDim.y = 16;
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.stream = s;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    if (p.stride % 4 == 0)
-        return p.stride <= 128 ? cudaLaunchKernelEx(&cfg, tree_attention_join<4, 1>, p) : cudaLaunchKernelEx(&cfg, tree_attention_join<4, 2>, p);
-    return p.stride <= 64 ? cudaLaunchKernelEx(&cfg, tree_attention_join<1, 2>, p) : cudaLaunchKernelEx(&cfg, tree_attention_join<1, 8>, p);
+    unsigned y = (unsigned)(lines < 1 ? 1 : lines < p.lines ? lines : p.lines);
+    if (y > 16) y = 16;
+    auto kern = p.stride % 4 == 0 ? (p.stride <= 128 ? tree_attention_join<4, 1> : tree_attention_join<4, 2>)
+                                  : (p.stride <= 64 ? tree_attention_join<1, 2> : tree_attention_join<1, 8>);
+    return launch_close(kern, dim3(grid, y), 32 * kJoinWarps, 0, s, p);
 }
 
 }  // namespace attn

@@ -45,6 +45,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_f32(const __grid_c
     float *own = sq + kLines * QS + warp * warp_floats(D), *sp = own + kStages * stage_floats(D);
     float2 *sml = reinterpret_cast<float2 *>(sh + kLines * QS + kWarps * warp_floats(D));  // [warp][line]
 
+    after_predecessor();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0) {
         const Share s = share_of(p);
@@ -297,8 +298,7 @@ cudaError_t launch_f32(Params p, int grid, cudaStream_t s) {
     auto kern = p.a.D > 64 ? tree_attention_f32<true> : tree_attention_f32<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, kThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_close(kern, grid, kThreads, smem, s, p);
 }
 
 }  // namespace attn

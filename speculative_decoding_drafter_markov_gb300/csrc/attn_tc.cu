@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tc::smem_u32(smem) & 1023u) {  // the swizzled tiles need it; the launch gives it
+        after_predecessor();
         if (tid == 0) set_err(a.err, DSPARK_ERR_UNSUPPORTED);
         return;
     }
@@ -222,14 +223,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_mbar_init();
     } else if (warp == 1) {
         if (lane < 24) bad[lane] = 0;
-        if (lane == 31) p.join[blockIdx.x].pieces = 0;
     } else if (warp == 8 && lane == 0) {
         tc::prefetch_tmap(&tmQ);
         tc::prefetch_tmap(&tmK);
         tc::prefetch_tmap(&tmV);
     }
+    after_predecessor();  // nothing of the inputs or the workspace was touched so far
     Share share{};
-    if (warp == 11) share = share_of(p);
+    if (warp == 11) {
+        share = share_of(p);
+        if (lane == 0) p.join[blockIdx.x].pieces = 0;
+    }
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
@@ -709,8 +713,7 @@ cudaError_t launch_as(const TcParams &tp, int grid, const CUtensorMap &q, const 
     auto kern = tree_attention_tc<C>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, kThreads, C::kSmem, s>>>(q, k, v, tp);
-    return cudaGetLastError();
+    return launch_close(kern, grid, kThreads, C::kSmem, s, q, k, v, tp);
 }
 
 }  // namespace

@@ -56,6 +56,7 @@ __device__ __forceinline__ unsigned need_of(const dspark_page_map_args &a, const
 
 __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const dspark_page_map_args a, const Page page) {
     extern __shared__ int sh[];
+    after_predecessor();
     const int R = a.R;
     const MapSums s{sh, sh + (R + 1), sh + 2 * (R + 1)};
     __shared__ unsigned wsum[2][3][kMapThreads / 32];
@@ -210,6 +211,7 @@ constexpr int kStoreThreads = 256;
 
 template <typename Vec, int kRows>
 __global__ void __launch_bounds__(kStoreThreads) cache_store_kernel(const dspark_cache_store_args a, const Page page, int es) {
+    after_predecessor();
     const int vpe = (int)sizeof(Vec) / es;  // elements of a piece
     const int per_head = a.D / vpe, per_row = a.H * per_head;
     int piece = blockIdx.y * kStoreThreads + threadIdx.x;
@@ -247,9 +249,8 @@ cudaError_t store_as(const dspark_cache_store_args &a, const Page &page, int es,
     const int pieces = 2 * a.H * (a.D / ((int)sizeof(Vec) / es)), y = (pieces + kStoreThreads - 1) / kStoreThreads;
     // eight rows a thread where that leaves every SM a few CTAs, else one
     const bool many = (long long)a.N * y >= 8ll * 4 * sm_count();
-    if (many) cache_store_kernel<Vec, 8><<<dim3((a.N + 7) / 8, y), kStoreThreads, 0, s>>>(a, page, es);
-    else cache_store_kernel<Vec, 1><<<dim3(a.N, y), kStoreThreads, 0, s>>>(a, page, es);
-    return cudaGetLastError();
+    return many ? launch_close(cache_store_kernel<Vec, 8>, dim3((a.N + 7) / 8, y), kStoreThreads, 0, s, a, page, es)
+                : launch_close(cache_store_kernel<Vec, 1>, dim3(a.N, y), kStoreThreads, 0, s, a, page, es);
 }
 
 Page page_of_size(int size) { return Page{(unsigned)size, (size & (size - 1)) == 0 ? __builtin_ctz((unsigned)size) : -1}; }
@@ -265,8 +266,7 @@ cudaError_t launch_page_map(const dspark_page_map_args &a, cudaStream_t s) {
     const int items = a.N > a.R + 1 ? a.N : a.R + 1;
     int blocks = (items + kMapThreads - 1) / kMapThreads;
     if (blocks > 4 * sm_count()) blocks = 4 * sm_count();
-    page_map_kernel<<<blocks, kMapThreads, smem, s>>>(a, page_of_size(a.page));
-    return cudaGetLastError();
+    return launch_close(page_map_kernel, blocks, kMapThreads, smem, s, a, page_of_size(a.page));
 }
 
 cudaError_t launch_cache_store(const dspark_cache_store_args &a, cudaStream_t s) {

@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kRulesThreads, 3) logit_rules_kernel(const dsp
     __shared__ int bias_n;
     __shared__ uint32_t keep[4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    after_predecessor();
     if (kAligned) vec = true;
     if (tid < 4) keep[tid] = (tid & 1 ? 0xffffu : 0u) | (tid & 2 ? 0xffff0000u : 0u);
     __syncthreads();
@@ -408,8 +409,7 @@ cudaError_t launch_as(const dspark_logit_rules_args &a, cudaStream_t s) {
     auto kern = aligned ? logit_rules_kernel<T, true> : logit_rules_kernel<T, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, kRulesThreads, smem, s>>>(a, slice, ((t ^ o) & 15) == 0);
-    return cudaGetLastError();
+    return launch_close(kern, grid, kRulesThreads, smem, s, a, slice, ((t ^ o) & 15) == 0);
 }
 
 }  // namespace
