@@ -449,6 +449,129 @@ def test_attention_same_bits_again():
         assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scale", [0.0, -0.25, 0.5])
+def test_attention_scales(dtype, scale):
+    s = make([300, 0, 77], [3, 2, 40], 8, 2, 64, 16, dtype, seed=3, tree=True)
+    s["scale"] = scale
+    check(s, *call(s))
+
+
+def shifted(t):
+    """The same values, contiguous, one element after an aligned address."""
+    flat = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+    out = flat[1:].view(t.shape)
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("what", ["q", "kc", "vc", "q_row", "q_head", "out"])
+def test_attention_alignment(dtype, what):
+    s = make([300, 0, 77], [3, 2, 40], 8, 2, 64, 16, dtype, seed=4)
+    s["q"] = s["q"].contiguous()
+    N, Hq, D = s["q"].shape
+    kw = {}
+    if what in ("q", "kc", "vc"):
+        s[what] = shifted(s[what])
+    elif what == "out":
+        kw["out"] = {"out": shifted(s["q"]), "lse": torch.empty((N, Hq), device="cuda")}
+    else:
+        wide = torch.zeros((N, Hq * D + 1) if what == "q_row" else (N, Hq, D + 3), dtype=dtype, device="cuda")
+        view = wide[:, :Hq * D].view(N, Hq, D) if what == "q_row" else wide[:, :, :D]
+        view.copy_(s["q"])
+        s["q"] = view
+    got, err = call(s, **kw)
+    check(s, got, err)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_attention_rows_of_one_tensor(dtype):
+    """Every row reads the same queries (a stride of zero)."""
+    s = make([30, 150], [2, 3], 4, 2, 64, 16, dtype, seed=5)
+    s["q"] = s["q"][:1].expand(5, -1, -1)
+    check(s, *call(s))
+
+
+def test_operators_between_other_work_in_a_graph():
+    """A kernel waits for whatever stands before it, of this library or not, on its
+    own stream or joined to it by an event; what stands after it sees its results."""
+    lens, rows, page, V = [70, 0, 33], [3, 2, 4], 16, 777
+    s = make(lens, rows, 4, 2, 64, page, torch.bfloat16, seed=6)
+    want = expect(s)
+    N, H, D = sum(rows), 2, 64
+    n, held, free, n_free = ints(rows), ints([0] * 3), ints(list(range(40))), ints([40])
+    lens_g, table = ints(lens), torch.full((3, 8), -1, dtype=torch.int32, device="cuda")
+    k, v, q = (torch.empty_like(x) for x in (s["q"][:, :H].contiguous(), s["q"][:, :H].contiguous(), s["q"].contiguous()))
+    start = s["start"]
+    ctx_k, ctx_v = torch.zeros((40, H, page, D), dtype=torch.bfloat16, device="cuda"), torch.zeros((40, H, page, D), dtype=torch.bfloat16, device="cuda")
+    rows_k, rows_v = [], []
+    for r in range(3):
+        for t in range(lens[r], lens[r] + rows[r]):
+            p = int(s["table"][r, t // page])
+            rows_k.append(s["kc"][p, :, t % page])
+            rows_v.append(s["vc"][p, :, t % page])
+    rows_k, rows_v = torch.stack(rows_k), torch.stack(rows_v)
+    T0 = torch.randn((N, V), device="cuda")
+    T, err = torch.empty_like(T0), err_word()
+    pres = torch.tensor([1.0, 2.0, 3.0], device="cuda")
+    hist, hist_len = torch.zeros((3, 1), dtype=torch.int32, device="cuda"), ints([1, 1, 1])
+    # the pages that the map will take hold the caches' tokens
+    probe = dsp.page_map(lens_g, n, table.clone(), held, free.clone(), n_free, page=page, N=N)
+    assert probe["row_start"].tolist() == start
+    trial = table.clone()
+    dsp.page_map(lens_g, n, trial, held, free.clone(), n_free, page=page, N=N)
+    for r in range(3):
+        for t in range(lens[r]):
+            a, b = int(trial[r, t // page]), int(s["table"][r, t // page])
+            ctx_k[a, :, t % page], ctx_v[a, :, t % page] = s["kc"][b, :, t % page], s["vc"][b, :, t % page]
+    kc, vc = torch.empty_like(ctx_k), torch.empty_like(ctx_v)
+
+    def cycle(side):
+        here = torch.cuda.current_stream()
+        kc.copy_(ctx_k)
+        m = dsp.page_map(lens_g, n, table, held, free, n_free, page=page, N=N, err=err)
+        fork = torch.cuda.Event()
+        fork.record(here)
+        with torch.cuda.stream(side):
+            side.wait_event(fork)
+            k.copy_(rows_k)
+            v.copy_(rows_v)
+            vc.copy_(ctx_v)
+            q.copy_(s["q"])
+            join = torch.cuda.Event()
+            join.record(side)
+        here.wait_event(join)
+        dsp.cache_store(k, v, m["slot"], kc, vc, err=err)
+        o = dsp.tree_attention(q, kc, vc, table, lens_g, m["row_start"], scale=s["scale"], max_rows=4, err=err)
+        T.copy_(T0)
+        z = dsp.logit_rules(T, m["row_start"], hist=hist, hist_len=hist_len, pres=pres, err=err)
+        T.zero_()
+        after = o["out"] * 1
+        return o, z, after
+
+    side = torch.cuda.Stream()
+    rules = T0.clone()
+    rules[:, 0] -= torch.repeat_interleave(pres, n.long())
+
+    def right(o, z, after):
+        check(s, o, err, want)
+        assert torch.equal(z, rules) and torch.equal(after, o["out"])
+
+    for _ in range(3):
+        right(*cycle(side))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = cycle(side)
+    for _ in range(3):
+        for x in (kc, vc, k, v, q, T):
+            x.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        right(*got)
+
+
 # ------------------------------------------------------------------ rules
 def rules_case(R, most, V, dtype, seed, tree=False, hist=60, bias=6):
     rng = np.random.default_rng(seed)
