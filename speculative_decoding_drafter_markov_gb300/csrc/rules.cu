@@ -28,13 +28,48 @@ namespace {
 // and the grammar on the way out; no warp waits for another.  In place there is
 // no copy to join, and the listed entries are scattered.
 // Bound by HBM: the logits' one read and one write.  The text is read once per
-// slice, from L2, which is why a slice is large.
+// slice, from L2, which is why a slice is large.  512 requests of up to 9 rows,
+// V = 129280, bf16, texts of up to 8192 tokens: 243 us, 5.5 TB/s; without the texts
+// 213 us.  (The CTAs of a request counting its text together, as a cluster of 2 / 4 / 8
+// through each other's shared memory, moved in step and took 3 / 13 / 35 us more than
+// each counting alone.)
 constexpr int kRulesThreads = 256;
 constexpr int kBiasList = 256;   // bias entries of a slice kept in shared memory
 constexpr int kWarps = kRulesThreads / 32;
 constexpr int kPart = 2048;      // bytes of a row that a warp stages: its part of a slice
 constexpr int kSliceBytes = kPart * kWarps;
-constexpr uint32_t kPromptBit = 1u << 31, kBiasBit = 1u << 30, kDraftBit = 1u << 29, kCountMask = kDraftBit - 1;
+
+// An entry's word: said in the prompt, marked (in the bias list or drafted), how often
+// in the output text.  16 bits serve texts of up to 16383 tokens; half the shared
+// memory leaves bf16 four CTAs on an SM instead of three: 243 us instead of 293 for
+// texts of up to 8192 tokens.
+template <typename Word>
+struct Entry;
+template <>
+struct Entry<uint16_t> {
+    static constexpr uint32_t kPrompt = 1u << 15, kMark = 1u << 14, kCount = kMark - 1;
+    using Listed = uint32_t;
+    static __device__ __forceinline__ void add(uint16_t *words, unsigned at, uint32_t x) {
+        atomicAdd(reinterpret_cast<uint32_t *>(words) + (at >> 1), x << (16 * (at & 1)));
+    }
+    static __device__ __forceinline__ void set(uint16_t *words, unsigned at, uint32_t x) {
+        atomicOr(reinterpret_cast<uint32_t *>(words) + (at >> 1), x << (16 * (at & 1)));
+    }
+    static __device__ __forceinline__ Listed listed(uint32_t word, int place) { return word | (uint32_t)place << 16; }
+    static __device__ __forceinline__ uint32_t word(Listed l) { return l & 0xffffu; }
+    static __device__ __forceinline__ int place(Listed l) { return (int)(l >> 16); }
+};
+template <>
+struct Entry<uint32_t> {
+    static constexpr uint32_t kPrompt = 1u << 31, kMark = 1u << 30, kCount = kMark - 1;
+    using Listed = uint2;
+    static __device__ __forceinline__ void add(uint32_t *words, unsigned at, uint32_t x) { atomicAdd(words + at, x); }
+    static __device__ __forceinline__ void set(uint32_t *words, unsigned at, uint32_t x) { atomicOr(words + at, x); }
+    static __device__ __forceinline__ Listed listed(uint32_t word, int place) { return make_uint2(word, (uint32_t)place); }
+    static __device__ __forceinline__ uint32_t word(Listed l) { return l.x; }
+    static __device__ __forceinline__ int place(Listed l) { return (int)l.y; }
+};
+constexpr int kShortText = Entry<uint16_t>::kCount;
 
 struct Bias {
     const int *id;      // the slice's entries in shared memory, in their order,
@@ -46,12 +81,12 @@ struct RowRules {
     float rep, inv_rep, freq, pres;
 };
 
-__device__ __forceinline__ float apply(float z, uint32_t word, int v, const RowRules &k, const Bias &b) {
-    const uint32_t c = word & kCountMask;
-    if (word & (kPromptBit | kCountMask)) z *= z > 0.f ? k.inv_rep : k.rep;
+// c: occurrences in the output and on the row's path
+__device__ __forceinline__ float apply(float z, uint32_t c, bool prompt, bool marked, int v, const RowRules &k, const Bias &b) {
+    if (prompt || c) z *= z > 0.f ? k.inv_rep : k.rep;
     z = fmaf(-k.freq, (float)c, z);
     if (c) z -= k.pres;
-    if (word & kBiasBit)
+    if (marked)
         for (int i = 0; i < b.n; ++i)
             if (b.id[i] == v) z += b.val[i];
     return z;
@@ -82,10 +117,11 @@ __device__ __forceinline__ uint32_t allowed(const uint32_t *allow, int v, int bi
 
 // kAligned: every row of T and out starts on a 16-byte boundary; else vec: T and out
 // lie alike to 16 bytes
-template <typename T, bool kAligned>
-__global__ void __launch_bounds__(kRulesThreads, 3) logit_rules_kernel(const dspark_logit_rules_args a, int slice, bool vec) {
+template <typename T, typename Word, bool kAligned>
+__global__ void __launch_bounds__(kRulesThreads, sizeof(Word) <= sizeof(T) ? 4 : 3) logit_rules_kernel(const dspark_logit_rules_args a, int slice, bool vec) {
     extern __shared__ __align__(128) unsigned char stage[];  // [warp][2][kPart], then the slice's words
-    uint32_t *word = reinterpret_cast<uint32_t *>(stage + 2 * kSliceBytes);
+    using W = Entry<Word>;
+    Word *word = reinterpret_cast<Word *>(stage + 2 * kSliceBytes);
     __shared__ uint64_t landed[kWarps][2];
     __shared__ int abort_word;
     __shared__ int bias_id[kBiasList];
@@ -234,31 +270,62 @@ __global__ void __launch_bounds__(kRulesThreads, 3) logit_rules_kernel(const dsp
     uint32_t ok[kMine];
     const uint32_t *allow = staged ? grammar_bits(j0, ok) : nullptr;
     // the first tokens of the text are on their way while the words are cleared
-    constexpr int kAhead = 8;
+    // (16 bytes at a time between the row's first and last 16-byte boundary)
+    constexpr int kAhead = 4;
     const int32_t *text = a.hist + (size_t)r * a.max_hist;
     if (!penal) n = 0;
-    int ahead[kAhead];
+    const int lead = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(text) & 15)) & 15) / 4), quads = (n - lead) / 4;
+    const int4 *text4 = reinterpret_cast<const int4 *>(text + lead);
+    int4 ahead[kAhead];
+    auto quad = [&](int q) { return q < quads ? text4[q] : make_int4(0, 0, 0, 0); };
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) ahead[i] = tid + i * kRulesThreads < n ? text[tid + i * kRulesThreads] : 0;
-    for (int i = 4 * tid; i < slice; i += 4 * kRulesThreads) *reinterpret_cast<uint4 *>(word + i) = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < kAhead; ++i) ahead[i] = quad(tid + i * kRulesThreads);
+    constexpr int kWords16 = 16 / (int)sizeof(Word);
+    for (int i = kWords16 * tid; i < slice; i += kWords16 * kRulesThreads)
+        *reinterpret_cast<uint4 *>(word + i) = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
+    const unsigned width = v1 - v0;
+    unsigned most = 0;  // largest token: those out of range are reported once
     auto count = [&](int i, int v) {
-        if ((unsigned)v >= (unsigned)a.V) set_err(a.err, DSPARK_ERR_RANGE);
-        if (v >= v0 && v < v1) {
-            if (i < np) atomicOr(&word[v - v0], kPromptBit);
-            else atomicAdd(&word[v - v0], 1u);
+        most = max(most, (unsigned)v);
+        const unsigned at = (unsigned)v - v0;
+        if (at < width) {
+            if (i < np) W::set(word, at, W::kPrompt);
+            else W::add(word, at, 1u);
         }
     };
+    auto count4 = [&](int q, const int4 &v) {
+        const int i = lead + 4 * q;
+        if (i >= np) {
+            most = max(max(max(most, (unsigned)v.x), max((unsigned)v.y, (unsigned)v.z)), (unsigned)v.w);
+            const unsigned x = (unsigned)v.x - v0, y = (unsigned)v.y - v0, z = (unsigned)v.z - v0, w = (unsigned)v.w - v0;
+            if (x < width) W::add(word, x, 1u);
+            if (y < width) W::add(word, y, 1u);
+            if (z < width) W::add(word, z, 1u);
+            if (w < width) W::add(word, w, 1u);
+        } else {
+            count(i, v.x);
+            count(i + 1, v.y);
+            count(i + 2, v.z);
+            count(i + 3, v.w);
+        }
+    };
+#pragma unroll 1
+    for (int q = tid; q < quads; q += kRulesThreads) {
+        const int4 v = ahead[0];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-        if (tid + i * kRulesThreads < n) count(tid + i * kRulesThreads, ahead[i]);
-#pragma unroll 8
-    for (int i = kAhead * kRulesThreads + tid; i < n; i += kRulesThreads) count(i, text[i]);
+        for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
+        ahead[kAhead - 1] = quad(q + kAhead * kRulesThreads);
+        count4(q, v);
+    }
+    if (tid < lead) count(tid, text[tid]);
+    if (tid < n - lead - 4 * quads) count(lead + 4 * quads + tid, text[lead + 4 * quads + tid]);
+    if (most >= (unsigned)a.V) set_err(a.err, DSPARK_ERR_RANGE);
     if (path)  // whatever a row of the run may continue
         for (int at = 1 + tid; at < rows; at += kRulesThreads) {
             const int v = a.tok[row0 + at];
             if ((unsigned)v >= (unsigned)a.V) set_err(a.err, DSPARK_ERR_RANGE);
-            if (v >= v0 && v < v1) atomicOr(&word[v - v0], kDraftBit);
+            if (v >= v0 && v < v1) W::set(word, v - v0, W::kMark);
         }
     if (b1 > b0 && tid < 32) {  // one warp, so that the list keeps the entries' order
         int found = 0;
@@ -269,7 +336,7 @@ __global__ void __launch_bounds__(kRulesThreads, 3) logit_rules_kernel(const dsp
             const unsigned who = __ballot_sync(0xffffffffu, in);
             const int at = found + __popc(who & ((1u << lane) - 1));
             if (in) {
-                atomicOr(&word[v - v0], kBiasBit);
+                W::set(word, v - v0, W::kMark);
                 if (at < kBiasList) {
                     bias_id[at] = v;
                     bias_val[at] = a.bias_val[i + lane];
@@ -282,20 +349,22 @@ __global__ void __launch_bounds__(kRulesThreads, 3) logit_rules_kernel(const dsp
     __syncthreads();
     bias.n = bias_n;
     if (bias.n > kBiasList) bias = Bias{a.bias_id + b0, a.bias_val + b0, b1 - b0};
-    // The warp's list of touched entries {word, place}, over its words: a lane takes
-    // `part / 32` of them into registers.  With more entries than fit there the words
-    // stay, and are searched for every row.
-    constexpr int kLaneWords = kPart / (int)sizeof(T) / 32;
-    uint32_t *mine = word + warp * part;
-    uint2 *list = reinterpret_cast<uint2 *>(mine);
+    // The warp's list of touched entries, over its words: a lane takes `part / 32` of
+    // them into registers.  With more entries than fit there the words stay, and are
+    // searched for every row.
+    constexpr int kPacked = 4 / (int)sizeof(Word);  // words of a register
+    constexpr int kLaneWords = kPart / (int)sizeof(T) / 32 / kPacked;
+    const Word *mine = word + warp * part;
+    typename W::Listed *list = reinterpret_cast<typename W::Listed *>(word + warp * part);
     int listed = 0;
     {
         uint32_t w[kLaneWords];
         int n_own = 0;
 #pragma unroll
         for (int i = 0; i < kLaneWords; ++i) {
-            w[i] = 32 * i < part ? mine[32 * i + lane] : 0u;
-            n_own += w[i] != 0;
+            w[i] = 32 * i * kPacked < part ? reinterpret_cast<const uint32_t *>(mine)[32 * i + lane] : 0u;
+            if (kPacked == 2) n_own += ((w[i] & 0xffffu) != 0) + ((w[i] >> 16) != 0);
+            else n_own += w[i] != 0;
         }
         int at = n_own;
 #pragma unroll
@@ -308,8 +377,16 @@ __global__ void __launch_bounds__(kRulesThreads, 3) logit_rules_kernel(const dsp
         if (listed <= part / 2) {
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < kLaneWords; ++i)
-                if (w[i]) list[at++] = make_uint2(w[i], (uint32_t)(32 * i + lane));
+            for (int i = 0; i < kLaneWords; ++i) {
+                if (!w[i]) continue;
+                const int place = (32 * i + lane) * kPacked;
+                if (kPacked == 1) {
+                    list[at++] = W::listed(w[i], place);
+                } else {
+                    if (w[i] & 0xffffu) list[at++] = W::listed(w[i] & 0xffffu, place);
+                    if (w[i] >> 16) list[at++] = W::listed(w[i] >> 16, place + 1);
+                }
+            }
             __syncwarp();
         }
     }
@@ -317,21 +394,22 @@ __global__ void __launch_bounds__(kRulesThreads, 3) logit_rules_kernel(const dsp
     // f(place in the part, word) for the touched entries, a lane each
     auto touched = [&](auto f) {
         if (by_list) {
-            for (int i = lane; i < listed; i += 32) f((int)list[i].y, list[i].x);
+            for (int i = lane; i < listed; i += 32) f(W::place(list[i]), W::word(list[i]));
         } else {
             for (int i = lane; i < part; i += 32)
-                if (mine[i]) f(i, mine[i]);
+                if (mine[i]) f(i, (uint32_t)mine[i]);
         }
     };
 
     // entry v of row j, whose word is w
     auto value = [&](int j, int v, uint32_t w, float z) {
-        if (w & kDraftBit) {  // drafted in the request: how often on this row's path
+        uint32_t c = w & W::kCount;
+        if ((w & W::kMark) && path) {  // perhaps drafted in the request: how often on this row's path
             const uint64_t *mine = a.mask ? a.mask + (size_t)(row0 + j) * a.W : nullptr;
             for (int at = 1; at < (mine ? rows : j + 1); ++at)
-                if (a.tok[row0 + at] == v && (!mine || ((mine[at >> 6] >> (at & 63)) & 1))) ++w;
+                if (a.tok[row0 + at] == v && (!mine || ((mine[at >> 6] >> (at & 63)) & 1))) ++c;
         }
-        return apply(z, w, v, k, bias);
+        return apply(z, c, w & W::kPrompt, w & W::kMark, v, k, bias);
     };
     auto scatter = [&](int j, int v, uint32_t w, const uint32_t *allow, const T *src, T *dst) {
         if (!allow || allowed<true>(allow, v, 1)) put(dst + v, value(j, v, w, to_f32(src[v])));
@@ -390,7 +468,7 @@ __global__ void __launch_bounds__(kRulesThreads, 3) logit_rules_kernel(const dsp
     }
 }
 
-template <typename T>
+template <typename T, typename Word>
 cudaError_t launch_as(const dspark_logit_rules_args &a, cudaStream_t s) {
     // Slices as large as leave every SM three CTAs; where requests are few the
     // rows are spread too, at the price of counting the text for each run.
@@ -403,10 +481,10 @@ cudaError_t launch_as(const dspark_logit_rules_args &a, cudaStream_t s) {
     if (runs > per) runs = per;
     if (runs < 1) runs = 1;
     const dim3 grid(slices, a.R, (unsigned)runs);
-    const size_t smem = 2 * kSliceBytes + sizeof(uint32_t) * (kSliceBytes / sizeof(T));
+    const size_t smem = 2 * kSliceBytes + sizeof(Word) * (kSliceBytes / sizeof(T));
     const uintptr_t t = reinterpret_cast<uintptr_t>(a.T), o = reinterpret_cast<uintptr_t>(a.out);
     const bool aligned = ((t | o | (uintptr_t)a.V * sizeof(T)) & 15) == 0;
-    auto kern = aligned ? logit_rules_kernel<T, true> : logit_rules_kernel<T, false>;
+    auto kern = aligned ? logit_rules_kernel<T, Word, true> : logit_rules_kernel<T, Word, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_close(kern, grid, kRulesThreads, smem, s, a, slice, ((t ^ o) & 15) == 0);
@@ -415,7 +493,8 @@ cudaError_t launch_as(const dspark_logit_rules_args &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_logit_rules(const dspark_logit_rules_args &a, cudaStream_t s) {
-    return a.dtype == DSPARK_BF16 ? launch_as<__nv_bfloat16>(a, s) : launch_as<float>(a, s);
+    if (a.dtype != DSPARK_BF16) return launch_as<float, uint32_t>(a, s);
+    return !a.hist || a.max_hist <= kShortText ? launch_as<__nv_bfloat16, uint16_t>(a, s) : launch_as<__nv_bfloat16, uint32_t>(a, s);
 }
 
 }  // namespace dspark

@@ -709,6 +709,23 @@ def test_rules_texts_of_many_tokens(dtype, V):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("hist,shift", [(16383, 0), (16384, 0), (40001, 0), (16381, 3)])
+def test_rules_long_texts(dtype, hist, shift):
+    """One token said nearly all the time, next to others; rows of the text that do
+    not start on 16 bytes."""
+    s = rules_case(3, 4, 1500, dtype, seed=hist, hist=hist)
+    s["hist"][:, 7:] = np.where(np.arange(hist - 7) % 97 == 0, s["hist"][:, 7:], 701)
+    s["hist_len"][:], s["prompt_len"][:] = (hist, hist - 1, hist), (0, 5, 16001 if hist > 16001 else 9)
+    s["freq"] *= 2.0 ** -10
+    args = rules_args(s)
+    if shift:
+        flat = torch.zeros(3 * hist + shift, dtype=torch.int32, device="cuda")
+        flat[shift:] = args["hist"].flatten()
+        args["hist"] = flat[shift:].view(3, hist)
+    rules_check(s, dsp.logit_rules(s["T"], ints(s["start"]), **args), rules_expect(s))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("V", [1024, 1023])
 def test_rules_infinities_and_nan(dtype, V):
     """-inf and NaN logits stay themselves where allowed and are -inf where not."""
