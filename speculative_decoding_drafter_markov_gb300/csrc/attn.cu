@@ -399,6 +399,8 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws,
     p.block_rows = kLines / p.heads;
     p.lines = p.block_rows * p.heads;
     p.stride = a.D;
+    p.small_rows = p.block_rows;
+    p.small_places = p.large_places = 1;
     if (f32_supported(a)) {
         const int grid = f32_grid();
         carve(p, ws, grid);

@@ -7,9 +7,10 @@
 // tiles.  The tiles of all units stand in one line -- by request, block, head --
 // and each CTA takes an equal, consecutive share of the line, whatever the
 // lengths of the requests are: a long cache is spread over many CTAs, many short
-// ones are packed into one, and no length reaches the host.  Before its tiles a
-// unit has `unit_cost` empty places in the line, the tiles' worth of its start and
-// end, so that CTAs with many short units get fewer tiles.  A CTA leaves a unit
+// ones are packed into one, and no length reaches the host.  A tile has as many places
+// in the line as its time is worth, and before its tiles a unit has `unit_cost` empty
+// tiles' worth of places for its start and end, so that CTAs with many short units get
+// fewer tiles.  A tile is the CTA's whose share holds its first place.  A CTA leaves a unit
 // that it did not do whole as a partial (unnormalised sums, maximum and sum of
 // the weights); a second launch joins the partials of each unit.
 #pragma once
@@ -34,7 +35,9 @@ struct Params {
     int block_rows;   // rows of a unit
     int lines;        // block_rows * heads
     int tile_log2;    // tokens of a tile
-    int unit_cost;    // places of a unit in the line beside its tiles
+    int unit_cost;    // empty tiles of a unit before its tiles
+    int small_rows;   // a unit of up to so many rows has tiles of small_places,
+    int small_places, large_places;  // one of more rows of large_places
     int stride;       // floats of a partial's line
     int mixed;        // partials in the order of the tensor-core fragments (see `plain_column`)
     int vec;          // CUDA-core kernel: 16-byte loads are possible
@@ -80,10 +83,15 @@ __device__ __forceinline__ int tiles_of(const Params &p, const Request &q, int b
     return (int)(((unsigned)tokens_of(p, q, b) + (1u << p.tile_log2) - 1) >> p.tile_log2);
 }
 
+// places of a tile of block b
+__device__ __forceinline__ int tile_places(const Params &p, const Request &q, int b) {
+    return min(p.block_rows, q.rows - b * p.block_rows) > p.small_rows ? p.large_places : p.small_places;
+}
+
 __device__ __forceinline__ long long request_places(const Params &p, const Request &q) {
     const int n = blocks_of(p, q.rows);
     long long t = 0;
-    for (int b = 0; b < n; ++b) t += tiles_of(p, q, b) + p.unit_cost;
+    for (int b = 0; b < n; ++b) t += (long long)(tiles_of(p, q, b) + p.unit_cost) * tile_places(p, q, b);
     return t * (p.a.H * p.subs);
 }
 
@@ -122,12 +130,14 @@ __device__ inline Share share_of(const Params &p) {
     }
     long long total = __shfl_sync(0xffffffffu, inc, 31);
     Share s{0, 0, 1, 0, 0, 0};
-    if (total > 0x7fffffffll) {  // months of work: not a case to count in 64 bits for
+    if (total > 0x7fffffffll) {  // far above the work of a call: not counted in 64 bits
         if (lane == 0 && blockIdx.x == 0) set_err(p.a.err, DSPARK_ERR_UNSUPPORTED);
         total = 0;
     }
-    const unsigned t = (unsigned)total, c = blockIdx.x, ctas = min(gridDim.x, t);
-    if (c >= ctas) return s;
+    // no share is smaller than a tile, so every CTA between a unit's first and last one
+    // has a tile of it
+    const unsigned t = (unsigned)total, c = blockIdx.x, ctas = min(gridDim.x, max(1u, t / (unsigned)p.large_places));
+    if (t == 0 || c >= ctas) return s;
     s.each = t / ctas;
     s.more = t - s.each * ctas;
     s.lo = c * s.each + min((int)c, s.more);
@@ -153,7 +163,8 @@ struct Walk {
     int at;            // next place of the line
     int r, b, h;       // its unit
     int begin;         // the unit's first place
-    int tiles, blocks; // of the unit, of the request
+    int tiles, places; // of the unit: tiles, and places of one
+    int blocks;        // of the request
     Request q;
     bool first;
 
@@ -164,20 +175,37 @@ struct Walk {
         blocks = blocks_of(p, q.rows);
         int left = s.lo - s.r_begin;
         for (;; ++b) {
-            tiles = tiles_of(p, q, b);
-            const int line = (tiles + p.unit_cost) * p.a.H * p.subs;
+            shape();
+            const int line = (tiles + p.unit_cost) * places * p.a.H * p.subs;
             if (left < line) break;
             left -= line;
         }
-        h = (unsigned)left / (unsigned)(tiles + p.unit_cost);
-        begin = s.lo - (left - h * (tiles + p.unit_cost));
+        const int unit = (tiles + p.unit_cost) * places;
+        h = (unsigned)left / (unsigned)unit;
+        begin = s.lo - (left - h * unit);
+    }
+
+    __device__ __forceinline__ void shape() {
+        tiles = tiles_of(p, q, b);
+        places = tile_places(p, q, b);
+    }
+
+    // the unit's first tile at or after a place of the line
+    __device__ __forceinline__ int tile_at(int place) const {
+        const int d = place - (begin + p.unit_cost * places);
+        return d <= 0 ? 0 : min((unsigned)tiles, (unsigned)(d + places - 1) / (unsigned)places);
     }
 
     __device__ __forceinline__ bool next(Piece &out) {
-        if (s.hi <= begin + p.unit_cost || at >= s.hi) return false;  // no tile of the unit is left here
-        const int skip = begin + p.unit_cost;
-        out.t0 = max(0, at - skip);
-        out.t1 = min(tiles, s.hi - skip);
+        if (at >= s.hi) return false;
+        out.t0 = tile_at(at);
+        if (out.t0 == tiles) {  // the share begins within the unit's last tile
+            advance();
+            if (at >= s.hi) return false;
+            out.t0 = 0;
+        }
+        out.t1 = tile_at(s.hi);
+        if (out.t0 >= out.t1) return false;  // the unit's first tile is another CTA's
         out.r = r;
         out.head = h;
         out.tiles = tiles;
@@ -189,27 +217,32 @@ struct Walk {
         out.tokens = tokens_of(p, q, b);
         out.slot = out.t0 == 0 && out.t1 == tiles ? -1 : 2 * (int)blockIdx.x + (first ? 0 : 1);
         first = false;
-        at = skip + out.t1;
-        if (at < s.hi) {  // the unit is done: the next head, block or request
-            begin = at;
-            if (++h == p.a.H * p.subs) {
-                h = 0;
-                if (++b == blocks) {
-                    b = 0;
-                    do {
-                        q = request_of(p, ++r, false);
-                    } while (q.rows == 0);
-                    blocks = blocks_of(p, q.rows);
-                }
-                tiles = tiles_of(p, q, b);
-            }
-        }
+        if (out.t1 == tiles) advance();
+        else at = s.hi;
         return true;
     }
 
+    // the unit is done: the next head, block or request, if its places begin in the share
+    __device__ __forceinline__ void advance() {
+        at = begin + (p.unit_cost + tiles) * places;
+        if (at >= s.hi) return;
+        begin = at;
+        if (++h < p.a.H * p.subs) return;
+        h = 0;
+        if (++b == blocks) {
+            b = 0;
+            do {
+                q = request_of(p, ++r, false);
+            } while (q.rows == 0);
+            blocks = blocks_of(p, q.rows);
+        }
+        shape();
+    }
+
     // what the second launch needs of a piece that starts a unit and does not end it
+    // (the last one of its share: the walk still stands at its unit)
     __device__ __forceinline__ Join join_of(const Piece &x) const {
-        const unsigned last = (unsigned)(s.hi - x.t1 + x.tiles) - 1;  // the piece ends the share
+        const unsigned last = begin + (p.unit_cost + x.tiles - 1) * places;
         const unsigned big = (unsigned)s.more * (s.each + 1);
         const unsigned c = last < big ? last / (unsigned)(s.each + 1) : s.more + (last - big) / (unsigned)s.each;
         const int sub = p.subs == 1 ? 0 : x.head % p.subs, h0 = p.subs == 1 ? x.head : x.head / p.subs;

@@ -37,7 +37,10 @@ namespace {
 constexpr int kThreads = 384, kTileLog2 = 7, kTile = 1 << kTileLog2;
 constexpr float kSlack = 8.f;  // log2 by which half a tile may exceed the reference
 constexpr int kQueue = 4;      // pieces handed out ahead
-constexpr int kUnitCost = 3;   // tiles' worth of a unit's start and end
+// Places in the line of units: of a tile for one operand and for two, tiles' worth of a
+// unit's start and end.  With 3 : 5 : 3 the 16 trees of up to 64 rows over up to 16384
+// tokens took 100 us, with 1 : 1 : 3 112, with 2 : 4 : 3 106, with 2 : 3 : 3 101.
+constexpr int kTilePlaces = 3, kDualPlaces = 5, kUnitCost = 3;
 
 // DP: D padded to the copied width, NQ: operands a unit may have
 template <int DP_, int NQ_>
@@ -725,8 +728,10 @@ bool tc_supported(const dspark_tree_attention_args &a) {
            a.q_head > 0 && a.q_row < (1ll << 38) && a.q_head < (1ll << 38) && tc_kernels_enabled() && tc_available();
 }
 
-// One operand while the host's hint says that a request's lines fit it, else two:
-// a unit of two reads its keys once for twice the lines.
+// One operand while the host's hint says that a request's lines fit it, else two: a unit
+// of two reads its keys once for twice the lines.  (8 caches of up to 131072 tokens, up
+// to 256 lines: 438 us with two, 572 with one; 4 prompts of up to 4096 rows: 191 and 229;
+// 16 caches of up to 1000 tokens, where there are few pieces to share: 33 and 29.)
 void tc_shape(const dspark_tree_attention_args &a, int *block_rows, int *lines, int *stride) {
     const int G = a.Hq / a.H, one = 128 / G;
     *block_rows = a.max_rows > one ? 2 * one : one;
@@ -740,6 +745,9 @@ cudaError_t launch_tc(Params p, int grid, cudaStream_t s) {
     tp.op_rows = 128 / p.G;
     tp.inv_group = (65536 + p.G - 1) / p.G;
     p.tile_log2 = kTileLog2;
+    p.small_rows = tp.op_rows;
+    p.small_places = kTilePlaces;
+    p.large_places = p.block_rows > tp.op_rows ? kDualPlaces : kTilePlaces;
     p.unit_cost = kUnitCost;
     tp.p = p;
     tp.box = a.page & -a.page;

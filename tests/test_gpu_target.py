@@ -302,6 +302,15 @@ def test_attention_split_and_packed(dtype, R, ctx):
     check(s, *call(s))
 
 
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("lens,rows", [([3000, 10, 700, 0, 129, 5000], [1, 40, 64, 3, 65, 17]), ([0, 0, 0], [33, 1, 64]),
+                                       ([20000, 127], [64, 32]), ([60] * 40, [34, 2, 64, 30] * 10)])
+def test_attention_small_and_large_blocks(tree, lens, rows):
+    """Requests whose rows fill one operand of the tensor cores beside ones that need two."""
+    s = make(lens, rows, 8, 2, 128, 16, torch.bfloat16, seed=len(lens), tree=tree)
+    check(s, *call(s))
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("spread", [0.0, 30.0])
 def test_attention_flat_and_peaked(dtype, spread):
