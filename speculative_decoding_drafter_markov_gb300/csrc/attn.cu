@@ -15,7 +15,9 @@ namespace {
 // A unit of 16 lines (4 per warp) over tiles of 32 tokens; keys and values of a
 // tile are staged in shared memory as fp32 and shared by the lines.  A thread
 // scores one line against four tokens, then each warp adds its four lines'
-// weighted values, the lanes side by side over D.
+// weighted values, the lanes side by side over D.  Bound by its instructions: 64 caches
+// of up to 8192 tokens, 36 lines on each of 8 heads of 128, bf16: 1363 us, against 128 us
+// on the tensor cores; one row over 2047 tokens 28 against 12.
 constexpr int kLines = kSimtLines, kTileLog2 = 5, kTile = 1 << kTileLog2, kThreads = 128;
 
 template <typename T>
@@ -212,7 +214,8 @@ __global__ void __launch_bounds__(kThreads) tree_attention_simt(const __grid_con
 // lines of CTA c's unit: a warp a line, or, where a unit has many pieces (one long
 // cache over the whole GPU), the four warps of a CTA share a line's pieces.  Bound by
 // latency: partials that are still in L2, four under way before the weights are known
-// (eight take the registers of half of the CTAs: 2 us more for 256 lines).
+// (eight take the registers of half of the CTAs: 2 us more for 256 lines).  About 3 us
+// for a few lines, 9 us for 256 lines in each of 16 requests.
 constexpr int kJoinWarps = 4, kJoinMany = 8, kAhead = 4;
 
 // four (or, E = 1, one) adjacent floats per lane
