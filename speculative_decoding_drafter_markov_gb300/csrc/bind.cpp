@@ -2,7 +2,7 @@
 //
 // They run once per layer or per cycle, some on inputs so small that the host's
 // share is the whole time: through ctypes, checking thirteen tensors and making
-// five cost 24 us around a kernel of 3.  This module (8 us) does the same checks and
+// five cost 24 us around a kernel of 3.  This module (6 us) does the same checks and
 // allocations on the tensors themselves and calls the same C entry points; it
 // holds no state and none of the operators' arithmetic.
 #include <Python.h>
@@ -156,7 +156,33 @@ struct Outputs {
             }
             return gpu.want(name, o, dt, shape);
         }
-        at::Tensor t = gpu.empty(dt, shape);
+        return add(name, gpu.empty(dt, shape));
+    }
+    struct Part {
+        const char *name;
+        int64_t n;
+        int32_t **at;
+    };
+    // int32 vectors in one allocation, each on a 256-byte boundary: the allocator is what
+    // a call with small outputs costs most
+    void get_together(const Gpu &gpu, std::initializer_list<Part> parts) {
+        if (!own) {
+            for (const Part &p : parts) *p.at = static_cast<int32_t *>(get(gpu, p.name, at::kInt, {p.n}));
+            return;
+        }
+        int64_t all = 0;
+        for (const Part &p : parts) all += (p.n + 63) / 64 * 64;
+        const at::Tensor whole = gpu.empty(at::kInt, {all});
+        int64_t from = 0;
+        for (const Part &p : parts) {
+            at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
+            t.unsafeGetTensorImpl()->set_storage_offset(from);
+            t.unsafeGetTensorImpl()->set_sizes_contiguous({p.n});
+            *p.at = static_cast<int32_t *>(add(p.name, std::move(t)));
+            from += (p.n + 63) / 64 * 64;
+        }
+    }
+    void *add(const char *name, at::Tensor t) {
         void *at = t.data_ptr();
         PyObject *o = THPVariable_Wrap(std::move(t));
         const int rc = o ? PyDict_SetItemString(dict, name, o) : -1;
@@ -208,11 +234,9 @@ PyObject *page_map(PyObject *const *x, Py_ssize_t n) {
     a.n_free = i32(gpu.want("n_free", x[5], I32, {1}));
     a.err = i32(gpu.maybe("err", x[11], I32));
     Outputs out(x[10]);
-    a.held_out = i32(out.get(gpu, "held", I32, {R}));
-    a.n_free_out = i32(out.get(gpu, "n_free", I32, {1}));
-    a.row_start = i32(out.get(gpu, "row_start", I32, {R + 1}));
-    a.slot = i32(out.get(gpu, "slot", I32, {a.N}));
-    a.pos = i32(out.get(gpu, "pos", I32, {a.N}));
+    // what the next call reads apart from what the cycle does, so that it keeps no more alive
+    out.get_together(gpu, {{"held", R, &a.held_out}, {"n_free", 1, &a.n_free_out}});
+    out.get_together(gpu, {{"row_start", R + 1, &a.row_start}, {"slot", a.N, &a.slot}, {"pos", a.N, &a.pos}});
     if (a.parents) a.mask = static_cast<uint64_t *>(out.get(gpu, "mask", I64, {a.N, a.W}));
     check(dspark_page_map(&a, gpu.stream()));
     return out.take();
