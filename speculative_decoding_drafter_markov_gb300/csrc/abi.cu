@@ -505,7 +505,7 @@ static int check_tree_attention(const dspark_tree_attention_args *a) {
     if (a->dtype != DSPARK_F32 && a->dtype != DSPARK_BF16) return fail(DSPARK_ERR_INVAL, "bad dtype %d", a->dtype);
     if (a->D > DSPARK_ATTN_MAX_D) return fail(DSPARK_ERR_UNSUPPORTED, "D=%d above %d", a->D, DSPARK_ATTN_MAX_D);
     if ((long long)a->N * a->Hq > 0x7fffffffll || (long long)a->n_pages * a->H > 0x7fffffffll ||
-        (long long)a->max_pages * a->page > 0x7fffffffll)
+        (long long)a->max_pages * a->page > 0x7fffff00ll)  // the end of a request's last tile stays within 32 bits
         return fail(DSPARK_ERR_UNSUPPORTED, "too many rows, pages or tokens");
     if (a->mask && a->W < 1) return fail(DSPARK_ERR_INVAL, "bad W=%d", a->W);
     if (a->mask && a->W > DSPARK_ATTN_MAX_TREE / 64)

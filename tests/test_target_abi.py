@@ -94,3 +94,9 @@ def test_logit_rules_refusals(lib):
                        (dict(row_start=None), 1), (dict(hist_len=None), 1), (dict(bias_id=None), 1), (dict(allow_row=None), 1),
                        (dict(W=0), 1), (dict(max_hist=-1), 1)]:
         refused(lib, "dspark_logit_rules", filled(lib.LogitRulesArgs, **{**good, **over}), code, None)
+
+
+def test_tables_whose_last_tile_passes_32_bits_are_refused(lib):
+    a = filled(lib.TreeAttentionArgs, R=4, N=8, Hq=8, H=2, D=64, page=16, n_pages=10, max_pages=(1 << 27) - 1, dtype=1, W=1,
+               max_rows=4, scale=1.0)
+    refused(lib, "dspark_tree_attention", a, lib.ERR_UNSUPPORTED, SOME, None)
