@@ -89,12 +89,13 @@ __global__ void __launch_bounds__(kThreads) tree_attention_simt(const __grid_con
                 const int tk = i / per, d = i % per * 4, tok = tok0 + tk;
                 float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
                 if (tok < x.tokens) {
-                    int pg = a.table[(size_t)x.r * a.max_pages + tok / a.page];
+                    const int in_table = p.page.of(tok);
+                    int pg = a.table[(size_t)x.r * a.max_pages + in_table];
                     if (pg < 0 || pg >= a.n_pages) {
                         set_err(a.err, DSPARK_ERR_RANGE);
                         pg = 0;
                     }
-                    const size_t at = (((size_t)pg * a.H + h) * a.page + tok % a.page) * D + d;
+                    const size_t at = (((size_t)pg * a.H + h) * a.page + (tok - in_table * a.page)) * D + d;
                     if (p.vec) {
                         kv = load4(kc + at);
                         vv = load4(vc + at);
@@ -403,9 +404,11 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws,
     p.lines = p.block_rows * p.heads;
     p.stride = a.D;
     p.small_rows = p.block_rows;
-    p.small_places = p.large_places = 1;
+    p.small_places = p.large_places = div_by(1);
+    p.page = div_by(a.page);
     if (f32_supported(a)) {
         const int grid = f32_grid();
+        p.ctas = div_by(grid);
         carve(p, ws, grid);
         cudaError_t e = launch_f32(p, grid, s);
         return e == cudaSuccess ? launch_join(p, grid, s) : e;
@@ -415,6 +418,7 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws,
     const int es = a.dtype == DSPARK_BF16 ? 2 : 4;
     p.vec = a.D % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.k_cache) | reinterpret_cast<uintptr_t>(a.v_cache)) & (4 * es - 1)) == 0;
     const int grid = simt_grid(a.D);
+    p.ctas = div_by(grid);
     carve(p, ws, grid);
     const size_t smem = smem_bytes(a.D);
     const bool wide = a.D > 128;

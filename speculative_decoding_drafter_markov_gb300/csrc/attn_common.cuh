@@ -27,6 +27,21 @@ struct Join {
     int row, head, heads, lines;
 };
 
+// Division of a number below 2^31 by one that the host knows, as a product and a shift:
+// the divide routine's chain is long where one thread prepares a CTA's work.  With
+// 2^(l - 1) < by <= 2^l and mul = ceil(2^(31 + l) / by), x mul / 2^(31 + l) is above
+// x / by by less than 1 / by.
+struct Div {
+    unsigned by, mul;
+    int shift;
+    __device__ __forceinline__ int of(int x) const { return (int)(((unsigned long long)(unsigned)x * mul) >> shift); }
+};
+inline Div div_by(unsigned by) {
+    int l = 0;
+    while ((1ull << l) < by) ++l;
+    return Div{by, (unsigned)(((1ull << (31 + l)) + by - 1) / by), 31 + l};
+}
+
 struct Params {
     dspark_tree_attention_args a;
     int G;            // query heads per key-value head
@@ -37,7 +52,8 @@ struct Params {
     int tile_log2;    // tokens of a tile
     int unit_cost;    // empty tiles of a unit before its tiles
     int small_rows;   // a unit of up to so many rows has tiles of small_places,
-    int small_places, large_places;  // one of more rows of large_places
+    Div small_places, large_places;  // one of more rows of large_places
+    Div page, ctas;   // tokens of a page; CTAs of the launch
     int stride;       // floats of a partial's line
     int mixed;        // partials in the order of the tensor-core fragments (see `plain_column`)
     int vec;          // CUDA-core kernel: 16-byte loads are possible
@@ -70,6 +86,8 @@ __device__ __forceinline__ Request request_of(const Params &p, int r, bool repor
     return Request{row0, ok ? row1 - row0 : 0, len};
 }
 
+__device__ __forceinline__ Request request_of(const Params &p, int r) { return request_of(p, r, false); }
+
 __device__ __forceinline__ int blocks_of(const Params &p, int rows) {
     return rows <= p.block_rows ? (rows > 0 ? 1 : 0) : (rows + p.block_rows - 1) / p.block_rows;
 }
@@ -84,14 +102,14 @@ __device__ __forceinline__ int tiles_of(const Params &p, const Request &q, int b
 }
 
 // places of a tile of block b
-__device__ __forceinline__ int tile_places(const Params &p, const Request &q, int b) {
+__device__ __forceinline__ const Div &tile_places(const Params &p, const Request &q, int b) {
     return min(p.block_rows, q.rows - b * p.block_rows) > p.small_rows ? p.large_places : p.small_places;
 }
 
 __device__ __forceinline__ long long request_places(const Params &p, const Request &q) {
     const int n = blocks_of(p, q.rows);
     long long t = 0;
-    for (int b = 0; b < n; ++b) t += (long long)(tiles_of(p, q, b) + p.unit_cost) * tile_places(p, q, b);
+    for (int b = 0; b < n; ++b) t += (long long)(tiles_of(p, q, b) + p.unit_cost) * tile_places(p, q, b).by;
     return t * (p.a.H * p.subs);
 }
 
@@ -120,7 +138,13 @@ __device__ inline Share share_of(const Params &p) {
     const int lane = threadIdx.x & 31, R = p.a.R;
     const int per = (R + 31) / 32, r0 = min(R, lane * per), r1 = min(R, r0 + per);
     long long mine = 0;
-#pragma unroll 4
+    // (little code: it comes from L2 at the start of a launch, and is run once)
+#pragma unroll 1
+    for (int r = r0 + 1; r < r1; ++r) {
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.a.row_start + r + 1));
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.a.len + r));
+    }
+#pragma unroll 1
     for (int r = r0; r < r1; ++r) mine += request_places(p, request_of(p, r, blockIdx.x == 0));
     long long inc = mine;
 #pragma unroll
@@ -136,9 +160,9 @@ __device__ inline Share share_of(const Params &p) {
     }
     // no share is smaller than a tile, so every CTA between a unit's first and last one
     // has a tile of it
-    const unsigned t = (unsigned)total, c = blockIdx.x, ctas = min(gridDim.x, max(1u, t / (unsigned)p.large_places));
+    const unsigned t = (unsigned)total, c = blockIdx.x, ctas = min(gridDim.x, (unsigned)max(1, p.large_places.of(t)));
     if (t == 0 || c >= ctas) return s;
-    s.each = t / ctas;
+    s.each = ctas == p.ctas.by ? p.ctas.of(t) : t / ctas;
     s.more = t - s.each * ctas;
     s.lo = c * s.each + min((int)c, s.more);
     s.hi = s.lo + s.each + ((int)c < s.more ? 1 : 0);
@@ -146,7 +170,7 @@ __device__ inline Share share_of(const Params &p) {
     const bool here = begin <= s.lo && s.lo < begin + (int)mine;
     if (here)
         for (; r1 - r0 > 1; ++r) {
-            const int n = (int)request_places(p, request_of(p, r, false));
+            const int n = (int)request_places(p, request_of(p, r));
             if (s.lo < begin + n) break;
             begin += n;
         }
@@ -163,7 +187,8 @@ struct Walk {
     int at;            // next place of the line
     int r, b, h;       // its unit
     int begin;         // the unit's first place
-    int tiles, places; // of the unit: tiles, and places of one
+    int tiles;         // of the unit
+    Div places;        // of one of its tiles
     int blocks;        // of the request
     Request q;
     bool first;
@@ -171,16 +196,16 @@ struct Walk {
     __device__ __forceinline__ Walk(const Params &p_, const Share &s_) : p(p_), s(s_), at(s_.lo), b(0), h(0), first(true) {
         if (s.lo >= s.hi) return;
         r = s.r;
-        q = request_of(p, r, false);
+        q = request_of(p, r);
         blocks = blocks_of(p, q.rows);
         int left = s.lo - s.r_begin;
         for (;; ++b) {
             shape();
-            const int line = (tiles + p.unit_cost) * places * p.a.H * p.subs;
+            const int line = (tiles + p.unit_cost) * places.by * p.a.H * p.subs;
             if (left < line) break;
             left -= line;
         }
-        const int unit = (tiles + p.unit_cost) * places;
+        const int unit = (tiles + p.unit_cost) * places.by;
         h = (unsigned)left / (unsigned)unit;
         begin = s.lo - (left - h * unit);
     }
@@ -192,8 +217,8 @@ struct Walk {
 
     // the unit's first tile at or after a place of the line
     __device__ __forceinline__ int tile_at(int place) const {
-        const int d = place - (begin + p.unit_cost * places);
-        return d <= 0 ? 0 : min((unsigned)tiles, (unsigned)(d + places - 1) / (unsigned)places);
+        const int d = place - (begin + p.unit_cost * (int)places.by);
+        return d <= 0 ? 0 : min(tiles, places.of(d + (int)places.by - 1));
     }
 
     __device__ __forceinline__ bool next(Piece &out) {
@@ -224,7 +249,7 @@ struct Walk {
 
     // the unit is done: the next head, block or request, if its places begin in the share
     __device__ __forceinline__ void advance() {
-        at = begin + (p.unit_cost + tiles) * places;
+        at = begin + (p.unit_cost + tiles) * (int)places.by;
         if (at >= s.hi) return;
         begin = at;
         if (++h < p.a.H * p.subs) return;
@@ -232,7 +257,7 @@ struct Walk {
         if (++b == blocks) {
             b = 0;
             do {
-                q = request_of(p, ++r, false);
+                q = request_of(p, ++r);
             } while (q.rows == 0);
             blocks = blocks_of(p, q.rows);
         }
@@ -242,7 +267,7 @@ struct Walk {
     // what the second launch needs of a piece that starts a unit and does not end it
     // (the last one of its share: the walk still stands at its unit)
     __device__ __forceinline__ Join join_of(const Piece &x) const {
-        const unsigned last = begin + (p.unit_cost + x.tiles - 1) * places;
+        const unsigned last = begin + (p.unit_cost + x.tiles - 1) * (int)places.by;
         const unsigned big = (unsigned)s.more * (s.each + 1);
         const unsigned c = last < big ? last / (unsigned)(s.each + 1) : s.more + (last - big) / (unsigned)s.each;
         const int sub = p.subs == 1 ? 0 : x.head % p.subs, h0 = p.subs == 1 ? x.head : x.head / p.subs;

@@ -74,24 +74,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_f32(const __grid_c
         const int heads = min(p.heads, (h + 1) * p.G - head0);
         const int32_t *table = a.table + (size_t)x.r * a.max_pages;
         __syncthreads();  // the last piece's queries and sums are read
-        for (int i = tid; i < kLines * D; i += kThreads) {
-            const int l = i / D, d = i - l * D, jj = l / p.heads, gl = l - jj * p.heads;
-            float v = 0.f;
-            if (jj < x.n && gl < heads)
-                v = static_cast<const float *>(a.q)[(x.row0 + x.first + jj) * a.q_row + (head0 + gl) * a.q_head + d];
-            sq[l * QS + d] = v;
-        }
-        __syncthreads();
-
         // this warp's tokens of tile t into stage `st`; beyond the unit's tokens zeros
-        auto page_of = [&](int t) { return table[min((t << kTileLog2) + warp * kTokens + (lane & 7), x.tokens - 1) / a.page]; };
+        auto token_of = [&](int t) { return min((t << kTileLog2) + warp * kTokens + (lane & 7), x.tokens - 1); };
+        auto page_of = [&](int t) { return table[p.page.of(token_of(t))]; };
         auto load = [&](int t, int st, int pg) {
             const int tok0 = (t << kTileLog2) + warp * kTokens;
             if (pg < 0 || pg >= a.n_pages) {
                 set_err(a.err, DSPARK_ERR_RANGE);
                 pg = 0;
             }
-            const int in_page = min(tok0 + (lane & 7), x.tokens - 1) % a.page;
+            const int tok = token_of(t), in_page = tok - p.page.of(tok) * a.page;
             const size_t row = (((size_t)pg * a.H + h) * a.page + in_page) * D;  // of token lane & 7
             float *k = own + st * stage_floats(D), *v = k + kTokens * QS;
 #pragma unroll 1
@@ -127,6 +119,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_f32(const __grid_c
         };
 #pragma unroll 1
         for (int i = 0; i < kStages - 1; ++i) load_next(x.t0 + i);
+        // the queries while the first tiles are on their way
+        for (int i = tid; i < kLines * D; i += kThreads) {
+            const int l = i / D, d = i - l * D, jj = l / p.heads, gl = l - jj * p.heads;
+            float v = 0.f;
+            if (jj < x.n && gl < heads)
+                v = static_cast<const float *>(a.q)[(x.row0 + x.first + jj) * a.q_row + (head0 + gl) * a.q_head + d];
+            sq[l * QS + d] = v;
+        }
+        __syncthreads();
+
         for (int t = x.t0; t < x.t1; ++t, st = st + 1 == kStages ? 0 : st + 1) {
             load_next(t + kStages - 1);
             tc::cp_async_wait<kStages - 1>();

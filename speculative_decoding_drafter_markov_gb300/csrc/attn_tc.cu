@@ -114,7 +114,7 @@ struct Queue {
     uint32_t n;
     __device__ __forceinline__ bool read_one(const Waiter &w, Piece &x) {
         const int i = n % kQueue;
-        if (!w.one(&full[i], (n / kQueue) & 1u)) return false;
+        if (n > 0 && !w.one(&full[i], (n / kQueue) & 1u)) return false;  // the first is there
         x = *reinterpret_cast<const Piece *>(reinterpret_cast<const char *>(items) + 64 * i);
         tc::mbar_arrive(&empty[i]);
         ++n;
@@ -122,7 +122,7 @@ struct Queue {
     }
     __device__ __forceinline__ bool read_warp(const Waiter &w, Piece &x) {
         const int i = n % kQueue;
-        if (!w.warp(&full[i], (n / kQueue) & 1u)) return false;
+        if (n > 0 && !w.warp(&full[i], (n / kQueue) & 1u)) return false;
         x = *reinterpret_cast<const Piece *>(reinterpret_cast<const char *>(items) + 64 * i);
         __syncwarp();
         if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&empty[i]);
@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    Piece x;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tc::smem_u32(smem) & 1023u) {  // the swizzled tiles need it; the launch gives it
         after_predecessor();
@@ -238,35 +239,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::prefetch_tmap(&tmV);
     }
     after_predecessor();  // nothing of the inputs or the workspace was touched so far
-    Share share{};
-    if (warp == 11) {
-        share = share_of(p);
-        if (lane == 0) p.join[blockIdx.x].pieces = 0;
+    // the table on its way to L2, where it is small, while the CTAs find their shares
+    if (warp == 10 && a.R * (long long)a.max_pages <= 32ll * 32 * gridDim.x) {
+        const int line = 32 * (blockIdx.x * 32 + lane);
+        if (line < a.R * a.max_pages) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.table + line));
     }
-    __syncthreads();
-    tc::tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
     const Waiter wait{abort_flag, a.err};
-    Queue queue{pieces, queue_full, queue_empty, 0};
-    uint32_t next = 0, mine = 0;  // copy warps: the slot after the last copy; bit k: slot next - 1 - k was this warp's
-    Piece x;
-
     if (warp == 11) {
         // ------------------------------------------------------------ the walk
-        if (lane == 0) {
-            Walk walk(p, share);
-            for (uint32_t n = 0;; ++n) {
-                const bool more = walk.next(x);
-                if (!more) x.r = -1;
-                const int i = n % kQueue;
-                if (!wait.one(&queue_empty[i], ((n / kQueue) & 1u) ^ 1u)) break;
-                *reinterpret_cast<Piece *>(reinterpret_cast<char *>(pieces) + 64 * i) = x;
+        // The first piece is handed out by the CTA's barrier, the others by the queue.
+        const Share share = share_of(p);
+        Walk walk(p, share);
+        if (lane == 0) p.join[blockIdx.x].pieces = 0;
+        bool more = true;
+        for (uint32_t n = 0; more; ++n) {
+            more = walk.next(x);
+            if (!more) x.r = -1;
+            const int i = n % kQueue;
+            if (n > 0 && !wait.warp(&queue_empty[i], ((n / kQueue) & 1u) ^ 1u)) break;
+            if (lane == 0) *reinterpret_cast<Piece *>(reinterpret_cast<char *>(pieces) + 64 * i) = x;
+            if (n == 0) __syncthreads();
+            if (lane == 0) {
                 tc::mbar_arrive(&queue_full[i]);
-                if (!more) break;
-                if (x.t0 == 0 && x.t1 < x.tiles) p.join[blockIdx.x] = walk.join_of(x);
+                if (more && x.t0 == 0 && x.t1 < x.tiles) p.join[blockIdx.x] = walk.join_of(x);
             }
         }
-        __syncwarp();
+    } else {
+        __syncthreads();
+    }
+    tc::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    Queue queue{pieces, queue_full, queue_empty, 0};
+    uint32_t next = 0, mine = 0;  // copy warps: the slot after the last copy; bit k: slot next - 1 - k was this warp's
+
+    if (warp == 11) {
+        // the walk is done
     } else if (warp == 8 || warp == 10) {
         // ------------------------------------------------------------ keys; values
         const bool values = warp == 10;
@@ -279,7 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n = x.t1 - x.t0;
             const int32_t *table = a.table + (size_t)x.r * a.max_pages;
             const int last_tok = x.tokens - 1;
-            auto page_at = [&](int t) { return table[min(t * kTile + bx * tp.box, last_tok) / a.page]; };
+            int in_table = 0;  // of the lane's box
+            auto page_at = [&](int t) { return table[in_table = p.page.of(min(t * kTile + bx * tp.box, last_tok))]; };
             int pg = page_at(x.t0);
             bool ok = true;
             for (int t = 0; t < n; ++t) {
@@ -302,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pg = 0;
                     }
                     tc::tma_load_3d(smem + C::kOffRing + slot * C::kSlot + col * C::kBlock + bx * tp.box * 128, map,
-                                    &full[slot], 64 * col, tok % a.page, pg * a.H + x.head);
+                                    &full[slot], 64 * col, tok - in_table * a.page, pg * a.H + x.head);
                 }
                 __syncwarp();
                 if (t + 1 < n) pg = page_at(x.t0 + t + 1);
@@ -752,8 +760,10 @@ cudaError_t launch_tc(Params p, int grid, cudaStream_t s) {
     tp.inv_group = (65536 + p.G - 1) / p.G;
     p.tile_log2 = kTileLog2;
     p.small_rows = tp.op_rows;
-    p.small_places = kTilePlaces;
-    p.large_places = p.block_rows > tp.op_rows ? kDualPlaces : kTilePlaces;
+    p.small_places = div_by(kTilePlaces);
+    p.large_places = div_by(p.block_rows > tp.op_rows ? kDualPlaces : kTilePlaces);
+    p.page = div_by(a.page);
+    p.ctas = div_by(grid);
     p.unit_cost = kUnitCost;
     tp.p = p;
     tp.box = a.page & -a.page;
