@@ -169,6 +169,7 @@ __global__ void __launch_bounds__(kRulesThreads, sizeof(Word) <= sizeof(T) ? 4 :
     const bool in_place = a.T == a.out;
     auto grammar = [&](int row) -> const uint32_t * {
         const int m = a.allow ? a.allow_row[row] : -1;
+        if (tid == 0 && m >= a.n_allow) set_err(a.err, DSPARK_ERR_RANGE);
         return m >= 0 && m < a.n_allow ? a.allow + (size_t)m * words : nullptr;
     };
     constexpr int E = 16 / (int)sizeof(T);
@@ -188,7 +189,6 @@ __global__ void __launch_bounds__(kRulesThreads, sizeof(Word) <= sizeof(T) ? 4 :
         vb = va + (hi - va) / E * E;
     };
     auto copy_row = [&](int row) {
-        if (tid == 0 && a.allow && a.allow_row[row] >= a.n_allow) set_err(a.err, DSPARK_ERR_RANGE);
         const uint32_t *allow = grammar(row);
         const T *src = static_cast<const T *>(a.T) + (size_t)row * a.V;
         T *dst = static_cast<T *>(a.out) + (size_t)row * a.V;
@@ -432,7 +432,6 @@ __global__ void __launch_bounds__(kRulesThreads, sizeof(Word) <= sizeof(T) ? 4 :
         const int b = (j - j0) & 1;
         uint32_t ok_next[kMine];
         const uint32_t *allow_next = j + 1 < j1 ? grammar_bits(j + 1, ok_next) : nullptr;
-        if (tid == 0 && a.allow && a.allow_row[row0 + j] >= a.n_allow) set_err(a.err, DSPARK_ERR_RANGE);
         const T *src = static_cast<const T *>(a.T) + (size_t)(row0 + j) * a.V;
         T *dst = static_cast<T *>(a.out) + (size_t)(row0 + j) * a.V;
         int va, vb;
@@ -470,14 +469,16 @@ __global__ void __launch_bounds__(kRulesThreads, sizeof(Word) <= sizeof(T) ? 4 :
 
 template <typename T, typename Word>
 cudaError_t launch_as(const dspark_logit_rules_args &a, cudaStream_t s) {
-    // Slices as large as leave every SM three CTAs; where requests are few the
-    // rows are spread too, at the price of counting the text for each run.
-    const long long want = 3ll * sm_count();
+    // The four CTAs that an SM holds: where requests are few their rows are spread, at the
+    // price of counting the text for each run of rows; the slices are made smaller only
+    // where even a CTA for every row leaves SMs empty.  (4 requests of up to 9 rows, V =
+    // 129280, texts of up to 8192: 11.7 us, with small slices first 19.5; 16 requests: 18.7
+    // and 32; up to 17 rows, texts of up to 1000, 4 requests: 9.4 and 25.)
+    const long long want = 4ll * sm_count(), per = (a.N + a.R - 1) / a.R;
     int slice = kSliceBytes / (int)sizeof(T);
-    while (slice > 1024 && (long long)a.R * ((a.V + slice - 1) / slice) < want) slice /= 2;
+    while (slice > 1024 && a.R * per * ((a.V + slice - 1) / slice) < sm_count()) slice /= 2;
     const int slices = (a.V + slice - 1) / slice;
-    const long long per = (a.N + a.R - 1) / a.R;
-    long long runs = want / ((long long)slices * a.R);
+    long long runs = (want + (long long)slices * a.R - 1) / ((long long)slices * a.R);
     if (runs > per) runs = per;
     if (runs < 1) runs = 1;
     const dim3 grid(slices, a.R, (unsigned)runs);
