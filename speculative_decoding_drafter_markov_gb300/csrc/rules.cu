@@ -34,7 +34,10 @@ namespace {
 // through each other's shared memory, moved in step and took 3 / 13 / 35 us more than
 // each counting alone.)
 constexpr int kRulesThreads = 256;
-constexpr int kBiasList = 256;   // bias entries of a slice kept in shared memory
+constexpr int kBiasList = 256;   // bias entries of a slice kept in shared memory,
+constexpr int kDraftList = 128;  // drafted tokens too
+constexpr int kSearch = 8;       // entries of both up to which they are searched for every row
+constexpr int kMarked = 24;      // marked entries of a warp prepared for all rows
 constexpr int kWarps = kRulesThreads / 32;
 constexpr int kPart = 2048;      // bytes of a row that a warp stages: its part of a slice
 constexpr int kSliceBytes = kPart * kWarps;
@@ -71,24 +74,53 @@ struct Entry<uint32_t> {
 };
 constexpr int kShortText = Entry<uint16_t>::kCount;
 
-struct Bias {
-    const int *id;      // the slice's entries in shared memory, in their order,
-    const float *val;
-    int n;              // or, when they are more than fit there, all of the
-};                      // request's entries in global memory
+// What a marked entry looks through: the slice's bias entries in their order and its
+// drafted tokens, in shared memory; or, when they are more than fit there, all of the
+// request's in global memory.
+struct Marks {
+    const int *id;
+    const float *val;   // biases
+    const int *at;      // drafts: the row, or NULL: the place in the list is the row
+    int n;
+};
+
+// The marked entries of a warp.  Where a request's rows fit 64 bits and an entry has one
+// bias at most, bit i of `where` says that it is the token of row i (i > 0); else bit 0 is
+// set, and it is searched for in every row.
+template <typename Listed>
+struct Marked {
+    uint64_t where[kWarps][kMarked];
+    Listed entry[kWarps][kMarked];
+    float bias[kWarps][kMarked];
+};
 
 struct RowRules {
     float rep, inv_rep, freq, pres;
 };
 
 // c: occurrences in the output and on the row's path
-__device__ __forceinline__ float apply(float z, uint32_t c, bool prompt, bool marked, int v, const RowRules &k, const Bias &b) {
+// c: occurrences in the output and on the row's path
+__device__ __forceinline__ float penalised(float z, uint32_t c, bool prompt, const RowRules &k) {
     if (prompt || c) z *= z > 0.f ? k.inv_rep : k.rep;
     z = fmaf(-k.freq, (float)c, z);
     if (c) z -= k.pres;
-    if (marked)
-        for (int i = 0; i < b.n; ++i)
-            if (b.id[i] == v) z += b.val[i];
+    return z;
+}
+
+// a marked entry by search: how often it was drafted on the path of row j (mine: its
+// mask words, NULL: a chain), and its biases
+__device__ __forceinline__ float searched(float z, uint32_t c, bool prompt, int v, const RowRules k, const Marks bias, const Marks draft,
+                                       const uint64_t *mine, int j) {
+#pragma unroll 1
+    for (int i = 0; i < draft.n; ++i) {
+        if (draft.id[i] != v) continue;
+        const int at = draft.at ? draft.at[i] : i;
+        if (at > 0 && (mine ? (mine[at >> 6] >> (at & 63)) & 1 : at <= j)) ++c;
+    }
+    z = penalised(z, c, prompt, k);
+#pragma unroll 1
+    for (int i = 0; i < bias.n; ++i)
+        if (bias.id[i] == v) z += bias.val[i];
     return z;
 }
 
@@ -126,7 +158,9 @@ __global__ void __launch_bounds__(kRulesThreads, sizeof(Word) <= sizeof(T) ? 4 :
     __shared__ int abort_word;
     __shared__ int bias_id[kBiasList];
     __shared__ float bias_val[kBiasList];
-    __shared__ int bias_n;
+    __shared__ int bias_n, draft_n;
+    __shared__ int draft_id[kDraftList], draft_at[kDraftList];
+    __shared__ Marked<typename Entry<Word>::Listed> marked;
     __shared__ uint32_t keep[4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     after_predecessor();
@@ -163,7 +197,7 @@ __global__ void __launch_bounds__(kRulesThreads, sizeof(Word) <= sizeof(T) ? 4 :
     k.inv_rep = 1.f / k.rep;
     const bool penal = k.rep != 1.f || k.freq != 0.f || k.pres != 0.f;
     const bool path = penal && a.tok;
-    Bias bias{bias_id, bias_val, 0};
+    Marks bias{bias_id, bias_val, nullptr, 0}, draft{draft_id, nullptr, draft_at, 0};
 
     const int words = (a.V + 31) / 32;
     const bool in_place = a.T == a.out;
@@ -252,7 +286,7 @@ __global__ void __launch_bounds__(kRulesThreads, sizeof(Word) <= sizeof(T) ? 4 :
             if (j0 + 1 < j1) load(j0 + 1);
         }
     }
-    if (tid == 0) abort_word = bias_n = 0;
+    if (tid == 0) abort_word = bias_n = draft_n = 0;
     // the grammar's bits of a row are read a row ahead, the first during the counting
     constexpr int kMine = kPart / 16 / 32;  // a lane's pieces
     auto grammar_bits = [&](int j, uint32_t (&ok)[kMine]) {
@@ -325,7 +359,14 @@ __global__ void __launch_bounds__(kRulesThreads, sizeof(Word) <= sizeof(T) ? 4 :
         for (int at = 1 + tid; at < rows; at += kRulesThreads) {
             const int v = a.tok[row0 + at];
             if ((unsigned)v >= (unsigned)a.V) set_err(a.err, DSPARK_ERR_RANGE);
-            if (v >= v0 && v < v1) W::set(word, v - v0, W::kMark);
+            if (v >= v0 && v < v1) {
+                W::set(word, v - v0, W::kMark);
+                const int i = atomicAdd(&draft_n, 1);
+                if (i < kDraftList) {
+                    draft_id[i] = v;
+                    draft_at[i] = at;
+                }
+            }
         }
     if (b1 > b0 && tid < 32) {  // one warp, so that the list keeps the entries' order
         int found = 0;
@@ -348,13 +389,15 @@ __global__ void __launch_bounds__(kRulesThreads, sizeof(Word) <= sizeof(T) ? 4 :
     }
     __syncthreads();
     bias.n = bias_n;
-    if (bias.n > kBiasList) bias = Bias{a.bias_id + b0, a.bias_val + b0, b1 - b0};
+    if (bias.n > kBiasList) bias = Marks{a.bias_id + b0, a.bias_val + b0, nullptr, b1 - b0};
+    draft.n = draft_n;
+    if (draft.n > kDraftList) draft = Marks{a.tok + row0, nullptr, nullptr, rows};
     // The warp's list of touched entries, over its words: a lane takes `part / 32` of
     // them into registers.  With more entries than fit there the words stay, and are
     // searched for every row.
     constexpr int kPacked = 4 / (int)sizeof(Word);  // words of a register
     constexpr int kLaneWords = kPart / (int)sizeof(T) / 32 / kPacked;
-    const Word *mine = word + warp * part;
+    Word *mine = word + warp * part;
     typename W::Listed *list = reinterpret_cast<typename W::Listed *>(word + warp * part);
     int listed = 0;
     {
@@ -391,6 +434,52 @@ __global__ void __launch_bounds__(kRulesThreads, sizeof(Word) <= sizeof(T) ? 4 :
         }
     }
     const bool by_list = listed <= part / 2;
+    // The marked entries among them get a list of their own, of what they found in the lists
+    // of biases and drafts (the warp looks for an entry together); where they stood is left
+    // as if untouched.
+    int prepared = 0;
+    if (bias.n + draft.n > kSearch) {
+        const int n_all = by_list ? listed : part;
+        for (int i0 = 0; i0 < n_all && prepared < kMarked; i0 += 32) {
+            const int i = i0 + lane;
+            uint32_t w = 0;
+            if (i < n_all) w = by_list ? W::word(list[i]) : (uint32_t)mine[i];
+            const uint32_t who = __ballot_sync(0xffffffffu, (w & W::kMark) != 0);
+            const int at = prepared + __popc(who & ((1u << lane) - 1));
+            if ((w & W::kMark) && at < kMarked) {
+                const int place = by_list ? W::place(list[i]) : i;
+                marked.entry[warp][at] = W::listed(w, place);
+                if (by_list) list[i] = W::listed(0u, place);
+                else mine[i] = 0;
+            }
+            prepared = min(kMarked, prepared + __popc(who));
+        }
+        __syncwarp();
+        for (int e = 0; e < prepared; ++e) {
+            const int v = lo + W::place(marked.entry[warp][e]);
+            uint64_t where = rows > 64;  // bit 0: to be searched for in every row
+            float val = 0.f;
+            int found = 0;
+            for (int i0 = 0; i0 < draft.n; i0 += 32) {
+                const int i = i0 + lane;
+                const bool hit = i < draft.n && draft.id[i] == v;
+                if (hit) where |= 1ull << ((draft.at ? draft.at[i] : i) & 63);
+            }
+            for (int i0 = 0; i0 < bias.n; i0 += 32) {
+                const int i = i0 + lane;
+                const bool hit = i < bias.n && bias.id[i] == v;
+                if (hit) val = bias.val[i];
+                found += __popc(__ballot_sync(0xffffffffu, hit));
+            }
+            const uint32_t lo32 = __reduce_or_sync(0xffffffffu, (uint32_t)where), hi32 = __reduce_or_sync(0xffffffffu, (uint32_t)(where >> 32));
+            const uint32_t bits = __reduce_or_sync(0xffffffffu, __float_as_uint(val));  // of one entry, if there is one
+            if (lane == 0) {
+                marked.where[warp][e] = (uint64_t)hi32 << 32 | lo32 | (found > 1);
+                marked.bias[warp][e] = __uint_as_float(bits);
+            }
+        }
+        __syncwarp();
+    }
     // f(place in the part, word) for the touched entries, a lane each
     auto touched = [&](auto f) {
         if (by_list) {
@@ -403,13 +492,9 @@ __global__ void __launch_bounds__(kRulesThreads, sizeof(Word) <= sizeof(T) ? 4 :
 
     // entry v of row j, whose word is w
     auto value = [&](int j, int v, uint32_t w, float z) {
-        uint32_t c = w & W::kCount;
-        if ((w & W::kMark) && path) {  // perhaps drafted in the request: how often on this row's path
-            const uint64_t *mine = a.mask ? a.mask + (size_t)(row0 + j) * a.W : nullptr;
-            for (int at = 1; at < (mine ? rows : j + 1); ++at)
-                if (a.tok[row0 + at] == v && (!mine || ((mine[at >> 6] >> (at & 63)) & 1))) ++c;
-        }
-        return apply(z, c, w & W::kPrompt, w & W::kMark, v, k, bias);
+        if (w & W::kMark)
+            return searched(z, w & W::kCount, w & W::kPrompt, v, k, bias, draft, a.mask ? a.mask + (size_t)(row0 + j) * a.W : nullptr, j);
+        return penalised(z, w & W::kCount, w & W::kPrompt, k);
     };
     auto scatter = [&](int j, int v, uint32_t w, const uint32_t *allow, const T *src, T *dst) {
         if (!allow || allowed<true>(allow, v, 1)) put(dst + v, value(j, v, w, to_f32(src[v])));
@@ -423,6 +508,11 @@ __global__ void __launch_bounds__(kRulesThreads, sizeof(Word) <= sizeof(T) ? 4 :
             const T *src = static_cast<const T *>(a.T) + (size_t)(row0 + j) * a.V;
             T *dst = static_cast<T *>(a.out) + (size_t)(row0 + j) * a.V;
             touched([&](int i, uint32_t w) { scatter(j, lo + i, w, allow, src, dst); });
+            __syncwarp();
+            if (lane < prepared) {
+                const auto m = marked.entry[warp][lane];
+                scatter(j, lo + W::place(m), W::word(m), allow, src, dst);
+            }
         }
         return;
     }
@@ -449,6 +539,27 @@ __global__ void __launch_bounds__(kRulesThreads, sizeof(Word) <= sizeof(T) ? 4 :
             if (!kAligned && (v < va || v >= vb)) scatter(j, v, w, allow, src, dst);
             else put(row + v, value(j, v, w, to_f32(row[v])));
         });
+        if (prepared > 0) {
+            __syncwarp();
+            if (lane < prepared) {
+                const auto m = marked.entry[warp][lane];
+                const uint32_t w = W::word(m);
+                const int v = lo + W::place(m);
+                const uint64_t where = marked.where[warp][lane];
+                if (!kAligned && (v < va || v >= vb)) {
+                    scatter(j, v, w, allow, src, dst);
+                } else {
+                    float z = to_f32(row[v]);
+                    if (where & 1) {
+                        z = value(j, v, w, z);
+                    } else {
+                        const uint64_t seen = a.mask ? a.mask[(size_t)(row0 + j) * a.W] : j < 63 ? (2ull << j) - 1 : ~0ull;
+                        z = penalised(z, (w & W::kCount) + __popcll(where & seen), w & W::kPrompt, k) + marked.bias[warp][lane];
+                    }
+                    put(row + v, z);
+                }
+            }
+        }
         __syncwarp();
 #pragma unroll
         for (int u = 0; u < kMine; ++u) {
@@ -478,6 +589,8 @@ cudaError_t launch_as(const dspark_logit_rules_args &a, cudaStream_t s) {
     int slice = kSliceBytes / (int)sizeof(T);
     while (slice > 1024 && a.R * per * ((a.V + slice - 1) / slice) < sm_count()) slice /= 2;
     const int slices = (a.V + slice - 1) / slice;
+    // of one size, whole 64 entries for a warp
+    slice = ((a.V + slices - 1) / slices + 64 * kWarps - 1) / (64 * kWarps) * (64 * kWarps);
     long long runs = (want + (long long)slices * a.R - 1) / ((long long)slices * a.R);
     if (runs > per) runs = per;
     if (runs < 1) runs = 1;

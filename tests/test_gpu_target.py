@@ -718,6 +718,21 @@ def test_rules_texts_of_many_tokens(dtype, V):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [512, 1001])
+@pytest.mark.parametrize("most,tree,bias", [(12, True, 60), (9, False, 200), (64, True, 40), (100, True, 30), (200, False, 9), (5, True, 700)])
+def test_rules_many_biases_and_drafts(dtype, V, most, tree, bias):
+    """Biases and drafted tokens all over a small vocabulary, some of them twice; more
+    than a warp prepares, and rows beyond 64 bits."""
+    s = rules_case(3, most, V, dtype, seed=V + most, tree=tree, hist=200, bias=bias)
+    rng = np.random.default_rng(most)
+    s["bias_id"] = rng.integers(0, V, s["bias_start"][-1])
+    s["tok"] = rng.integers(0, V, len(s["tok"]))
+    rules_check(s, dsp.logit_rules(s["T"], ints(s["start"]), **rules_args(s)), rules_expect(s))
+    out = s["T"].clone()
+    rules_check(s, dsp.logit_rules(out, ints(s["start"]), out=out, **rules_args(s)), rules_expect(s))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("hist,shift", [(16383, 0), (16384, 0), (40001, 0), (16381, 3)])
 def test_rules_long_texts(dtype, hist, shift):
     """One token said nearly all the time, next to others; rows of the text that do
