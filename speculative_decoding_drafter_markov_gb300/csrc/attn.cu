@@ -212,12 +212,13 @@ __global__ void __launch_bounds__(kThreads) tree_attention_simt(const __grid_con
 // ---------------------------------------------------------------- join
 // out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over a unit's partials.
 // At most one unit starts in a CTA and ends in a later one, so CTAs (c, ..) join the
-// lines of CTA c's unit: a warp a line, or, where a unit has many pieces (one long
-// cache over the whole GPU), the four warps of a CTA share a line's pieces.  Bound by
-// latency: partials that are still in L2, four under way before the weights are known
+// lines of CTA c's unit: a warp a line, or, where that takes fewer rounds (many pieces
+// and few lines, as of one long cache over the whole GPU), the four warps of a CTA share
+// a line's pieces.  (Always sharing above eight pieces: 434 lines on 4 heads, 5 caches of
+// up to 1312 tokens took 41 us, by rounds 24.)  Bound by latency: partials that are still in L2, four under way before the weights are known
 // (eight take the registers of half of the CTAs: 2 us more for 256 lines).  About 3 us
 // for a few lines, 9 us for 256 lines in each of 16 requests.
-constexpr int kJoinWarps = 4, kJoinMany = 8, kAhead = 4;
+constexpr int kJoinWarps = 4, kAhead = 4;
 
 // four (or, E = 1, one) adjacent floats per lane
 template <int E>
@@ -241,7 +242,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 8) tree_attention_join(const 
     const Join n = p.join[blockIdx.x];
     if (n.pieces == 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.stride;
-    const bool many = n.pieces > kJoinMany;
+    // rounds of kAhead partials, and one for the weights, either way
+    const int y = gridDim.y, turns = (n.lines + y - 1) / y, turns_warp = (n.lines + y * kJoinWarps - 1) / (y * kJoinWarps);
+    const bool many = turns * ((n.pieces + kAhead * kJoinWarps - 1) / (kAhead * kJoinWarps) + 1) <
+                      turns_warp * ((n.pieces + kAhead - 1) / kAhead + 1);
     // partial i: the first one, then the first partials of the CTAs after it
     auto slot = [&](int i, int ln) { return (size_t)(i == 0 ? n.first : 2 * ((int)blockIdx.x + i)) * p.lines + ln; };
     const int step = many ? kJoinWarps : 1;  // pieces of this warp: own, own + step, ..
@@ -364,7 +368,7 @@ cudaError_t launch_join(const Params &p, int grid, cudaStream_t s) {
     // them come up while it runs
     const long long lines = (long long)p.a.max_rows * p.heads;
     unsigned y = (unsigned)(lines < 1 ? 1 : lines < p.lines ? lines : p.lines);
-    if (y > 16) y = 16;
+    if (y > 32) y = 32;
     auto kern = p.stride % 4 == 0 ? (p.stride <= 128 ? tree_attention_join<4, 1> : tree_attention_join<4, 2>)
                                   : (p.stride <= 64 ? tree_attention_join<1, 2> : tree_attention_join<1, 8>);
     return launch_close(kern, dim3(grid, y), 32 * kJoinWarps, 0, s, p);

@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int lines = (dual ? (w ? x.n - tp.op_rows : tp.op_rows) : x.n) * p.G;
             const int steps = dual ? n : (n + 1 - w) >> 1;
             const bool active = 32 * q < lines, live = row < lines;
-            const int jj = row / p.G, j = row_first + jj;
+            const int jj = (row * tp.inv_group) >> 16, j = row_first + jj;  // row / G
             // rows of the cycle before `base_rel` are seen by every line of the unit
             const int base_rel = a.mask ? 0 : x.first + 1;
             const uint32_t *words = a.mask && live ? reinterpret_cast<const uint32_t *>(a.mask + (size_t)(x.row0 + j) * a.W) : nullptr;
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (live && (dual || w == 0)) {
                     if (!whole) p.part_ml[prow0 + row] = make_float2(m, l);
-                    else if (a.lse) a.lse[(size_t)(x.row0 + j) * a.Hq + x.head * p.G + row % p.G] = lse_of(m, l);
+                    else if (a.lse) a.lse[(size_t)(x.row0 + j) * a.Hq + x.head * p.G + row - jj * p.G] = lse_of(m, l);
                 }
             }
             tc::tc_fence_before();
