@@ -16,7 +16,7 @@ namespace {
 // tile are staged in shared memory as fp32 and shared by the lines.  A thread
 // scores one line against four tokens, then each warp adds its four lines'
 // weighted values, the lanes side by side over D.  Bound by its instructions: 64 caches
-// of up to 8192 tokens, 36 lines on each of 8 heads of 128, bf16: 1363 us, against 128 us
+// of up to 8192 tokens, 36 lines on each of 8 heads of 128, bf16: 1363 us, against 127 us
 // on the tensor cores; one row over 2047 tokens 28 against 12.
 constexpr int kLines = kSimtLines, kTileLog2 = 5, kTile = 1 << kTileLog2, kThreads = 128;
 

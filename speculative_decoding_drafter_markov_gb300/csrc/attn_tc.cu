@@ -21,7 +21,7 @@
 // Bound by HBM while lines are few: a tile of D = 128 is 64 KB, 2,900 clocks of an
 // SM's share of the bandwidth, against 1,030 of MMA per operand.  8 heads of 128, bf16:
 // 8 caches of up to 131072 tokens with up to 68 lines take 423 us (6.8 TB/s), 64 of up to
-// 8192 with up to 36 lines 128 us (5.5 TB/s, the rest starts and ends of pieces), one row
+// 8192 with up to 36 lines 127 us (5.5 TB/s, the rest starts and ends of pieces), one row
 // over 2047 tokens 12.5 us (latency).  With many lines by the chain from S through the
 // softmax to P: 8 caches of up to 131072 with up to 256 lines 438 us, 0.87 PFLOP/s.
 // S in half tiles of 64 tokens, to give the softmax its first half earlier, is slower (558
