@@ -464,9 +464,9 @@ DSPARK_API int dspark_cache_store(const dspark_cache_store_args *a, dspark_strea
  * page number outside the cache is reported and the rows that see it are then
  * unspecified.  max_rows, the largest number of rows of a request as far as
  * the host knows, only chooses the tile shape.
- * Statistics and sums are fp32.  bf16 with D a multiple of 8 up to 128 and
- * pages of a multiple of 8 tokens, and q (its strides too), the caches and out
- * 16-byte aligned, runs on the tensor cores (the softmax weights are rounded
+ * Statistics and sums are fp32.  bf16 with D a multiple of 8 up to 128, pages
+ * of a multiple of 8 tokens, a scale that is not negative, and q (its strides
+ * too), the caches and out 16-byte aligned, runs on the tensor cores (the softmax weights are rounded
  * to bf16 for the second product); everything else
  * with D <= DSPARK_ATTN_MAX_D on the CUDA cores in fp32.  With a mask a request
  * has at most DSPARK_ATTN_MAX_TREE rows (W <= 4).  Results do not depend on

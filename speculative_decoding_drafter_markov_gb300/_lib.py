@@ -509,7 +509,8 @@ def page_map(lens, rows, table, held, free, n_free, *, page, N, parents=None, ma
     rows trees; max_rows is then the largest number of rows of a request.
     Returns {"held", "n_free", "row_start", "slot", "pos"} and, for trees,
     "mask" [N, ceil(max_rows / 64)] int64.  The new held and n_free are other
-    tensors than the ones passed in: hand them to the next call."""
+    tensors than the ones passed in: hand them to the next call.  Outputs made here
+    share two allocations, held and n_free apart from the others."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return page_map(lens, rows, table, held, free, n_free, page=page, N=N, parents=parents, max_rows=max_rows,
