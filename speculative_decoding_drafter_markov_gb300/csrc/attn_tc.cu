@@ -12,7 +12,17 @@
 // partials.  The softmax works and hands P over in halves, so that the first half's
 // product runs while the second half is formed.  The maximum m is only moved, and O
 // rescaled in tensor memory, when a half exceeds it by 2^8 (any reference gives
-// the same result; P stays below 2^8 and the fp32 sums far from overflow).
+// the same result; P stays below 2^8 and the fp32 sums far from overflow): the
+// running-maximum softmax of Milakov and Gimelshein (arXiv 1805.02867) with a
+// reference that may lag behind.
+//
+// P is rounded to one bf16 term (the MMA wants A in the type of B, the values): against
+// 64 bits the outputs are off by 0.0023 of their size (of 0.0017 the rounding
+// of the output alone).  A second term, the rest of P in the half of S's columns that the
+// first leaves free, brings that to 0.0017, but doubles the second product and a third of
+// the softmax, both in the chain that bounds a tile: 64 caches of up to 8192 tokens 146
+// instead of 126 us, 16 of up to 16384 with trees of up to 64 rows 126 instead of 98, 8 of
+// up to 131072 with up to 256 lines 587 instead of 433, and with 68 lines 433 instead of 420.
 //
 // Warps 0-7 softmax, 8 and 10 copy keys and values by TMA, a box per page piece,
 // through one ring of slots in the order of their use, 9 copies Q and issues the
