@@ -15,6 +15,7 @@
 // the weights); a second launch joins the partials of each unit.
 #pragma once
 
+#include "attn_cut.h"
 #include "common.cuh"
 #include "target.h"
 

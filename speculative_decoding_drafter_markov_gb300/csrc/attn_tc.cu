@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int32_t *table = a.table + (size_t)x.r * a.max_pages;
             const int last_tok = x.tokens - 1;
             int in_table = 0;  // of the lane's box
-            auto page_at = [&](int t) { return table[in_table = p.page.of(min(t * kTile + bx * tp.box, last_tok))]; };
+            auto page_at = [&](int t) { return table[in_table = p.page.of(lookup_token(t, kTileLog2, bx, tp.box, last_tok))]; };
             int pg = page_at(x.t0);
             bool ok = true;
             for (int t = 0; t < n; ++t) {
