@@ -16,7 +16,8 @@
  * - All tensor pointers are DEVICE pointers owned by the caller; row-major,
  *   contiguous, with the shapes given per field.  The library allocates no
  *   device memory: scratch comes from the caller through `ws`, whose size the
- *   matching *_workspace_size() function returns (256-byte aligned pointer).
+ *   matching *_workspace_size() function returns (256-byte aligned pointer;
+ *   one that is not even 16-byte aligned is refused).
  * - Every call only enqueues work on `stream` (a cudaStream_t) and returns
  *   without synchronising.  Calls on one stream run in order.
  * - dtype: DSPARK_F32 or DSPARK_BF16 applies to U, h, W1, W2t, W and T.

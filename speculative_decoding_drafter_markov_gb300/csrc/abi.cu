@@ -41,6 +41,14 @@ constexpr int kMaxRank = 512;  // shared-memory bound of the CUDA-core draft ker
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// A workspace's parts lie 256 bytes apart from its start on; the kernels read and write
+// them by up to 16 bytes at a time, and an address between would be a fault on the GPU.
+int check_ws(const void *ws) {
+    if (!ws) return fail(DSPARK_ERR_INVAL, "null workspace");
+    if (!aligned16(ws)) return fail(DSPARK_ERR_INVAL, "the workspace must be aligned");
+    return DSPARK_OK;
+}
+
 int check_draft(const dspark_draft_args *a) {
     if (!a) return fail(DSPARK_ERR_INVAL, "null argument struct");
     if (a->R < 1 || a->gamma < 1 || a->V < 1 || a->r < 1 || a->d < 0)
@@ -199,7 +207,7 @@ DSPARK_API size_t dspark_draft_markov_workspace_size(const dspark_draft_args *a)
 DSPARK_API int dspark_draft_markov(const dspark_draft_args *a, void *ws, dspark_stream_t stream) {
     int rc = check_draft(a);
     if (rc != DSPARK_OK) return rc;
-    if (!ws) return fail(DSPARK_ERR_INVAL, "null workspace");
+    if ((rc = check_ws(ws)) != DSPARK_OK) return rc;
     rc = run_draft_loop(a, nullptr, ws, reinterpret_cast<cudaStream_t>(stream), nullptr, 1, a->gamma);
     return rc == DSPARK_OK ? ok() : rc;
 }
@@ -209,7 +217,7 @@ DSPARK_API int dspark_draft_markov_step(const dspark_draft_args *a, int32_t k, v
     int rc = check_draft(a);
     if (rc != DSPARK_OK) return rc;
     if (k < 1 || k > a->gamma) return fail(DSPARK_ERR_INVAL, "step k=%d outside 1..%d", k, a->gamma);
-    if (!ws) return fail(DSPARK_ERR_INVAL, "null workspace");
+    if ((rc = check_ws(ws)) != DSPARK_OK) return rc;
     rc = run_draft_loop(a, nullptr, ws, reinterpret_cast<cudaStream_t>(stream), nullptr, k, k);
     return rc == DSPARK_OK ? ok() : rc;
 }
@@ -306,7 +314,7 @@ DSPARK_API int dspark_draft_rnn(const dspark_rnn_args *a, void *ws, dspark_strea
     int rc = check_draft(&a->base);
     if (rc != DSPARK_OK) return rc;
     if (!a->W || !a->A) return fail(DSPARK_ERR_INVAL, "null RNN tensor pointer");
-    if (!ws) return fail(DSPARK_ERR_INVAL, "null workspace");
+    if ((rc = check_ws(ws)) != DSPARK_OK) return rc;
     const dspark_draft_args &b = a->base;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const size_t state_bytes = sizeof(float) * (size_t)b.R * b.r;
@@ -407,7 +415,7 @@ DSPARK_API size_t dspark_verify_workspace_size(const dspark_verify_args *a) {
 DSPARK_API int dspark_verify(const dspark_verify_args *a, void *ws, dspark_stream_t stream) {
     int rc = check_verify(a);
     if (rc != DSPARK_OK) return rc;
-    if (!ws) return fail(DSPARK_ERR_INVAL, "null workspace");
+    if ((rc = check_ws(ws)) != DSPARK_OK) return rc;
     const dspark::VerifyWs w = dspark::verify_ws_carve(ws, a->R, a->gamma, a->V, a->N);
     cudaError_t e = dspark::launch_verify(*a, w, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "verify");
@@ -427,8 +435,10 @@ DSPARK_API int dspark_sts_fit(const dspark_sts_args *a, void *ws, dspark_stream_
     if (a->gamma > dspark::kStsMaxGamma || a->n_bins > dspark::kStsMaxBins)
         return fail(DSPARK_ERR_UNSUPPORTED, "gamma=%d or n_bins=%d above %d", a->gamma, a->n_bins,
                     dspark::kStsMaxGamma);
-    if (!a->logit || !a->n_accept || !a->grid || !a->T || !a->ece || !ws)
+    if (!a->logit || !a->n_accept || !a->grid || !a->T || !a->ece)
         return fail(DSPARK_ERR_INVAL, "null pointer");
+    int rc = check_ws(ws);
+    if (rc != DSPARK_OK) return rc;
     dspark::StsFit f{};
     f.M = a->M; f.gamma = a->gamma; f.G = a->G; f.n_bins = a->n_bins;
     f.logit = a->logit; f.n_accept = a->n_accept; f.grid = a->grid;
@@ -524,7 +534,7 @@ DSPARK_API int dspark_tree_attention(const dspark_tree_attention_args *a, void *
     if (a->N == 0) return ok();
     if (!a->q || !a->k_cache || !a->v_cache || !a->table || !a->len || !a->row_start || !a->out)
         return fail(DSPARK_ERR_INVAL, "null tensor pointer");
-    if (!ws) return fail(DSPARK_ERR_INVAL, "null workspace");
+    if ((rc = check_ws(ws)) != DSPARK_OK) return rc;
     cudaError_t e = dspark::launch_tree_attention(*a, ws, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ok() : cuda_fail(e, "tree attention");
 }
