@@ -388,6 +388,7 @@ size_t tree_attention_ws_bytes(const dspark_tree_attention_args &a) {
 
 cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws, cudaStream_t s) {
     using namespace attn;
+    if (sm_count() < 1) return cudaErrorNoDevice;  // the work is cut by the SMs there are
     Params p{};
     p.a = a;
     p.G = a.Hq / a.H;

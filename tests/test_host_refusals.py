@@ -1,4 +1,5 @@
-"""A workspace that the kernels could not address is refused on the host."""
+"""A workspace that the kernels could not address, and a machine without a GPU, are
+errors that the host returns."""
 import ctypes
 
 import pytest
@@ -57,3 +58,19 @@ def test_views_off_the_boundary_are_refused(lib, dtype):
             call(s, ws=ws[off:])
     same, err = call(s, ws=ws[16:])
     assert torch.equal(same["out"], out["out"])
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="pointers that are not memory: for a machine without a GPU")
+def test_no_gpu_is_an_error_code(lib):
+    """Arguments that pass every check, on a machine without a GPU."""
+    L = lib.load()
+    for name, a, more in calls(lib):
+        assert getattr(L, name)(ctypes.byref(a), *more, SOME, None) == lib.ERR_CUDA, name
+    for name, a in (("dspark_page_map", filled(lib.PageMapArgs, R=4, page=16, n_pages=100, max_pages=10, N=20, n_parents=20, W=1,
+                                               held_out=ctypes.c_void_p(512), n_free_out=ctypes.c_void_p(768))),
+                    ("dspark_cache_store", filled(lib.CacheStoreArgs, N=4, H=2, D=64, page=16, n_pages=10, dtype=1)),
+                    ("dspark_logit_rules", filled(lib.LogitRulesArgs, R=4, N=8, V=100, dtype=1, max_hist=5, n_bias=3, n_allow=2, W=1))):
+        assert getattr(L, name)(ctypes.byref(a), None) == lib.ERR_CUDA, name
+    for dtype, D in ((0, 64), (1, 200), (0, 3)):  # the other two kernels of the attention
+        a = filled(lib.TreeAttentionArgs, R=4, N=8, Hq=8, H=2, D=D, page=16, n_pages=10, max_pages=4, dtype=dtype, W=1, max_rows=4, scale=1.0)
+        assert L.dspark_tree_attention(ctypes.byref(a), SOME, None) == lib.ERR_CUDA, (dtype, D)
