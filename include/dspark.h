@@ -463,7 +463,9 @@ DSPARK_API int dspark_cache_store(const dspark_cache_store_args *a, dspark_strea
  * A request whose sizes are negative, whose rows pass N (or 64 W with a mask)
  * or whose tokens pass the table is reported and its rows are not written; a
  * page number outside the cache is reported and the rows that see it are then
- * unspecified.  max_rows, the largest number of rows of a request as far as
+ * unspecified.  A call in which each SM would walk more than about 2^34 tokens,
+ * minutes of work, is reported as DSPARK_ERR_UNSUPPORTED and no row is written.
+ * max_rows, the largest number of rows of a request as far as
  * the host knows, only chooses the tile shape.
  * Statistics and sums are fp32.  bf16 with D a multiple of 8 up to 128, pages
  * of a multiple of 8 tokens, a scale that is not negative, and q (its strides

@@ -391,7 +391,9 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws,
     if (sm_count() < 1) return cudaErrorNoDevice;  // the work is cut by the SMs there are
     Params p{};
     p.a = a;
+    p.H = a.H;
     p.G = a.Hq / a.H;
+    p.masked = a.mask != nullptr;
     p.scale_log2 = a.scale * kLog2e;
     if (tc_supported(a)) {
         p.heads = p.G;

@@ -21,6 +21,7 @@ import numpy as np
 import pytest
 import torch
 
+import speculative_decoding_drafter_markov_gb300 as dsp
 from test_gpu_target import call, expect, make
 
 pytestmark = pytest.mark.gpu
@@ -93,3 +94,30 @@ def test_every_tile_of_values_counts(dtype, G, D, lens, rows, tree):
         if n_ctx >= 256:
             rows_r = slice(start[r], start[r + 1])
             assert (np.abs(wrong - want)[rows_r] > 2 * tol[rows_r]).mean() > 0.5
+
+
+def test_tokens_to_the_end_of_32_bits():
+    """43 caches whose 2^31 - 256 tokens are 47 times the same page: the last token that
+    a table may name, and a line of more than 2^31 places.  Keys of zero, values of 0
+    but for a few of 1 in each column: sums of whole numbers below 2^24, and means.
+    Partials of the sums and weights are joined in fp32, four at most: 8 2^-24."""
+    R, page, pages, D = 43, 45691136, 47, 8
+    kc, vc = (torch.zeros((1, 1, page, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    rng = np.random.default_rng(1)
+    count = [1, 100, 5000, 70000, 300000, 17, 2, 0]
+    for d, n in enumerate(count):  # the first token of the page, some others and the last
+        at = np.unique(np.concatenate([[0] * (n > 0), rng.integers(1, page - 1, 2 * n)])).astype(np.int64)[:n]
+        at[1:][-1:] = page - 1
+        vc[0, 0, torch.from_numpy(at).cuda(), d] = 1
+    tokens = page * pages
+    assert tokens == 0x7fffff00
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    err = ints([0])
+    q = torch.ones((R, 1, D), dtype=torch.bfloat16, device="cuda")
+    got = dsp.tree_attention(q, kc, vc, torch.zeros((R, pages), dtype=torch.int32, device="cuda"), ints([tokens - 1] * R),
+                             ints(list(range(R + 1))), err=err)
+    assert int(err) == 0
+    want = torch.tensor(count, dtype=torch.float64, device="cuda") / page
+    assert ((got["out"].double() - want).abs() <= (2.0 ** -8 + 8 * 2.0 ** -24) * want).all()
+    lse = np.log(float(tokens))
+    assert ((got["lse"].double() - lse).abs() <= 1e-6 * (1 + lse)).all()
