@@ -404,7 +404,10 @@ DSPARK_API int dspark_train_losses(const dspark_train_loss_args *a, dspark_strea
  * pages, more than max_pages pages, N or n_parents rows or 64 W rows of a
  * request (with `parents`), or a negative size is reported, row_start becomes
  * 0, every slot -1, held_out = held, n_free_out = n_free, and the table and
- * the stack stay as they are.  held_out and n_free_out must not be held and
+ * the stack stay as they are.  A page number outside the cache, among a
+ * request's held entries or on the stack, is reported by the call that stores
+ * rows into it (their slots are -1), gives it back or takes it; it stays what it
+ * is and moves like any other.  held_out and n_free_out must not be held and
  * n_free: what the call reads it leaves (but for the table entries and the
  * stack entries that it fills), so a call may be repeated.  R at most
  * DSPARK_MAP_MAX_R, n_pages * page below 2^31.  One launch, no workspace. */

@@ -153,16 +153,27 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const dspark_page
     auto page_of = [&](int k) {  // the k-th page taken
         return k < m ? given(k) : a.free_list[before - 1 - (k - m)];
     };
+    // whoever moves a page, or stores into it, reports one that the cache has not
+    auto is_page = [&](int pg) {
+        const bool ok = (unsigned)pg < (unsigned)a.n_pages;
+        if (!ok) set_err(a.err, DSPARK_ERR_RANGE);
+        return ok;
+    };
 
     if (first == 0) *a.n_free_out = after - taken;
     for (int r = first; r <= R; r += step) {
         a.row_start[r] = s.rows[r];
         if (r < R) a.held_out[r] = (int)need_of(a, page, r);
     }
-    for (int k = first; k < m; k += step) a.free_list[after - 1 - k] = given(k);
+    for (int k = first; k < m; k += step) {
+        const int pg = given(k);
+        is_page(pg);
+        a.free_list[after - 1 - k] = pg;
+    }
     for (int k = first; k < taken; k += step) {
-        const int r = holder(s.more, R, k);
-        a.table[(size_t)r * a.max_pages + a.held[r] + (k - s.more[r])] = page_of(k);
+        const int r = holder(s.more, R, k), pg = page_of(k);
+        is_page(pg);
+        a.table[(size_t)r * a.max_pages + a.held[r] + (k - s.more[r])] = pg;
     }
     for (int i = first; i < a.N; i += step) {
         int slot = -1, pos = 0;
@@ -170,7 +181,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const dspark_page
             const int r = holder(s.rows, R, i), start = s.rows[r], j = i - start;
             const int t = a.len[r] + j, pi = (int)page.of(t), held = a.held[r];
             const int pg = pi < held ? a.table[(size_t)r * a.max_pages + pi] : page_of(s.more[r] + pi - held);
-            slot = pg * a.page + (t - pi * a.page);
+            if (is_page(pg)) slot = pg * a.page + (t - pi * a.page);
             pos = t;
             if (a.parents) {
                 // walk up: a parent is an earlier row, so the walk ends
