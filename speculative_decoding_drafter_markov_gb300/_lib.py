@@ -487,13 +487,14 @@ _bind = None
 
 
 def _target():
-    """The module of the target-pass calls, loaded beside the library."""
+    """The module of the target-pass calls, loaded beside the library (and built first
+    if needed)."""
     global _bind
     if _bind is None:
         load()
         with _lock:
             if _bind is None:
-                loader = importlib.machinery.ExtensionFileLoader("_dspark_bind", _build.BIND)
+                loader = importlib.machinery.ExtensionFileLoader("_dspark_bind", _build.build_bind())
                 module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_dspark_bind", loader))
                 loader.exec_module(module)
                 module.set_errors(DSparkError, torch.OutOfMemoryError)

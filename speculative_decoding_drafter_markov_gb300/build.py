@@ -4,7 +4,8 @@ Each translation unit compiles in parallel with nvcc; the objects link into
 one shared library whose exported symbols are exactly the C ABI of
 include/dspark.h.  Beside it g++ compiles the Python calls of the target-pass
 operators (bind.cpp, against the installed PyTorch's headers) into a module that
-links to the library.  Outputs go to speculative_decoding_drafter_markov_gb300/_build/.
+links to the library; the library does not need the module.  Outputs go to
+speculative_decoding_drafter_markov_gb300/_build/.
 """
 from __future__ import annotations
 
@@ -36,21 +37,26 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found: the DSpark CUDA library cannot be built")
 
 
-def _deps():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(ROOT, "include", "dspark.h"))
-    return files
+HEADER = os.path.join(ROOT, "include", "dspark.h")
+BIND_SOURCE = os.path.join(CSRC, "bind.cpp")
 
 
-def _build_bind(obj: str) -> None:
-    """Compile bind.cpp; the module is linked once the library is there."""
+def _current(out, deps) -> bool:
+    return os.path.exists(out) and os.path.getmtime(out) >= max(os.path.getmtime(f) for f in deps)
+
+
+def _library_deps():
+    return [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != "bind.cpp"] + [HEADER]
+
+
+def _compile_bind(obj: str) -> None:
     import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(f"-I{d}" for d in (inc, os.path.join(inc, "torch", "csrc", "api", "include"),
                                 sysconfig.get_paths()["include"], "/usr/local/cuda/include")),
-           "-c", os.path.join(CSRC, "bind.cpp"), "-o", obj]
+           "-c", BIND_SOURCE, "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed on bind.cpp:\n{res.stderr}")
@@ -68,12 +74,28 @@ def _link_bind(obj: str) -> None:
     os.replace(tmp, BIND)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
+def build_bind(force: bool = False, library=None) -> str:
+    """The module of the target-pass calls (bind.cpp), for the Python and the PyTorch
+    that run.  `library` waits for the library, which is built if it is not given."""
+    if not force and _current(BIND, [BIND_SOURCE, HEADER]):
+        return BIND
     os.makedirs(OUT, exist_ok=True)
-    if not force and os.path.exists(LIB) and os.path.exists(BIND):
-        newest = max(os.path.getmtime(f) for f in _deps())
-        if min(os.path.getmtime(LIB), os.path.getmtime(BIND)) >= newest:
-            return LIB
+    obj = os.path.join(OUT, f"bind.{os.getpid()}.o")
+    try:
+        _compile_bind(obj)
+        (library or build)()
+        _link_bind(obj)
+    finally:
+        if os.path.exists(obj):
+            os.remove(obj)
+    return BIND
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """The library."""
+    os.makedirs(OUT, exist_ok=True)
+    if not force and _current(LIB, _library_deps()):
+        return LIB
     nvcc = _nvcc()
 
     def compile_one(src):
@@ -89,19 +111,25 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(res.stderr)
         return obj
 
-    bind = os.path.join(OUT, "bind.o")
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        python_side = ex.submit(_build_bind, bind)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-        python_side.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     res = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stderr}")
     os.replace(tmp, LIB)
-    _link_bind(bind)
     return LIB
 
 
+def build_all(force: bool = False, verbose: bool = False) -> str:
+    """The library and the module, compiled side by side."""
+    with concurrent.futures.ThreadPoolExecutor(max_workers=2) as ex:
+        library = ex.submit(build, force, verbose)
+        bind = ex.submit(build_bind, force, library.result)
+        path = library.result()
+        bind.result()
+    return path
+
+
 if __name__ == "__main__":
-    print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    print(build_all(force="--force" in sys.argv, verbose="-v" in sys.argv))
