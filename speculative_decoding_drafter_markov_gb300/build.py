@@ -21,7 +21,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libdspark.so")
-BIND = os.path.join(OUT, "_dspark_bind.so")
 SOURCES = ["abi.cu", "attn.cu", "attn_f32.cu", "attn_tc.cu", "diag.cu", "draft.cu", "draft_tc.cu", "gemm_tc.cu", "paged.cu", "rules.cu",
            "sched.cu", "sts.cu", "train_loss.cu", "verify.cu", "verify_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -49,6 +48,14 @@ def _library_deps():
     return [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f != "bind.cpp"] + [HEADER]
 
 
+def bind_path() -> str:
+    """The module's file, named by what its machine code depends on: PyTorch's C++
+    interface and Python's.  Another PyTorch finds no module of its name and builds one."""
+    import torch
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.join(OUT, f"_dspark_bind.torch{torch.__version__}.abi{abi}.{sysconfig.get_config_var('SOABI')}.so")
+
+
 def _compile_bind(obj: str) -> None:
     import torch
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
@@ -62,33 +69,34 @@ def _compile_bind(obj: str) -> None:
         raise RuntimeError(f"g++ failed on bind.cpp:\n{res.stderr}")
 
 
-def _link_bind(obj: str) -> None:
+def _link_bind(obj: str, out: str) -> None:
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = BIND + f".{os.getpid()}.tmp"
+    tmp = out + f".{os.getpid()}.tmp"
     cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", OUT, "-l:libdspark.so", "-Wl,-rpath,$ORIGIN",
            "-L", lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{res.stderr}")
-    os.replace(tmp, BIND)
+    os.replace(tmp, out)
 
 
 def build_bind(force: bool = False, library=None) -> str:
     """The module of the target-pass calls (bind.cpp), for the Python and the PyTorch
     that run.  `library` waits for the library, which is built if it is not given."""
-    if not force and _current(BIND, [BIND_SOURCE, HEADER]):
-        return BIND
+    out = bind_path()
+    if not force and _current(out, [BIND_SOURCE, HEADER]):
+        return out
     os.makedirs(OUT, exist_ok=True)
     obj = os.path.join(OUT, f"bind.{os.getpid()}.o")
     try:
         _compile_bind(obj)
         (library or build)()
-        _link_bind(obj)
+        _link_bind(obj, out)
     finally:
         if os.path.exists(obj):
             os.remove(obj)
-    return BIND
+    return out
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

@@ -64,3 +64,17 @@ assert callable(m.page_map) and m.__file__.startswith({str(where)!r}), m.__file_
     assert r.returncode == 0, r.stdout + r.stderr
     assert (where / PKG / "_build" / "libdspark.so").stat().st_mtime == before
     assert not [f for f in os.listdir(where / PKG / "_build") if f.endswith((".o", ".tmp"))]
+
+
+def test_another_pytorch_does_not_load_this_ones_module(copy):
+    """The module of one PyTorch is not current for another, whatever its time."""
+    where, broken = copy
+    build = f"from {PKG} import build; print(build.build_bind())"
+    first = python(where, build)
+    assert first.returncode == 0, first.stderr
+    os.utime(first.stdout.strip(), (time.time() + 100,) * 2)
+    again = python(where, build, broken)  # current: no compiler is called
+    assert again.returncode == 0 and again.stdout == first.stdout
+    for other in ("torch.__version__ = '1.99.0'", "sysconfig.get_config_var = lambda name: 'cpython-399'"):
+        r = python(where, f"import sysconfig, torch; {other}; {build}", broken)
+        assert r.returncode != 0 and "bind.cpp" in r.stderr, (other, r.stdout)
