@@ -749,7 +749,7 @@ bool tc_supported(const dspark_tree_attention_args &a) {
     auto al16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
     return a.dtype == DSPARK_BF16 && a.scale >= 0.f && a.D % 8 == 0 && a.D <= 128 && a.page % 8 == 0 && a.Hq / a.H <= 128 && al16(a.q) &&
            al16(a.k_cache) && al16(a.v_cache) && al16(a.out) && a.q_row % 8 == 0 && a.q_head % 8 == 0 && a.q_row > 0 &&
-           a.q_head > 0 && a.q_row < (1ll << 38) && a.q_head < (1ll << 38) && tc_kernels_enabled() && tc_available();
+           a.q_head > 0 && a.q_row < (1ll << 38) && a.q_head < (1ll << 38) && tc_available();
 }
 
 // One operand while the host's hint says that a request's lines fit it, else two: a unit

@@ -17,6 +17,11 @@ and column, n tokens and u = 2^-24:
 With keys of zero and values of +-1 every weight is 1, every sum a whole number
 below 2^24, so nothing is rounded before the division: 4 u |out| and the bf16.
 """
+import os
+import subprocess
+import sys
+import tempfile
+
 import numpy as np
 import pytest
 import torch
@@ -121,3 +126,25 @@ def test_tokens_to_the_end_of_32_bits():
     assert ((got["out"].double() - want).abs() <= (2.0 ** -8 + 8 * 2.0 ** -24) * want).all()
     lse = np.log(float(tokens))
     assert ((got["lse"].double() - lse).abs() <= 1e-6 * (1 + lse)).all()
+
+
+def test_the_drafts_switch_is_the_drafts():
+    """DSPARK_DRAFT_KERNEL chooses the draft's kernel; the attention's results are the same bits."""
+    code = """
+import sys, torch
+from test_gpu_target import call, make
+s = make([700, 40, 3], [5, 2, 1], 8, 2, 128, 16, torch.bfloat16, seed=1)
+out, err = call(s)
+torch.save((out["out"].cpu(), out["lse"].cpu()), sys.argv[1])
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    path = os.pathsep.join([here, os.path.dirname(here)])
+    got = []
+    for value in (None, "simt"):
+        env = {k: v for k, v in os.environ.items() if k != "DSPARK_DRAFT_KERNEL"}
+        if value:
+            env["DSPARK_DRAFT_KERNEL"] = value
+        with tempfile.NamedTemporaryFile(suffix=".pt") as f:
+            subprocess.run([sys.executable, "-c", code, f.name], env=dict(env, PYTHONPATH=path), check=True)
+            got.append(torch.load(f.name))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
