@@ -4,9 +4,11 @@ pass runs on the paged-cache operators.
 One cycle, all on the GPU and without a wait on the host: draft, schedule,
 flattened tags, batch map (pages, slots, positions), the target's pass (per layer
 cache writes and attention over the cache), the rules on its logits,
-verification, and the bookkeeping of what was accepted.  The target is a
-stand-in with random weights (embeddings, attention layers, a vocabulary
-projection); the drafter's inputs are the synthetic ones of `workloads`.
+verification, and the bookkeeping of what was accepted.  A request is verified no
+further than its text has room, and is done when that is full; a cycle for which
+the cache has not the pages changes nothing.  The target is a stand-in with random
+weights (embeddings, attention layers, a vocabulary projection); the drafter's
+inputs are the synthetic ones of `workloads`.
 
     python -m speculative_decoding_drafter_markov_gb300.cycle
 """
@@ -55,8 +57,8 @@ class StandInTarget:
 
 
 class Server:
-    """R requests decoded together; `rules` are the keyword arguments of
-    dsp.logit_rules that do not change from cycle to cycle."""
+    """R requests decoded together, texts of up to `max_text` tokens; `rules` are the
+    keyword arguments of dsp.logit_rules that do not change from cycle to cycle."""
 
     def __init__(self, wl, target, prompts, *, seed=0, max_text=512, rules=None):
         dev = target.emb.device
@@ -65,6 +67,13 @@ class Server:
         self.rules = rules or {}
         n_pages = target.caches[0][0].shape[0]
         R, width = wl.R, (max_text + wl.gamma) // target.page + 2
+        if max_text > target.place.shape[0]:
+            raise ValueError(f"texts of up to {max_text} tokens, above the target's {target.place.shape[0]}")
+        if len(prompts) != R or not all(1 <= len(p) <= max_text for p in prompts):
+            raise ValueError(f"{R} prompts of 1 to {max_text} tokens are needed")
+        need = sum(-(-(len(p) - 1) // target.page) for p in prompts)
+        if need > n_pages:
+            raise ValueError(f"the prompts take {need} pages, the cache has {n_pages}")
         self.table = torch.full((R, width), -1, dtype=torch.int32, device=dev)
         self.held, self.free, self.n_free = i32([0] * R), torch.arange(n_pages, dtype=torch.int32, device=dev), i32([n_pages])
         self.lens = i32([0] * R)
@@ -84,6 +93,13 @@ class Server:
             self.pass_of(i32(tok), rows, len(tok), max(len(p) for p in prompts))
         self.lens = rows
         self.anchor = i32([p[-1] for p in prompts])
+        self.done = self.hist_len >= max_text
+
+    def finish(self, r):
+        """Request r is done: its pages go back in the next cycle, but for the one of an
+        idle row (every cycle has a row of every request), and it gets no more tokens."""
+        self.done[r] = True
+        self.lens[r] = 0
 
     def pass_of(self, tok, rows, N, max_rows, parents=None):
         """Reserve pages for `rows` new rows per request and run the target on them."""
@@ -97,7 +113,9 @@ class Server:
     def cycle(self):
         """One decoding cycle.  Returns the drafted tokens, the verified lengths, the
         stand-in's logits T, the logits that it makes of them before and after the
-        rules, and the outcome."""
+        rules, and the outcome: "n_new" tokens of `out_tokens` are new text, none of a
+        request that is done, and none at all where "ok" is false: the cache had not the
+        pages (the error word says so), and the server stands where it stood."""
         wl, err = self.wl, self.err
         inp = W.draft_inputs(wl, seed=self.seed + self.cycles, device=self.anchor.device)
         key = dict(seed=self.seed, cycle=self.cycles, err=err)
@@ -105,12 +123,14 @@ class Server:
         mode = dsp.SCHED_ASYNC if wl.sched == "async" else dsp.SCHED_SYNC
         s = dsp.schedule(d["c"], self.sps, self.B_min, mode=mode, K_in=self.K[0], err=err)
         self.K = [self.K[1], s["K_out"]]
-        tags, N = dsp.build_tags(s["ell"], wl.gamma, err=err)
+        room = torch.where(self.done, 0, self.hist.shape[1] - self.hist_len)  # tokens
+        ell = torch.minimum(s["ell"], (room - 1).clamp(min=0)).to(torch.int32)
+        tags, N = dsp.build_tags(ell, wl.gamma, err=err)
         req, at = tags[:, 0].long().clamp(0, wl.R - 1), tags[:, 1].long().clamp(0, wl.gamma)
         used = torch.arange(tags.shape[0], device=tags.device) < N
         req, at = torch.where(used, req, 0), torch.where(used, at, 0)
         tok = torch.where(at == 0, self.anchor[req], d["x"][req, (at - 1).clamp(min=0)])
-        rows = s["ell"] + 1
+        rows = ell + 1
         T, m = self.pass_of(tok, rows, tags.shape[0], wl.gamma + 1)
         # a drafter that knows something of its target: the stand-in's logits move around
         # the drafter's base logits
@@ -120,26 +140,30 @@ class Server:
                                 out=torch.zeros_like(logits), err=err, **self.rules)
         v = dsp.verify(ruled, tags, self.anchor, d["x"], d["logq"], d["lse"], inp["U"], inp["W1"], inp["W2t"], N_dev=N, **key)
         # the anchor and the accepted tokens stay in the caches; they and the target's
-        # own token are text
-        out, n = v["out_tokens"], v["n_accept"] + 1
+        # own token are text.  (A map that failed has no rows; else there is one at least.)
+        ok = m["row_start"][-1] > 0
+        out, n = v["out_tokens"], torch.where(ok & ~self.done, v["n_accept"] + 1, 0)
         col = torch.arange(wl.gamma + 1, device=out.device)
         place = torch.where(col < n[:, None], self.hist_len[:, None] + col, self.hist.shape[1])
-        room = torch.nn.functional.pad(self.hist, (0, 1))
-        self.hist = room.scatter(1, place.clamp(max=self.hist.shape[1]).long(), out)[:, :-1].contiguous()
-        self.hist_len = (self.hist_len + n).clamp(max=self.hist.shape[1])
-        self.lens = self.lens + n
-        self.anchor = v["next_anchor"]
+        pad = torch.nn.functional.pad(self.hist, (0, 1))  # where the other columns go
+        self.hist = pad.scatter(1, place.long(), out)[:, :-1].contiguous()
+        self.hist_len = self.hist_len + n
+        self.done = self.done | (self.hist_len >= self.hist.shape[1])
+        self.lens = torch.where(self.done, 0, self.lens + n)
+        self.anchor = torch.where(n > 0, v["next_anchor"], self.anchor)
         self.cycles += 1
-        return {"x": d["x"], "ell": s["ell"], "row_start": m["row_start"], "T": T, "logits": logits,
-                "ruled": ruled, **v}
+        return {"x": d["x"], "ell": ell, "row_start": m["row_start"], "T": T, "logits": logits,
+                "ruled": ruled, "n_new": n, "ok": ok, **v}
 
 
-def small_server(seed=0, *, R=6, gamma=4, V=2048, rules=None, **target):
-    """A server of random prompts, small enough to run anywhere."""
+def small_server(seed=0, *, R=6, gamma=4, V=2048, max_text=512, rules=None, **target):
+    """A server of random prompts, small enough to run anywhere; with a cache that holds
+    all texts unless `n_pages` says otherwise."""
     wl = W.small("heavy", R=R, gamma=gamma, V=V, r=64, d=64)
     g = torch.Generator().manual_seed(seed)
     prompts = [torch.randint(0, V, (int(torch.randint(1, 40, (1,), generator=g)),), generator=g).tolist() for _ in range(R)]
-    return Server(wl, StandInTarget(V, seed=seed, **target), prompts, seed=seed, rules=rules)
+    target.setdefault("n_pages", max(256, R * ((max_text + gamma) // target.get("page", 16) + 1)))
+    return Server(wl, StandInTarget(V, seed=seed, **target), prompts, seed=seed, max_text=max_text, rules=rules)
 
 
 def main():
@@ -152,8 +176,8 @@ def main():
     s = small_server(R=R, rules=dict(rep=per(1.2), freq=per(0.1), pres=per(0.0)))
     for c in range(a.cycles):
         o = s.cycle()
-        print(f"cycle {c}: verified {int(o['ell'].sum())} drafted tokens, accepted {int(o['n_accept'].sum())}, "
-              f"pages free {int(s.n_free)}")
+        print(f"cycle {c}: verified {int(o['ell'].sum())} drafted tokens, new tokens {int(o['n_new'].sum())}, "
+              f"done {int(s.done.sum())}, pages free {int(s.n_free)}")
     assert int(s.err) == 0, f"device error {int(s.err)}"
     for r in range(R):
         n, p = int(s.hist_len[r]), int(s.prompt_len[r])
