@@ -232,6 +232,10 @@ DSPARK_API int dspark_build_tags(int32_t R, int32_t gamma, const int32_t *ell, i
 /* tags[i] = (r, j), i.e. the distribution of x_{j+1} given x_0..x_j; rows    */
 /* are grouped by request with positions 0..l_r ascending, every request      */
 /* present (violations: DSPARK_ERR_INVAL in *err).                            */
+/* Entries of -inf have probability 0.  A row of nothing else allows no token: */
+/* the drafted token tested on it is rejected, and the request's y, which is  */
+/* then drawn from it, is 0, a token that it does not allow either, with      */
+/* DSPARK_ERR_NONFINITE in *err; the other requests are not touched by it.    */
 /* ------------------------------------------------------------------------ */
 typedef struct {
     int32_t R, gamma, V, r, dtype;
@@ -509,7 +513,9 @@ DSPARK_API int dspark_tree_attention(const dspark_tree_attention_args *a, void *
  *       z = z > 0 ? z / rep[r] : z * rep[r];
  *   z -= freq[r] c + pres[r] [c > 0];  z += the bias entries of v;
  *   out[i, v] = allow bit v of row allow_row[i] clear ? -inf : z
- * (allow_row[i] < 0: everything allowed).  Computed in fp32, rounded once.
+ * (allow_row[i] < 0: everything allowed; one at or beyond n_allow is reported
+ * and read as that).  A row that allows nothing comes out as -inf throughout,
+ * which dspark_verify reports.  Computed in fp32, rounded once.
  * Any rule may be absent: hist, tok, rep, freq, pres, bias_start, allow NULL.
  * Several bias entries of one token add in their order.  out may be T.  Rows
  * at or beyond row_start[R] are not written.  Tokens outside the vocabulary
