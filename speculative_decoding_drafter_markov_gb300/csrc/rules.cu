@@ -99,7 +99,6 @@ struct RowRules {
 };
 
 // c: occurrences in the output and on the row's path
-// c: occurrences in the output and on the row's path
 __device__ __forceinline__ float penalised(float z, uint32_t c, bool prompt, const RowRules &k) {
     if (prompt || c) z *= z > 0.f ? k.inv_rep : k.rep;
     z = fmaf(-k.freq, (float)c, z);
@@ -145,6 +144,15 @@ __device__ __forceinline__ uint32_t allowed(const uint32_t *allow, int v, int bi
     uint32_t x = allow[v >> 5] >> sh;
     if (!kAligned && sh + bits > 32) x |= allow[(v >> 5) + 1] << (32 - sh);
     return x & ((1u << bits) - 1);
+}
+
+// Waits for the copy of a warp's row k (of its run; `left` rows to come, itself among
+// them).  A wait that runs out is reported and ends the warp's work: the rows left are
+// unspecified, but its copies under way, of this row and the next, have landed.
+__device__ __noinline__ bool row_landed(uint64_t *landed, int k, int left, volatile int *abort_flag, int32_t *err) {
+    if (tc::mbar_wait(&landed[k & 1], (k >> 1) & 1, abort_flag, err)) return true;
+    for (int i = k; i < k + min(left, 2); ++i) tc::mbar_wait_drain(&landed[i & 1], (i >> 1) & 1, err);
+    return false;
 }
 
 // kAligned: every row of T and out starts on a 16-byte boundary; else vec: T and out
@@ -532,9 +540,9 @@ __global__ void __launch_bounds__(kRulesThreads, sizeof(Word) <= sizeof(T) ? 4 :
             const int v = i < va - lo ? lo + i : vb + i - (va - lo);
             dst[v] = !allow || allowed<true>(allow, v, 1) ? src[v] : T(-INFINITY);
         }
-        // a wait that runs out is reported; the rows are then unspecified
-        if (lane == 0) tc::mbar_wait(&landed[warp][b], ((j - j0) >> 1) & 1, abort_flag, a.err);
-        __syncwarp();
+        int here = 1;
+        if (lane == 0) here = tc::mbar_try_wait(&landed[warp][b], ((j - j0) >> 1) & 1) || row_landed(landed[warp], j - j0, j1 - j, abort_flag, a.err);
+        if (!__shfl_sync(0xffffffffu, here, 0)) return;
         touched([&](int i, uint32_t w) {
             const int v = lo + i;
             if (!kAligned && (v < va || v >= vb)) scatter(j, v, w, allow, src, dst);
