@@ -274,7 +274,7 @@ Page page_of_size(int size) { return Page{(unsigned)size, (size & (size - 1)) ==
 
 cudaError_t launch_page_map(const dspark_page_map_args &a, cudaStream_t s) {
     const size_t smem = sizeof(int) * 3 * (size_t)(a.R + 1);
-    if (smem > 48 * 1024) {
+    if (smem > 32 * 1024) {  // well below the 48 KB, which the kernel's own variables share
         cudaError_t e = cudaFuncSetAttribute(page_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }

@@ -65,3 +65,14 @@ def test_bad_entry_of_the_stack(bad, tree):
 def test_page_numbers_of_the_last_page():
     out, table, free, err = call([9, 6], [3, 3], [3, 2], free=FREE[:4] + [9])
     assert err == 0 and out["slot"][-1] == 9 * 4
+
+
+@pytest.mark.parametrize("R", [4000, 4077, 4078, 4079, 4090, 4095, 4096, 8192])
+def test_any_number_of_requests(R):
+    """Around the sums' 48 KB of shared memory, where a launch has to ask for more."""
+    table, free = torch.full((R, 1), -1, dtype=torch.int32, device="cuda"), torch.arange(R, dtype=torch.int32, device="cuda")
+    one, err = torch.ones(R, dtype=torch.int32, device="cuda"), err_word()
+    out = dsp.page_map(one - 1, one, table, one - 1, free, ints([R]), page=4, N=R, err=err)
+    assert int(err) == 0 and int(out["n_free"]) == 0
+    assert table.flatten().tolist() == list(range(R - 1, -1, -1)) and out["row_start"].tolist() == list(range(R + 1))
+    assert torch.equal(out["slot"], 4 * table.flatten())
