@@ -72,6 +72,8 @@ class TrainLossArgs(ctypes.Structure):
 i64 = ctypes.c_int64
 
 
+# The target-pass operators of the C ABI, for ctypes callers of load(); the functions of
+# this module go through the one built from csrc/bind.cpp, which fills the structs itself.
 class PageMapArgs(ctypes.Structure):
     _fields_ = [("R", i32), ("page", i32), ("n_pages", i32), ("max_pages", i32), ("N", i32), ("n_parents", i32),
                 ("W", i32), ("len", P), ("rows", P), ("parents", P), ("held", P), ("n_free", P), ("table", P),
@@ -533,8 +535,9 @@ def tree_attention(q, k_cache, v_cache, table, lens, row_start, *, mask=None, sc
     """Attention of the drafted rows q [N, Hq, D] over the cache and over their
     ancestors among the rows (include/dspark.h): table, row_start and mask as
     page_map gives them (mask None: chains), lens [R] the tokens before the
-    rows, scale 1 / sqrt(D) unless given.  Returns {"out": [N, Hq, D],
-    "lse": [N, Hq] fp32}; an `out` passed in may leave "lse" out."""
+    rows, scale 1 / sqrt(D) unless given, ws scratch of tree_attention_workspace_size
+    bytes on a boundary of 256.  Returns {"out": [N, Hq, D], "lse": [N, Hq] fp32}; an
+    `out` passed in may leave "lse" out."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return tree_attention(q, k_cache, v_cache, table, lens, row_start, mask=mask, scale=scale, max_rows=max_rows,

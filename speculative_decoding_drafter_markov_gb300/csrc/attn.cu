@@ -16,8 +16,8 @@ namespace {
 // tile are staged in shared memory as fp32 and shared by the lines.  A thread
 // scores one line against four tokens, then each warp adds its four lines'
 // weighted values, the lanes side by side over D.  Bound by its instructions: 64 caches
-// of up to 8192 tokens, 36 lines on each of 8 heads of 128, bf16: 1363 us, against 127 us
-// on the tensor cores; one row over 2047 tokens 28 against 12.
+// of up to 8192 tokens, 36 lines on each of 8 heads of 128, bf16: 1351 us, against 127 us
+// on the tensor cores; one row over 2047 tokens 28 against 12.5.
 constexpr int kLines = kSimtLines, kTileLog2 = 5, kTile = 1 << kTileLog2, kThreads = 128;
 
 template <typename T>
@@ -215,9 +215,10 @@ __global__ void __launch_bounds__(kThreads) tree_attention_simt(const __grid_con
 // lines of CTA c's unit: a warp a line, or, where that takes fewer rounds (many pieces
 // and few lines, as of one long cache over the whole GPU), the four warps of a CTA share
 // a line's pieces.  (Always sharing above eight pieces: 434 lines on 4 heads, 5 caches of
-// up to 1312 tokens took 41 us, by rounds 24.)  Bound by latency: partials that are still in L2, four under way before the weights are known
-// (eight take the registers of half of the CTAs: 2 us more for 256 lines).  About 3 us
-// for a few lines, 9 us for 256 lines in each of 16 requests.
+// up to 1312 tokens took 41 us, by rounds 24.)  Bound by latency: partials that are still
+// in L2, four under way before the weights are known (eight take the registers of half of
+// the CTAs: 2 us more for 256 lines).  About 3 us for a few lines, 9 us for 256 lines in
+// each of 16 requests.
 constexpr int kJoinWarps = 4, kAhead = 4;
 
 // four (or, E = 1, one) adjacent floats per lane

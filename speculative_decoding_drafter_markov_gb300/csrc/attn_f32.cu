@@ -10,8 +10,8 @@
 // its registers hold: 4 lines x 4 tokens over a quarter of the columns for the scores
 // (8 16-byte reads per 64 products), 8 lines x 8 columns for the outputs (6 per 64).
 // A tile costs the same however few of the 16 lines are in use.  8 query
-// heads on 4 of 64: 16 caches of 8192 tokens, 17 rows, 342 us (the general kernel: 731);
-// one of 131072, 1 row, 120 (281); 4 of up to 1500, 5 rows, 12 (24).
+// heads on 4 of 64: 16 caches of 8192 tokens, 17 rows, 313 us (the general kernel: 730);
+// one of 131072, 1 row, 110 (278); 4 of up to 1500, 5 rows, 12.5 (24).
 #include <cuda_runtime.h>
 
 #include "attn_common.cuh"

@@ -17,9 +17,9 @@
 // reference that may lag behind.
 //
 // P is rounded to one bf16 term (the MMA wants A in the type of B, the values): against
-// 64 bits the outputs are off by 0.0023 of their size (of 0.0017 the rounding
-// of the output alone).  A second term, the rest of P in the half of S's columns that the
-// first leaves free, brings that to 0.0017, but doubles the second product and a third of
+// 64 bits the outputs are off by 0.0022 to 0.0023 of their size, the rounding of the output
+// alone by 0.0017.  A second term, the rest of P in the half of S's columns that the first
+// leaves free, brings that to 0.0017, but doubles the second product and a third of
 // the softmax, both in the chain that bounds a tile: 64 caches of up to 8192 tokens 146
 // instead of 126 us, 16 of up to 16384 with trees of up to 64 rows 126 instead of 98, 8 of
 // up to 131072 with up to 256 lines 587 instead of 433, and with 68 lines 433 instead of 420.
@@ -30,12 +30,12 @@
 //
 // Bound by HBM while lines are few: a tile of D = 128 is 64 KB, 2,900 clocks of an
 // SM's share of the bandwidth, against 1,030 of MMA per operand.  8 heads of 128, bf16:
-// 8 caches of up to 131072 tokens with up to 68 lines take 423 us (6.8 TB/s), 64 of up to
-// 8192 with up to 36 lines 127 us (5.5 TB/s, the rest starts and ends of pieces), one row
+// 8 caches of up to 131072 tokens with up to 68 lines take 424 us (6.8 TB/s), 64 of up to
+// 8192 with up to 36 lines 127 us (5.6 TB/s, the rest starts and ends of pieces), one row
 // over 2047 tokens 12.5 us (latency).  With many lines by the chain from S through the
-// softmax to P: 8 caches of up to 131072 with up to 256 lines 438 us, 0.87 PFLOP/s.
-// S in half tiles of 64 tokens, to give the softmax its first half earlier, is slower (558
-// against 535 us for 256 lines): an MMA of 64 columns takes 55 clocks, one of 128 takes 64.
+// softmax to P: 8 caches of up to 131072 with up to 256 lines 435 us, 0.88 PFLOP/s.
+// S in half tiles of 64 tokens, to give the softmax its first half earlier, took 4 % more
+// than whole tiles: an MMA of 64 columns takes 55 clocks, one of 128 takes 64.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -754,7 +754,7 @@ bool tc_supported(const dspark_tree_attention_args &a) {
 
 // One operand while the host's hint says that a request's lines fit it, else two: a unit
 // of two reads its keys once for twice the lines.  (8 caches of up to 131072 tokens, up
-// to 256 lines: 438 us with two, 572 with one; 4 prompts of up to 4096 rows: 191 and 229;
+// to 256 lines: 435 us with two, 572 with one; 4 prompts of up to 4096 rows: 192 and 229;
 // 16 caches of up to 1000 tokens, where there are few pieces to share: 33 and 29.)
 void tc_shape(const dspark_tree_attention_args &a, int *block_rows, int *lines, int *stride) {
     const int G = a.Hq / a.H, one = 128 / G;

@@ -23,10 +23,10 @@ namespace {
 // * table entries are written only at and beyond a taker's held pages, where
 //   nobody reads them (a row's slot takes its page by the same rule);
 // * held and n_free are not written (their new values go elsewhere).
-// Bound by latency, a chain of loads, a scan and a store: 4 requests 2.8 us, 96 prompts
-// of up to 32768 rows 5.4, 512 trees of up to 64 rows 8.1, of which 3 are the walk from
+// Bound by latency, a chain of loads, a scan and a store: 4 requests 3.0 us, 96 prompts
+// of up to 32768 rows 5.5, 512 trees of up to 64 rows 8.2, of which 3 are the walk from
 // a row to its root (the parents staged in shared memory first gained nothing).  With
-// 256 threads 8192 requests take 26 us; 128, 512 and 1024 were no faster.
+// 256 threads 8192 requests take 25 us; 128, 512 and 1024 were no faster.
 constexpr int kMapThreads = 256;
 
 struct MapSums {
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const dspark_page
 // A copy of 2 N H D elements: bound by HBM (read once, written once).  A thread has
 // one 16-byte piece of a row -- keys or values, head and columns are found once --
 // and takes it from kRows rows, all reads under way together; neighbouring threads
-// have neighbouring pieces.  24 prompts of up to 8192 rows, 8 heads of 128, bf16: 24.7 us,
+// have neighbouring pieces.  24 prompts of up to 8192 rows, 8 heads of 128, bf16: 24.3 us,
 // 5.7 TB/s (one row a thread: 31.5 us); 64 requests of up to 9 rows: 2.1 us.
 constexpr int kStoreThreads = 256;
 

@@ -29,7 +29,7 @@ namespace {
 // no copy to join, and the listed entries are scattered.
 // Bound by HBM: the logits' one read and one write.  The text is read once per
 // slice, from L2, which is why a slice is large.  512 requests of up to 9 rows,
-// V = 129280, bf16, texts of up to 8192 tokens: 237 us, 5.7 TB/s; without the texts
+// V = 129280, bf16, texts of up to 8192 tokens: 236 us, 5.7 TB/s; without the texts
 // 212 us.  (The CTAs of a request counting its text together, as a cluster of 2 / 4 / 8
 // through each other's shared memory, moved in step and took 3 / 13 / 35 us more than
 // each counting alone.)
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kRulesThreads, sizeof(Word) <= sizeof(T) ? 4 :
     // The marked entries among them get a list of their own, of what they found in the lists
     // of biases and drafts (the warp looks for an entry together); where they stood is left
     // as if untouched.  (235 requests of up to 15 rows, V = 2656, texts of up to 855 tokens,
-    // 64 biases: 30 us; with every marked entry searched for in every row 78 to 100.)
+    // 64 biases: 29 us; with every marked entry searched for in every row 78 to 100.)
     int prepared = 0;
     if (bias.n + draft.n > kSearch) {
         const int n_all = by_list ? listed : part;
@@ -592,7 +592,7 @@ cudaError_t launch_as(const dspark_logit_rules_args &a, cudaStream_t s) {
     // The four CTAs that an SM holds: where requests are few their rows are spread, at the
     // price of counting the text for each run of rows; the slices are made smaller only
     // where even a CTA for every row leaves SMs empty.  (4 requests of up to 9 rows, V =
-    // 129280, texts of up to 8192: 11.7 us, with small slices first 19.5; 16 requests: 18.7
+    // 129280, texts of up to 8192: 11.8 us, with small slices first 19.5; 16 requests: 18.8
     // and 32; up to 17 rows, texts of up to 1000, 4 requests: 9.4 and 25.)
     const long long want = 4ll * sm_count(), per = (a.N + a.R - 1) / a.R;
     int slice = kSliceBytes / (int)sizeof(T);
