@@ -464,6 +464,77 @@ typedef struct {
 
 DSPARK_API int dspark_cache_store(const dspark_cache_store_args *a, dspark_stream_t stream);
 
+/* Queries, keys and values of the rows on their way into the attention: norms of the
+ * queries and keys of each head, their rotation by position, and the append to the
+ * cache, in one pass.  For each head x of q and of k, computed in fp32 and rounded once:
+ *   with a weight w:  x_d <- x_d w_d / sqrt(mean_d x_d^2 + eps)
+ *   rotation by pos[i] freq[j] of pair j < rot / 2, (a, b) = (x_j, x_{j + rot / 2}), or
+ *   with `interleaved` (x_{2j}, x_{2j + 1}):  (a cos - b sin, b cos + a sin);
+ * elements at and beyond rot stay as they are.  The angle is that of the exact product,
+ * whole turns left out before it is rounded, so far positions lose nothing (freq finite
+ * and below 2^16, radians per position; pos any 32-bit number).
+ * With `slot` keys and values go into the cache as by dspark_cache_store, and a row
+ * whose slot is negative, or beyond the cache (reported), is left out altogether: its
+ * queries are not written either.  Without, keys go to k_out and v is not looked at.
+ * q or k may be NULL (no queries, no keys).  q_out may be q with q's strides, k_out
+ * may be k with k's; other overlaps of what is read and written are not allowed.
+ * Weights are of the type of the rows.  D at most DSPARK_ATTN_MAX_D, rot even, at most D
+ * (0: norms only).  One launch, no workspace. */
+typedef struct {
+    int32_t N, Hq, H, D;      /* rows, query and key-value heads, head size      */
+    int32_t rot, interleaved;
+    int32_t page, n_pages, dtype;
+    float eps;                /* above 0 with a weight                          */
+    const void *q, *k, *v;    /* [N, Hq, D], [N, H, D] twice, D adjacent; q or k may be NULL */
+    int64_t q_row, q_head, k_row, k_head, v_row, v_head;  /* strides in elements */
+    const int32_t *pos;       /* [N]                                            */
+    const float *freq;        /* [rot / 2]                                      */
+    const void *q_weight, *k_weight;  /* [D], or NULL: no norm                   */
+    const int32_t *slot;      /* [N], or NULL: no cache                          */
+    void *q_out;              /* out [N, Hq, D], strides below                   */
+    int64_t q_out_row, q_out_head;
+    void *k_out;              /* out [N, H, D], strides below, without slot       */
+    int64_t k_out_row, k_out_head;
+    void *k_cache, *v_cache;  /* [n_pages, H, page, D], with slot                */
+    int32_t *err;
+} dspark_rope_store_args;
+
+DSPARK_API int dspark_rope_store(const dspark_rope_store_args *a, dspark_stream_t stream);
+
+/* A cache in 4 bits: 4.5 bits per element instead of 16.  16 neighbouring elements of a
+ * head share a scale, held as one byte b:
+ *   s(b) = 2^(b / 8 - 16) (1 + b % 8 / 8) for b <= 254;  255: the 16 are NaN;
+ * an element is n s, n a whole number of -8 .. 7 held as n + 8.  The write takes
+ *   s = the s(b) nearest to max |x| / 7 of the 16 (halfway: the even b),
+ *   n = x / s rounded to the nearest whole number (halfway: the even one), within -7 .. 7,
+ * both exactly, so the bytes do not depend on how they are computed; 16 elements with
+ * an infinity or a NaN among them are held as NaN.  Values are off by 1/13 of the largest of
+ * their 16 at most, or by 2^-17 where those are all small; beyond 401408 they are held as that.
+ * Values written back give the same bytes.  n s has at most 8 significant bits: bf16
+ * holds it exactly.
+ * A page of a head is one run of page * D * 9 / 16 bytes: the codes of its tokens, D / 2
+ * bytes each, then their scales, D / 16 bytes each.  Eight elements e_0 .. e_7 are four
+ * bytes, two elements each (low half first): e_0 e_2, e_4 e_6, e_1 e_3, e_5 e_7.
+ * D is a multiple of 16 up to DSPARK_ATTN_MAX_D, page * D a multiple of 128, the caches
+ * [n_pages, H, page * D * 9 / 16] bytes on a boundary of 16. */
+
+/* Keys and values of the rows into their slots of such caches; slots, strides and the
+ * rest as for dspark_cache_store.  k_out and v_out, given both or neither, get the values
+ * that the cache then holds, in the type of the rows (skipped rows are not written).
+ * One launch, no workspace. */
+typedef struct {
+    int32_t N, H, D;          /* rows, key-value heads, head size               */
+    int32_t page, n_pages, dtype;  /* dtype of k, v, k_out and v_out             */
+    const void *k, *v;        /* [N, H, D]                                      */
+    int64_t k_row, k_head, v_row, v_head;  /* strides in elements               */
+    const int32_t *slot;      /* [N]                                            */
+    uint8_t *k_cache, *v_cache;    /* [n_pages, H, page * D * 9 / 16]            */
+    void *k_out, *v_out;      /* out [N, H, D] contiguous, or NULL               */
+    int32_t *err;
+} dspark_cache_store4_args;
+
+DSPARK_API int dspark_cache_store4(const dspark_cache_store4_args *a, dspark_stream_t stream);
+
 /* Attention of the drafted rows over the cache.  Row j of request r (its own
  * keys and values already stored) sees the tokens t < len[r] and, among the
  * request's new rows, row j' where bit j' of its mask words is set (mask NULL:
@@ -509,6 +580,13 @@ typedef struct {
 
 DSPARK_API size_t dspark_tree_attention_workspace_size(const dspark_tree_attention_args *a);
 DSPARK_API int dspark_tree_attention(const dspark_tree_attention_args *a, void *ws, dspark_stream_t stream);
+
+/* The same attention over caches in 4 bits (above), k_cache and v_cache [n_pages, H,
+ * page * D * 9 / 16] bytes; dtype is that of q and out.  What is said of
+ * dspark_tree_attention holds: what a row sees, rows that see nothing, errors, sums in
+ * fp32.  On the CUDA cores.  A workspace of its own size. */
+DSPARK_API size_t dspark_tree_attention4_workspace_size(const dspark_tree_attention_args *a);
+DSPARK_API int dspark_tree_attention4(const dspark_tree_attention_args *a, void *ws, dspark_stream_t stream);
 
 /* Rules on the target's logits before dspark_verify.  For row i, row j of
  * request r, and token v, with c the number of times v stands in the output

@@ -87,6 +87,20 @@ class CacheStoreArgs(ctypes.Structure):
                 ("k_cache", P), ("v_cache", P), ("err", P)]
 
 
+class RopeStoreArgs(ctypes.Structure):
+    _fields_ = [("N", i32), ("Hq", i32), ("H", i32), ("D", i32), ("rot", i32), ("interleaved", i32), ("page", i32),
+                ("n_pages", i32), ("dtype", i32), ("eps", ctypes.c_float), ("q", P), ("k", P), ("v", P), ("q_row", i64),
+                ("q_head", i64), ("k_row", i64), ("k_head", i64), ("v_row", i64), ("v_head", i64), ("pos", P), ("freq", P),
+                ("q_weight", P), ("k_weight", P), ("slot", P), ("q_out", P), ("q_out_row", i64), ("q_out_head", i64),
+                ("k_out", P), ("k_out_row", i64), ("k_out_head", i64), ("k_cache", P), ("v_cache", P), ("err", P)]
+
+
+class CacheStore4Args(ctypes.Structure):
+    _fields_ = [("N", i32), ("H", i32), ("D", i32), ("page", i32), ("n_pages", i32), ("dtype", i32), ("k", P),
+                ("v", P), ("k_row", i64), ("k_head", i64), ("v_row", i64), ("v_head", i64), ("slot", P),
+                ("k_cache", P), ("v_cache", P), ("k_out", P), ("v_out", P), ("err", P)]
+
+
 class TreeAttentionArgs(ctypes.Structure):
     _fields_ = [("R", i32), ("N", i32), ("Hq", i32), ("H", i32), ("D", i32), ("page", i32), ("n_pages", i32),
                 ("max_pages", i32), ("dtype", i32), ("W", i32), ("max_rows", i32), ("scale", ctypes.c_float),
@@ -132,6 +146,10 @@ SYMBOLS = {
     "dspark_train_losses": ([ctypes.POINTER(TrainLossArgs), P], ctypes.c_int),
     "dspark_page_map": ([ctypes.POINTER(PageMapArgs), P], ctypes.c_int),
     "dspark_cache_store": ([ctypes.POINTER(CacheStoreArgs), P], ctypes.c_int),
+    "dspark_rope_store": ([ctypes.POINTER(RopeStoreArgs), P], ctypes.c_int),
+    "dspark_cache_store4": ([ctypes.POINTER(CacheStore4Args), P], ctypes.c_int),
+    "dspark_tree_attention4_workspace_size": ([ctypes.POINTER(TreeAttentionArgs)], ctypes.c_size_t),
+    "dspark_tree_attention4": ([ctypes.POINTER(TreeAttentionArgs), P, P], ctypes.c_int),
     "dspark_tree_attention_workspace_size": ([ctypes.POINTER(TreeAttentionArgs)], ctypes.c_size_t),
     "dspark_tree_attention": ([ctypes.POINTER(TreeAttentionArgs), P, P], ctypes.c_int),
     "dspark_logit_rules": ([ctypes.POINTER(LogitRulesArgs), P], ctypes.c_int),
@@ -530,6 +548,40 @@ def cache_store(k, v, slot, k_cache, v_cache, *, err=None, stream=None):
     return (_bind or _target()).cache_store(k, v, slot, k_cache, v_cache, err)
 
 
+def rope_store(q, k, v, pos, freq, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, slot=None, k_cache=None,
+               v_cache=None, out=None, err=None, stream=None):
+    """Norms of the heads of q [N, Hq, D] and k [N, H, D] (where their weight [D] is given),
+    their rotation by pos [N] int32 times freq [rot / 2] fp32 radians, in pairs of halves
+    or with `interleaved` of neighbours, and with slot [N] int32 the append of k and v
+    to the caches [n_pages, H, page, D], in one pass (include/dspark.h).  Views of a
+    fused projection are fine; q or k may be None.  Returns {"q"} and, without slot, {"k"}
+    of the rows' shapes; an `out` passed in may hold q and k themselves, or views."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rope_store(q, k, v, pos, freq, q_weight=q_weight, k_weight=k_weight, eps=eps, interleaved=interleaved,
+                              slot=slot, k_cache=k_cache, v_cache=v_cache, out=out, err=err)
+    return (_bind or _target()).rope_store(q, k, v, pos, freq, q_weight, k_weight, eps, interleaved, slot, k_cache, v_cache,
+                                           out, err)
+
+
+def cache4(n_pages, H, page, D, *, device="cuda"):
+    """An empty cache in 4 bits for cache_store4 and tree_attention4: [n_pages, H, page *
+    D * 9 / 16] bytes (include/dspark.h).  Keys and values have one each."""
+    if min(n_pages, H, page, D) < 1 or D % 16 or page * D % 128:
+        raise ValueError(f"a cache in 4 bits takes D a multiple of 16 and page * D one of 128, not page {page}, D {D}")
+    return torch.zeros((n_pages, H, page * D * 9 // 16), dtype=torch.uint8, device=device)
+
+
+def cache_store4(k, v, slot, k_cache, v_cache, *, values=False, out=None, err=None, stream=None):
+    """Write the rows' keys and values k, v [N, H, D] into the slots slot [N] int32 of
+    caches in 4 bits (from cache4).  With `values`, or with `out`, returns {"k", "v"}: what
+    the cache then holds of the rows, in their type."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return cache_store4(k, v, slot, k_cache, v_cache, values=values, out=out, err=err)
+    return (_bind or _target()).cache_store4(k, v, slot, k_cache, v_cache, values, out, err)
+
+
 def tree_attention(q, k_cache, v_cache, table, lens, row_start, *, mask=None, scale=None, max_rows=1, out=None, ws=None,
                    err=None, stream=None):
     """Attention of the drafted rows q [N, Hq, D] over the cache and over their
@@ -550,6 +602,24 @@ def tree_attention_workspace_size(q, k_cache, v_cache, table, lens, row_start, *
     """Scratch bytes dspark_tree_attention needs for this shape."""
     return _target().tree_attention_workspace_size(q, k_cache, v_cache, table, lens, row_start, mask, None, max_rows, None,
                                                    None, None)
+
+
+def tree_attention4(q, k_cache, v_cache, table, lens, row_start, *, mask=None, scale=None, max_rows=1, out=None, ws=None,
+                    err=None, stream=None):
+    """tree_attention over caches in 4 bits (from cache4, filled by cache_store4); ws scratch
+    of tree_attention4_workspace_size bytes."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return tree_attention4(q, k_cache, v_cache, table, lens, row_start, mask=mask, scale=scale, max_rows=max_rows,
+                                   out=out, ws=ws, err=err)
+    return (_bind or _target()).tree_attention4(q, k_cache, v_cache, table, lens, row_start, mask, scale, max_rows, out, ws,
+                                                err)
+
+
+def tree_attention4_workspace_size(q, k_cache, v_cache, table, lens, row_start, *, mask=None, max_rows=1):
+    """Scratch bytes dspark_tree_attention4 needs for this shape."""
+    return _target().tree_attention4_workspace_size(q, k_cache, v_cache, table, lens, row_start, mask, None, max_rows, None,
+                                                    None, None)
 
 
 def logit_rules(T, row_start, *, tok=None, mask=None, hist=None, hist_len=None, prompt_len=None, rep=None, freq=None,

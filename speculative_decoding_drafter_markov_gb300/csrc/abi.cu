@@ -506,6 +506,51 @@ DSPARK_API int dspark_cache_store(const dspark_cache_store_args *a, dspark_strea
     return e == cudaSuccess ? ok() : cuda_fail(e, "cache store");
 }
 
+DSPARK_API int dspark_rope_store(const dspark_rope_store_args *a, dspark_stream_t stream) {
+    if (!a) return fail(DSPARK_ERR_INVAL, "null argument struct");
+    const int Hq = a->q ? a->Hq : 0, H = a->k ? a->H : 0;
+    if (a->N < 0 || Hq < 0 || H < 0 || (a->N > 0 && Hq + H < 1) || a->D < 1)
+        return fail(DSPARK_ERR_INVAL, "bad shape N=%d Hq=%d H=%d D=%d", a->N, a->Hq, a->H, a->D);
+    if (a->dtype != DSPARK_F32 && a->dtype != DSPARK_BF16) return fail(DSPARK_ERR_INVAL, "bad dtype %d", a->dtype);
+    if (a->D > DSPARK_ATTN_MAX_D) return fail(DSPARK_ERR_UNSUPPORTED, "D=%d above %d", a->D, DSPARK_ATTN_MAX_D);
+    if (a->rot < 0 || a->rot > a->D || a->rot % 2) return fail(DSPARK_ERR_INVAL, "bad rot=%d of D=%d", a->rot, a->D);
+    if ((a->q_weight || a->k_weight) && !(a->eps >= 1e-30f && a->eps < 1e30f)) return fail(DSPARK_ERR_INVAL, "bad eps=%g", (double)a->eps);
+    if ((long long)(Hq + 2ll * H) * a->D > (1 << 20))
+        return fail(DSPARK_ERR_UNSUPPORTED, "rows of %lld elements, above 2^20", (Hq + 2ll * H) * a->D);
+    if (a->slot && (H < 1 || a->page < 1 || a->n_pages < 1))
+        return fail(DSPARK_ERR_INVAL, "bad cache: H=%d page=%d n_pages=%d", H, a->page, a->n_pages);
+    if (a->N == 0) return ok();
+    if (!a->pos || (a->rot > 0 && !a->freq) || (Hq > 0 && !a->q_out)) return fail(DSPARK_ERR_INVAL, "null tensor pointer");
+    if (H > 0 && (a->slot ? !a->v || !a->k_cache || !a->v_cache : !a->k_out)) return fail(DSPARK_ERR_INVAL, "null tensor pointer");
+    cudaError_t e = dspark::launch_rope_store(*a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "rope store");
+}
+
+// what a cache in 4 bits asks of its shape and address
+static int check_cache4(int page, int D, const void *k_cache, const void *v_cache) {
+    if (D % 16 || (long long)page * D % 128)
+        return fail(DSPARK_ERR_UNSUPPORTED, "a cache in 4 bits takes D a multiple of 16 and page * D one of 128, not page=%d D=%d", page, D);
+    if (!aligned16(k_cache) || !aligned16(v_cache)) return fail(DSPARK_ERR_INVAL, "the caches must be aligned");
+    return DSPARK_OK;
+}
+
+DSPARK_API int dspark_cache_store4(const dspark_cache_store4_args *a, dspark_stream_t stream) {
+    if (!a) return fail(DSPARK_ERR_INVAL, "null argument struct");
+    if (a->N < 0 || a->H < 1 || a->D < 1 || a->page < 1 || a->n_pages < 1)
+        return fail(DSPARK_ERR_INVAL, "bad shape N=%d H=%d D=%d page=%d n_pages=%d", a->N, a->H, a->D, a->page, a->n_pages);
+    if (a->dtype != DSPARK_F32 && a->dtype != DSPARK_BF16) return fail(DSPARK_ERR_INVAL, "bad dtype %d", a->dtype);
+    if (a->D > DSPARK_ATTN_MAX_D) return fail(DSPARK_ERR_UNSUPPORTED, "D=%d above %d", a->D, DSPARK_ATTN_MAX_D);
+    if ((long long)a->H * a->D > (1 << 20)) return fail(DSPARK_ERR_UNSUPPORTED, "H * D = %lld above 2^20", (long long)a->H * a->D);
+    int rc = check_cache4(a->page, a->D, a->k_cache, a->v_cache);
+    if (rc != DSPARK_OK) return rc;
+    if ((a->k_out != nullptr) != (a->v_out != nullptr)) return fail(DSPARK_ERR_INVAL, "k_out and v_out go together");
+    if (!aligned16(a->k_out) || !aligned16(a->v_out)) return fail(DSPARK_ERR_INVAL, "k_out and v_out must be aligned");
+    if (a->N == 0) return ok();
+    if (!a->k || !a->v || !a->slot || !a->k_cache || !a->v_cache) return fail(DSPARK_ERR_INVAL, "null tensor pointer");
+    cudaError_t e = dspark::launch_cache_store4(*a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "cache store in 4 bits");
+}
+
 static int check_tree_attention(const dspark_tree_attention_args *a) {
     if (!a) return fail(DSPARK_ERR_INVAL, "null argument struct");
     if (a->R < 1 || a->N < 0 || a->H < 1 || a->Hq < a->H || a->Hq % a->H || a->D < 1 || a->page < 1 || a->n_pages < 1 ||
@@ -537,6 +582,27 @@ DSPARK_API int dspark_tree_attention(const dspark_tree_attention_args *a, void *
     if ((rc = check_ws(ws)) != DSPARK_OK) return rc;
     cudaError_t e = dspark::launch_tree_attention(*a, ws, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ok() : cuda_fail(e, "tree attention");
+}
+
+static int check_tree_attention4(const dspark_tree_attention_args *a) {
+    const int rc = check_tree_attention(a);
+    return rc != DSPARK_OK ? rc : check_cache4(a->page, a->D, a->k_cache, a->v_cache);
+}
+
+DSPARK_API size_t dspark_tree_attention4_workspace_size(const dspark_tree_attention_args *a) {
+    if (check_tree_attention4(a) != DSPARK_OK) return 0;
+    return dspark::tree_attention4_ws_bytes(*a);
+}
+
+DSPARK_API int dspark_tree_attention4(const dspark_tree_attention_args *a, void *ws, dspark_stream_t stream) {
+    int rc = check_tree_attention4(a);
+    if (rc != DSPARK_OK) return rc;
+    if (a->N == 0) return ok();
+    if (!a->q || !a->k_cache || !a->v_cache || !a->table || !a->len || !a->row_start || !a->out)
+        return fail(DSPARK_ERR_INVAL, "null tensor pointer");
+    if ((rc = check_ws(ws)) != DSPARK_OK) return rc;
+    cudaError_t e = dspark::launch_tree_attention4(*a, ws, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "tree attention in 4 bits");
 }
 
 DSPARK_API int dspark_logit_rules(const dspark_logit_rules_args *a, dspark_stream_t stream) {

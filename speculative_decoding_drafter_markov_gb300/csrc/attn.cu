@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "attn_common.cuh"
+#include "cache4.cuh"
 
 namespace dspark {
 namespace attn {
@@ -39,7 +40,16 @@ inline size_t smem_bytes(int D) {
     return sizeof(float) * ((size_t)kLines * d + (size_t)kTile * (d + 4) + (size_t)kTile * d + kLines * kTile);
 }
 
-template <typename T, int kDV>  // kDV: float4 columns per lane, ceil(D / 128)
+// elements d .. d + 3 of token `off` of a page of 4-bit codes
+__device__ __forceinline__ float4 load4(const unsigned char *page, const dspark_tree_attention_args &a, int off, int d) {
+    const unsigned word = *reinterpret_cast<const unsigned *>(page + (long long)off * (a.D / 2) + d / 8 * 4);
+    const float s = cache4::scale_of(page[cache4::code_bytes(a.page, a.D) + (long long)off * (a.D / 16) + d / 16]);
+    auto at = [&](int e) { return (float)((int)(word >> cache4::code_shift((d & 4) + e) & 15u) - 8) * s; };
+    return make_float4(at(0), at(1), at(2), at(3));
+}
+
+// T: of the queries and outputs; kFour: caches in 4 bits, else of T
+template <typename T, int kDV, bool kFour>  // kDV: float4 columns per lane, ceil(D / 128)
 __global__ void __launch_bounds__(kThreads) tree_attention_simt(const __grid_constant__ Params p) {
     extern __shared__ __align__(16) float sh[];
     __shared__ Share shared_share;
@@ -96,7 +106,11 @@ __global__ void __launch_bounds__(kThreads) tree_attention_simt(const __grid_con
                         pg = 0;
                     }
                     const size_t at = (((size_t)pg * a.H + h) * a.page + (tok - in_table * a.page)) * D + d;
-                    if (p.vec) {
+                    if (kFour) {
+                        const size_t page = ((size_t)pg * a.H + h) * cache4::page_bytes(a.page, D);
+                        kv = load4(static_cast<const unsigned char *>(a.k_cache) + page, a, tok - in_table * a.page, d);
+                        vv = load4(static_cast<const unsigned char *>(a.v_cache) + page, a, tok - in_table * a.page, d);
+                    } else if (p.vec) {
                         kv = load4(kc + at);
                         vv = load4(vc + at);
                     } else {
@@ -332,9 +346,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 8) tree_attention_join(const 
     }
 }
 
-template <typename T, int kDV>
+template <typename T, int kDV, bool kFour = false>
 cudaError_t launch_as(const Params &p, int grid, size_t smem, cudaStream_t s) {
-    auto kern = tree_attention_simt<T, kDV>;
+    auto kern = tree_attention_simt<T, kDV, kFour>;
     if (smem > 32 * 1024) {  // well below the 48 KB, which the kernel's own variables share
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
@@ -387,15 +401,60 @@ size_t tree_attention_ws_bytes(const dspark_tree_attention_args &a) {
     return tc > simt ? tc : simt;
 }
 
-cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws, cudaStream_t s) {
-    using namespace attn;
-    if (sm_count() < 1) return cudaErrorNoDevice;  // the work is cut by the SMs there are
+namespace attn {
+
+namespace {
+
+// what a call's arguments give, whichever kernel runs
+Params params_of(const dspark_tree_attention_args &a) {
     Params p{};
     p.a = a;
     p.H = a.H;
     p.G = a.Hq / a.H;
     p.masked = a.mask != nullptr;
     p.scale_log2 = a.scale * kLog2e;
+    return p;
+}
+
+// units of kSimtLines lines, for the kernels on the CUDA cores
+void cut_for_simt(Params &p) {
+    p.heads = p.G < kLines ? p.G : kLines;
+    p.subs = (p.G + p.heads - 1) / p.heads;
+    p.block_rows = kLines / p.heads;
+    p.lines = p.block_rows * p.heads;
+    p.stride = p.a.D;
+    p.small_rows = p.block_rows;
+    p.small_places = p.large_places = div_by(1);
+    p.page = div_by(p.a.page);
+}
+
+// the general kernel and the join
+template <bool kFour>
+cudaError_t launch_simt(Params &p, void *ws, cudaStream_t s) {
+    const dspark_tree_attention_args &a = p.a;
+    p.tile_log2 = kTileLog2;
+    p.unit_cost = 1;
+    const int grid = simt_grid(a.D);
+    p.ctas = div_by(grid);
+    carve(p, ws, grid);
+    const size_t smem = smem_bytes(a.D);
+    const bool wide = a.D > 128;
+    cudaError_t e;
+    if (a.dtype == DSPARK_BF16)
+        e = wide ? launch_as<__nv_bfloat16, 2, kFour>(p, grid, smem, s) : launch_as<__nv_bfloat16, 1, kFour>(p, grid, smem, s);
+    else
+        e = wide ? launch_as<float, 2, kFour>(p, grid, smem, s) : launch_as<float, 1, kFour>(p, grid, smem, s);
+    return e == cudaSuccess ? launch_join(p, grid, s) : e;
+}
+
+}  // namespace
+
+}  // namespace attn
+
+cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws, cudaStream_t s) {
+    using namespace attn;
+    if (sm_count() < 1) return cudaErrorNoDevice;  // the work is cut by the SMs there are
+    Params p = params_of(a);
     if (tc_supported(a)) {
         p.heads = p.G;
         p.subs = 1;
@@ -406,14 +465,7 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws,
         cudaError_t e = launch_tc(p, grid, s);
         return e == cudaSuccess ? launch_join(p, grid, s) : e;
     }
-    p.heads = p.G < kLines ? p.G : kLines;
-    p.subs = (p.G + p.heads - 1) / p.heads;
-    p.block_rows = kLines / p.heads;
-    p.lines = p.block_rows * p.heads;
-    p.stride = a.D;
-    p.small_rows = p.block_rows;
-    p.small_places = p.large_places = div_by(1);
-    p.page = div_by(a.page);
+    cut_for_simt(p);
     if (f32_supported(a)) {
         const int grid = f32_grid();
         p.ctas = div_by(grid);
@@ -421,22 +473,21 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws,
         cudaError_t e = launch_f32(p, grid, s);
         return e == cudaSuccess ? launch_join(p, grid, s) : e;
     }
-    p.tile_log2 = kTileLog2;
-    p.unit_cost = 1;
     const int es = a.dtype == DSPARK_BF16 ? 2 : 4;
     p.vec = a.D % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.k_cache) | reinterpret_cast<uintptr_t>(a.v_cache)) & (4 * es - 1)) == 0;
-    const int grid = simt_grid(a.D);
-    p.ctas = div_by(grid);
-    carve(p, ws, grid);
-    const size_t smem = smem_bytes(a.D);
-    const bool wide = a.D > 128;
-    cudaError_t e;
-    if (a.dtype == DSPARK_BF16)
-        e = wide ? launch_as<__nv_bfloat16, 2>(p, grid, smem, s) : launch_as<__nv_bfloat16, 1>(p, grid, smem, s);
-    else
-        e = wide ? launch_as<float, 2>(p, grid, smem, s) : launch_as<float, 1>(p, grid, smem, s);
-    if (e != cudaSuccess) return e;
-    return launch_join(p, grid, s);
+    return launch_simt<false>(p, ws, s);
+}
+
+size_t tree_attention4_ws_bytes(const dspark_tree_attention_args &a) {
+    return attn::workspace_bytes(attn::simt_grid(a.D), attn::kLines, a.D);
+}
+
+cudaError_t launch_tree_attention4(const dspark_tree_attention_args &a, void *ws, cudaStream_t s) {
+    using namespace attn;
+    if (sm_count() < 1) return cudaErrorNoDevice;
+    Params p = params_of(a);
+    cut_for_simt(p);
+    return launch_simt<true>(p, ws, s);
 }
 
 }  // namespace dspark

@@ -158,6 +158,18 @@ struct Outputs {
         }
         return add(name, gpu.empty(dt, shape));
     }
+    // the same for heads: the caller's may be a view whose D elements are adjacent
+    void *heads(const Gpu &gpu, const char *name, at::ScalarType dt, std::initializer_list<int64_t> shape, int64_t *row, int64_t *head) {
+        if (!own) {
+            PyObject *o = PyDict_GetItemString(dict, name);
+            if (!o || o == Py_None) raise(PyExc_KeyError, "%s", name);
+            return const_cast<void *>(gpu.heads(name, o, dt, shape, row, head));
+        }
+        const int64_t *n = shape.begin();
+        *row = n[1] * n[2];
+        *head = n[2];
+        return add(name, gpu.empty(dt, shape));
+    }
     struct Part {
         const char *name;
         int64_t n;
@@ -264,31 +276,121 @@ PyObject *cache_store(PyObject *const *x, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
-// q k_cache v_cache table lens row_start mask scale max_rows out ws err; size_only: the
-// workspace's bytes and no call
-PyObject *tree_attention_as(PyObject *const *x, Py_ssize_t n, bool size_only) {
-    count_args(n, 12);
-    const at::Tensor &cache = dims("k_cache", x[1], 4), &q = dims("q", x[0], 3), &table = dims("table", x[3], 2);
+float number(PyObject *o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+    return (float)v;
+}
+
+// q k v pos freq q_weight k_weight eps interleaved slot k_cache v_cache out err
+PyObject *rope_store(PyObject *const *x, Py_ssize_t n) {
+    count_args(n, 14);
+    const bool queries = x[0] != Py_None, keys = x[1] != Py_None, cached = x[9] != Py_None;
+    if (!queries && !keys) raise(PyExc_ValueError, "%s", "neither queries nor keys are given");
+    const at::Tensor &first = dims(queries ? "q" : "k", x[queries ? 0 : 1], 3);
+    const Gpu gpu(queries ? "q" : "k", first);
+    const c10::cuda::CUDAGuard guard(gpu.device);
+    const at::ScalarType dt = first.scalar_type();
+    const int64_t N = first.size(0), D = first.size(2);
+    dspark_rope_store_args a{};
+    a.N = small("N", N), a.D = small("D", D);
+    a.dtype = dtype_code(queries ? "q" : "k", first);
+    a.eps = number(x[7]);
+    a.interleaved = PyObject_IsTrue(x[8]);
+    if (a.interleaved < 0) throw Raised{};
+    a.pos = i32(gpu.want("pos", x[3], I32, {N}));
+    a.rot = small("rot", 2 * dims("freq", x[4], 1).size(0));
+    a.freq = f32(gpu.want("freq", x[4], F32));
+    a.q_weight = gpu.maybe("q_weight", x[5], dt, {D});
+    a.k_weight = gpu.maybe("k_weight", x[6], dt, {D});
+    a.err = i32(gpu.maybe("err", x[13], I32));
+    if (queries) {
+        a.Hq = small("Hq", first.size(1));
+        a.q = gpu.heads("q", x[0], dt, {N, a.Hq, D}, &a.q_row, &a.q_head);
+    }
+    if (keys) {
+        a.H = small("H", dims("k", x[1], 3).size(1));
+        a.k = gpu.heads("k", x[1], dt, {N, a.H, D}, &a.k_row, &a.k_head);
+    }
+    if (cached) {
+        if (!keys) raise(PyExc_ValueError, "%s", "slots are given without keys");
+        const at::Tensor &cache = dims("k_cache", x[10], 4);
+        dims("v", x[2], 3);
+        a.v = gpu.heads("v", x[2], dt, {N, a.H, D}, &a.v_row, &a.v_head);
+        a.slot = i32(gpu.want("slot", x[9], I32, {N}));
+        const int64_t pages = cache.size(0), page = cache.size(2);
+        a.page = small("page", page), a.n_pages = small("n_pages", pages);
+        a.k_cache = gpu.want("k_cache", x[10], dt, {pages, a.H, page, D});
+        a.v_cache = gpu.want("v_cache", x[11], dt, {pages, a.H, page, D});
+    } else if (x[10] != Py_None || x[11] != Py_None) {
+        raise(PyExc_ValueError, "%s", "caches are given without slots");
+    }
+    Outputs out(x[12]);
+    if (queries) a.q_out = out.heads(gpu, "q", dt, {N, a.Hq, D}, &a.q_out_row, &a.q_out_head);
+    if (keys && !cached) a.k_out = out.heads(gpu, "k", dt, {N, a.H, D}, &a.k_out_row, &a.k_out_head);
+    check(dspark_rope_store(&a, gpu.stream()));
+    return out.take();
+}
+
+// tokens of a page of a cache in 4 bits [n_pages, H, page * D * 9 / 16]
+int64_t page_of(const char *name, const at::Tensor &cache, int64_t D) {
+    if (D < 16 || D % 16 || cache.size(2) % (D / 16 * 9)) raise(PyExc_ValueError, "pages of %s are not whole tokens of this head size", name);
+    return cache.size(2) / (D / 16 * 9);
+}
+
+// k v slot k_cache v_cache values out err
+PyObject *cache_store4(PyObject *const *x, Py_ssize_t n) {
+    count_args(n, 8);
+    const at::Tensor &cache = dims("k_cache", x[3], 3), &k = dims("k", x[0], 3);
     const Gpu gpu("k_cache", cache);
     const c10::cuda::CUDAGuard guard(gpu.device);
-    const at::ScalarType dt = cache.scalar_type();
+    const at::ScalarType dt = k.scalar_type();
+    const int64_t N = k.size(0), pages = cache.size(0), H = cache.size(1), D = k.size(2);
+    dspark_cache_store4_args a{};
+    a.N = small("N", N), a.H = small("H", H), a.D = small("D", D), a.n_pages = small("n_pages", pages);
+    a.page = small("page", page_of("k_cache", cache, D));
+    a.dtype = dtype_code("k", k);
+    dims("v", x[1], 3);
+    a.k = gpu.heads("k", x[0], dt, {N, H, D}, &a.k_row, &a.k_head);
+    a.v = gpu.heads("v", x[1], dt, {N, H, D}, &a.v_row, &a.v_head);
+    a.slot = i32(gpu.want("slot", x[2], I32, {N}));
+    a.k_cache = static_cast<uint8_t *>(gpu.want("k_cache", x[3], at::kByte));
+    a.v_cache = static_cast<uint8_t *>(gpu.want("v_cache", x[4], at::kByte, {pages, H, cache.size(2)}));
+    a.err = i32(gpu.maybe("err", x[7], I32));
+    const int values = PyObject_IsTrue(x[5]);
+    if (values < 0) throw Raised{};
+    if (!values && x[6] == Py_None) {
+        check(dspark_cache_store4(&a, gpu.stream()));
+        Py_RETURN_NONE;
+    }
+    Outputs out(x[6]);
+    a.k_out = out.get(gpu, "k", dt, {N, H, D});
+    a.v_out = out.get(gpu, "v", dt, {N, H, D});
+    check(dspark_cache_store4(&a, gpu.stream()));
+    return out.take();
+}
+
+// q k_cache v_cache table lens row_start mask scale max_rows out ws err; size_only: the
+// workspace's bytes and no call; four: caches in 4 bits
+PyObject *tree_attention_as(PyObject *const *x, Py_ssize_t n, bool size_only, bool four) {
+    count_args(n, 12);
+    const at::Tensor &cache = dims("k_cache", x[1], four ? 3 : 4), &q = dims("q", x[0], 3), &table = dims("table", x[3], 2);
+    const Gpu gpu("k_cache", cache);
+    const c10::cuda::CUDAGuard guard(gpu.device);
+    const at::ScalarType dt = four ? q.scalar_type() : cache.scalar_type(), held = four ? at::kByte : dt;
     const int64_t N = q.size(0), Hq = q.size(1), R = table.size(0);
-    const int64_t pages = cache.size(0), H = cache.size(1), page = cache.size(2), D = cache.size(3);
+    const int64_t pages = cache.size(0), H = cache.size(1), D = four ? q.size(2) : cache.size(3);
+    const int64_t page = four ? page_of("k_cache", cache, D) : cache.size(2);
     dspark_tree_attention_args a{};
     a.R = small("R", R), a.N = small("N", N), a.Hq = small("Hq", Hq), a.H = small("H", H), a.D = small("D", D);
     a.page = small("page", page), a.n_pages = small("n_pages", pages), a.max_pages = small("max_pages", table.size(1));
-    a.dtype = dtype_code("k_cache", cache);
+    a.dtype = four ? dtype_code("q", q) : dtype_code("k_cache", cache);
     a.max_rows = integer("max_rows", x[8]);
-    if (x[7] != Py_None) {
-        const double scale = PyFloat_AsDouble(x[7]);
-        if (scale == -1.0 && PyErr_Occurred()) throw Raised{};
-        a.scale = (float)scale;
-    } else {
-        a.scale = D > 0 ? (float)(1.0 / std::sqrt((double)D)) : 1.f;
-    }
+    if (x[7] != Py_None) a.scale = number(x[7]);
+    else a.scale = D > 0 ? (float)(1.0 / std::sqrt((double)D)) : 1.f;
     a.q = gpu.heads("q", x[0], dt, {N, Hq, D}, &a.q_row, &a.q_head);
-    a.k_cache = gpu.want("k_cache", x[1], dt);
-    a.v_cache = gpu.want("v_cache", x[2], dt, {pages, H, page, D});
+    a.k_cache = gpu.want("k_cache", x[1], held);
+    a.v_cache = four ? gpu.want("v_cache", x[2], held, {pages, H, cache.size(2)}) : gpu.want("v_cache", x[2], held, {pages, H, page, D});
     a.table = i32(gpu.want("table", x[3], I32));
     a.len = i32(gpu.want("lens", x[4], I32, {R}));
     a.row_start = i32(gpu.want("row_start", x[5], I32, {R + 1}));
@@ -297,7 +399,7 @@ PyObject *tree_attention_as(PyObject *const *x, Py_ssize_t n, bool size_only) {
         a.mask = static_cast<uint64_t *>(gpu.want("mask", x[6], I64, {N, a.W}));
     }
     a.err = i32(gpu.maybe("err", x[11], I32));
-    const size_t bytes = dspark_tree_attention_workspace_size(&a);
+    const size_t bytes = four ? dspark_tree_attention4_workspace_size(&a) : dspark_tree_attention_workspace_size(&a);
     if (size_only) return PyLong_FromSize_t(bytes);
     Outputs out(x[9]);
     a.out = out.get(gpu, "out", dt, {N, Hq, D});
@@ -316,11 +418,13 @@ PyObject *tree_attention_as(PyObject *const *x, Py_ssize_t n, bool size_only) {
         }
         ws = t.data_ptr();
     }
-    check(dspark_tree_attention(&a, ws, gpu.stream()));
+    check(four ? dspark_tree_attention4(&a, ws, gpu.stream()) : dspark_tree_attention(&a, ws, gpu.stream()));
     return out.take();
 }
-PyObject *tree_attention(PyObject *const *x, Py_ssize_t n) { return tree_attention_as(x, n, false); }
-PyObject *tree_attention_workspace_size(PyObject *const *x, Py_ssize_t n) { return tree_attention_as(x, n, true); }
+PyObject *tree_attention(PyObject *const *x, Py_ssize_t n) { return tree_attention_as(x, n, false, false); }
+PyObject *tree_attention_workspace_size(PyObject *const *x, Py_ssize_t n) { return tree_attention_as(x, n, true, false); }
+PyObject *tree_attention4(PyObject *const *x, Py_ssize_t n) { return tree_attention_as(x, n, false, true); }
+PyObject *tree_attention4_workspace_size(PyObject *const *x, Py_ssize_t n) { return tree_attention_as(x, n, true, true); }
 
 // T row_start tok mask hist hist_len prompt_len rep freq pres bias_start bias_id bias_val allow allow_row out err
 PyObject *logit_rules(PyObject *const *x, Py_ssize_t n) {
@@ -409,6 +513,10 @@ PyMethodDef g_methods[] = {method<page_map>("page_map"),
                            method<cache_store>("cache_store"),
                            method<tree_attention>("tree_attention"),
                            method<tree_attention_workspace_size>("tree_attention_workspace_size"),
+                           method<rope_store>("rope_store"),
+                           method<cache_store4>("cache_store4"),
+                           method<tree_attention4>("tree_attention4"),
+                           method<tree_attention4_workspace_size>("tree_attention4_workspace_size"),
                            method<logit_rules>("logit_rules"),
                            method<set_errors>("set_errors"),
                            {nullptr, nullptr, 0, nullptr}};

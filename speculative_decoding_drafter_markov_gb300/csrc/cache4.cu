@@ -1,0 +1,152 @@
+// cache4.cu -- the write of the rows' keys and values into a cache of 4 bits.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "cache4.cuh"
+#include "common.cuh"
+#include "paged.cuh"
+#include "target.h"
+
+namespace dspark {
+
+namespace {
+
+// A thread has 8 elements of a row -- keys or values, head and columns are found once --
+// and takes them from kRows rows, all reads under way together; its neighbour has the
+// other 8 of the 16 that share a scale.  Reads, codes and the values given back are
+// adjacent among the threads of a warp.
+constexpr int kThreads = 256;
+
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+    uint4 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void load_each(const __nv_bfloat16 *p) {
+        const unsigned short *u = reinterpret_cast<const unsigned short *>(p);
+        v.x = u[0] | (unsigned)u[1] << 16, v.y = u[2] | (unsigned)u[3] << 16;
+        v.z = u[4] | (unsigned)u[5] << 16, v.w = u[6] | (unsigned)u[7] << 16;
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+    // n s is a bf16 number: its high half is all of it
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&x)[8]) {
+        unsigned w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __byte_perm(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]), 0x7632);
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    static __device__ __forceinline__ float whole(float x, float, float inv) { return cache4::whole_of_bf16(x, inv); }
+};
+template <>
+struct Eight<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = __ldcs(reinterpret_cast<const float4 *>(p));
+        b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+    }
+    __device__ __forceinline__ void load_each(const float *p) {
+        a = make_float4(p[0], p[1], p[2], p[3]);
+        b = make_float4(p[4], p[5], p[6], p[7]);
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+    static __device__ __forceinline__ void store(float *p, const float (&x)[8]) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    }
+    static __device__ __forceinline__ float whole(float x, float s, float inv) { return cache4::whole_of(x, s, inv); }
+};
+
+template <typename T, bool kWide, int kRows>
+__global__ void __launch_bounds__(kThreads) cache_store4_kernel(const dspark_cache_store4_args a, const Page page) {
+    after_predecessor();
+    const int per_head = a.D / 8, per_row = a.H * per_head;
+    int piece = blockIdx.y * kThreads + threadIdx.x;
+    const bool in = piece < 2 * per_row;  // (per_row is even: a pair of threads is in or out together)
+    const bool values = piece >= per_row;
+    if (values) piece -= per_row;
+    const int h = piece / per_head, e = (piece - h * per_head) * 8;
+    const T *src = static_cast<const T *>(values ? a.v : a.k) + (values ? a.v_head : a.k_head) * h + e;
+    const long long row = values ? a.v_row : a.k_row;
+    unsigned char *cache = values ? a.v_cache : a.k_cache;
+    T *held = static_cast<T *>(values ? a.v_out : a.k_out);
+    const unsigned slots = slots_of(a.n_pages, a.page);
+    const int row0 = blockIdx.x * kRows;
+    int slot[kRows];
+    Eight<T> v[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) slot[i] = in && row0 + i < a.N ? a.slot[row0 + i] : -1;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        slot[i] = checked_slot(slot[i], slots, a.err);
+        if (slot[i] < 0) continue;
+        if (kWide) v[i].load(src + (row0 + i) * row);
+        else v[i].load_each(src + (row0 + i) * row);
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        float x[8], most = 0.f;
+        if (slot[i] >= 0) {
+            v[i].get(x);
+            bool odd = false;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                most = fmaxf(most, fabsf(x[k]));
+                odd |= !(fabsf(x[k]) < INFINITY);
+            }
+            if (odd) most = INFINITY;  // the maximum skips a NaN
+        }
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        if (slot[i] < 0) continue;
+        const unsigned byte = cache4::scale_byte(most);
+        const float s = cache4::scale_of(byte), inv = __frcp_rn(s);
+        unsigned word = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float n = Eight<T>::whole(x[k], s, inv);
+            word |= (__float_as_uint(n + 12582920.f) & 15u) << cache4::code_shift(k);  // 1.5 2^23 + 8
+            x[k] = n * s;
+        }
+        if (byte == cache4::kNoNumbers) word = 0x88888888u;
+        const int pg = (int)page.of(slot[i]), off = slot[i] - pg * a.page;
+        unsigned char *at = cache + ((long long)pg * a.H + h) * cache4::page_bytes(a.page, a.D);
+        *reinterpret_cast<unsigned *>(at + (long long)off * (a.D / 2) + e / 2) = word;
+        if (e % cache4::kGroup == 0) at[cache4::code_bytes(a.page, a.D) + (long long)off * (a.D / 16) + e / 16] = (unsigned char)byte;
+        if (held) {
+            if (byte == cache4::kNoNumbers) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = s;
+            }
+            Eight<T>::store(held + (row0 + i) * ((long long)a.H * a.D) + h * a.D + e, x);
+        }
+    }
+}
+
+template <typename T, bool kWide>
+cudaError_t store_as(const dspark_cache_store4_args &a, const Page &page, cudaStream_t s) {
+    const int pieces = 2 * a.H * (a.D / 8), y = (pieces + kThreads - 1) / kThreads;
+    // four rows a thread where that leaves every SM a few CTAs, else one
+    const bool many = (long long)a.N * y >= 4ll * 4 * sm_count();
+    return many ? launch_close(cache_store4_kernel<T, kWide, 4>, dim3((a.N + 3) / 4, y), kThreads, 0, s, a, page)
+                : launch_close(cache_store4_kernel<T, kWide, 1>, dim3(a.N, y), kThreads, 0, s, a, page);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_store4(const dspark_cache_store4_args &a, cudaStream_t s) {
+    const int es = a.dtype == DSPARK_BF16 ? 2 : 4;
+    const uintptr_t all = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+                          (uintptr_t)((a.k_row | a.k_head | a.v_row | a.v_head) * es);
+    const Page page = page_of_size(a.page);
+    const bool wide = (all & 15) == 0;
+    if (a.dtype == DSPARK_BF16) return wide ? store_as<__nv_bfloat16, true>(a, page, s) : store_as<__nv_bfloat16, false>(a, page, s);
+    return wide ? store_as<float, true>(a, page, s) : store_as<float, false>(a, page, s);
+}
+
+}  // namespace dspark

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "paged.cuh"
 #include "target.h"
 
 namespace dspark {
@@ -43,13 +44,6 @@ __device__ __forceinline__ int holder(const int *sum, int R, int k) {
     }
     return lo;
 }
-
-// division by the page: a shift where it is a power of two
-struct Page {
-    unsigned size;
-    int shift;  // or -1
-    __device__ __forceinline__ unsigned of(unsigned t) const { return shift >= 0 ? t >> shift : t / size; }
-};
 
 // pages of a request; the sum of two non-negative 32-bit sizes fits 32 bits unsigned
 __device__ __forceinline__ unsigned need_of(const dspark_page_map_args &a, const Page &page, int r) {
@@ -267,8 +261,6 @@ cudaError_t store_as(const dspark_cache_store_args &a, const Page &page, int es,
     return many ? launch_close(cache_store_kernel<Vec, 8>, dim3((a.N + 7) / 8, y), kStoreThreads, 0, s, a, page, es)
                 : launch_close(cache_store_kernel<Vec, 1>, dim3(a.N, y), kStoreThreads, 0, s, a, page, es);
 }
-
-Page page_of_size(int size) { return Page{(unsigned)size, (size & (size - 1)) == 0 ? __builtin_ctz((unsigned)size) : -1}; }
 
 }  // namespace
 

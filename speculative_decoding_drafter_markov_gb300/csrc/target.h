@@ -29,8 +29,13 @@ __device__ __forceinline__ void after_predecessor() { asm volatile("griddepcontr
 
 cudaError_t launch_page_map(const dspark_page_map_args &a, cudaStream_t s);
 cudaError_t launch_cache_store(const dspark_cache_store_args &a, cudaStream_t s);
+cudaError_t launch_rope_store(const dspark_rope_store_args &a, cudaStream_t s);
+cudaError_t launch_cache_store4(const dspark_cache_store4_args &a, cudaStream_t s);
 size_t tree_attention_ws_bytes(const dspark_tree_attention_args &a);
 cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws, cudaStream_t s);
+// over caches in 4 bits
+size_t tree_attention4_ws_bytes(const dspark_tree_attention_args &a);
+cudaError_t launch_tree_attention4(const dspark_tree_attention_args &a, void *ws, cudaStream_t s);
 cudaError_t launch_logit_rules(const dspark_logit_rules_args &a, cudaStream_t s);
 
 }  // namespace dspark
