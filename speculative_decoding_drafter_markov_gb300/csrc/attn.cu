@@ -391,6 +391,9 @@ cudaError_t launch_join(const Params &p, int grid, cudaStream_t s) {
 
 }  // namespace attn
 
+// (of a cache in 4 bits too: the same two ways of cutting)
+size_t tree_attention4_ws_bytes(const dspark_tree_attention_args &a) { return tree_attention_ws_bytes(a); }
+
 size_t tree_attention_ws_bytes(const dspark_tree_attention_args &a) {
     // enough for either kernel: which one runs also depends on the pointers
     const size_t simt = attn::workspace_bytes(attn::simt_grid(a.D), attn::kLines, a.D);
@@ -414,6 +417,15 @@ Params params_of(const dspark_tree_attention_args &a) {
     p.masked = a.mask != nullptr;
     p.scale_log2 = a.scale * kLog2e;
     return p;
+}
+
+// units of one or two operands of the tensor cores
+void cut_for_tc(Params &p, void *ws, int grid) {
+    p.heads = p.G;
+    p.subs = 1;
+    tc_shape(p.a, &p.block_rows, &p.lines, &p.stride);
+    p.mixed = 1;
+    carve(p, ws, grid);
 }
 
 // units of kSimtLines lines, for the kernels on the CUDA cores
@@ -456,12 +468,8 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws,
     if (sm_count() < 1) return cudaErrorNoDevice;  // the work is cut by the SMs there are
     Params p = params_of(a);
     if (tc_supported(a)) {
-        p.heads = p.G;
-        p.subs = 1;
-        tc_shape(a, &p.block_rows, &p.lines, &p.stride);
-        p.mixed = 1;
         const int grid = sm_count();
-        carve(p, ws, grid);
+        cut_for_tc(p, ws, grid);
         cudaError_t e = launch_tc(p, grid, s);
         return e == cudaSuccess ? launch_join(p, grid, s) : e;
     }
@@ -478,14 +486,17 @@ cudaError_t launch_tree_attention(const dspark_tree_attention_args &a, void *ws,
     return launch_simt<false>(p, ws, s);
 }
 
-size_t tree_attention4_ws_bytes(const dspark_tree_attention_args &a) {
-    return attn::workspace_bytes(attn::simt_grid(a.D), attn::kLines, a.D);
-}
 
 cudaError_t launch_tree_attention4(const dspark_tree_attention_args &a, void *ws, cudaStream_t s) {
     using namespace attn;
     if (sm_count() < 1) return cudaErrorNoDevice;
     Params p = params_of(a);
+    if (tc4_supported(a)) {
+        const int grid = sm_count();
+        cut_for_tc(p, ws, grid);
+        cudaError_t e = launch_tc4(p, grid, s);
+        return e == cudaSuccess ? launch_join(p, grid, s) : e;
+    }
     cut_for_simt(p);
     return launch_simt<true>(p, ws, s);
 }

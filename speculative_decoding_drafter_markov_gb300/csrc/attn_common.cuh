@@ -93,7 +93,10 @@ void carve(Params &p, void *ws, int grid);
 // the tensor-core kernel: one CTA per SM
 bool tc_supported(const dspark_tree_attention_args &a);
 void tc_shape(const dspark_tree_attention_args &a, int *block_rows, int *lines, int *stride);
-cudaError_t launch_tc(Params p, int grid, cudaStream_t s);
+cudaError_t launch_tc(const Params &p, int grid, cudaStream_t s);
+// over a cache in 4 bits, cut in the same way
+bool tc4_supported(const dspark_tree_attention_args &a);
+cudaError_t launch_tc4(const Params &p, int grid, cudaStream_t s);
 // the fp32 kernel: units of kSimtLines lines, as the general CUDA-core kernel
 constexpr int kSimtLines = 16;
 bool f32_supported(const dspark_tree_attention_args &a);
