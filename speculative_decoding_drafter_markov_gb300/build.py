@@ -21,7 +21,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libdspark.so")
-SOURCES = ["abi.cu", "attn.cu", "attn4_tc.cu", "attn_f32.cu", "attn_tc.cu", "cache4.cu", "diag.cu", "draft.cu", "draft_tc.cu", "gemm_tc.cu", "paged.cu", "rope.cu", "rules.cu",
+SOURCES = ["abi.cu", "attn.cu", "attn4_mma.cu", "attn4_tc.cu", "attn_f32.cu", "attn_tc.cu", "cache4.cu", "diag.cu", "draft.cu", "draft_tc.cu", "gemm_tc.cu", "paged.cu", "rope.cu", "rules.cu",
            "sched.cu", "sts.cu", "train_loss.cu", "verify.cu", "verify_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 TU_FLAGS = {}

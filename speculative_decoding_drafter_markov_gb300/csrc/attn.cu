@@ -428,6 +428,17 @@ void cut_for_tc(Params &p, void *ws, int grid) {
     carve(p, ws, grid);
 }
 
+// units of 16 or 32 lines, of which a request has as few as the host's hint says
+void cut_for_mma(Params &p, void *ws, int grid) {
+    const int most = p.a.max_rows * p.G <= 16 ? 16 : 32;
+    p.heads = p.G < most ? p.G : most;
+    p.subs = (p.G + p.heads - 1) / p.heads;
+    p.block_rows = most / p.heads;
+    p.lines = p.block_rows * p.heads;
+    p.stride = p.a.D;
+    carve(p, ws, grid);
+}
+
 // units of kSimtLines lines, for the kernels on the CUDA cores
 void cut_for_simt(Params &p) {
     p.heads = p.G < kLines ? p.G : kLines;
@@ -493,8 +504,10 @@ cudaError_t launch_tree_attention4(const dspark_tree_attention_args &a, void *ws
     Params p = params_of(a);
     if (tc4_supported(a)) {
         const int grid = sm_count();
-        cut_for_tc(p, ws, grid);
-        cudaError_t e = launch_tc4(p, grid, s);
+        const bool few = (long long)a.max_rows * p.G <= 64;
+        if (few) cut_for_mma(p, ws, grid);
+        else cut_for_tc(p, ws, grid);
+        cudaError_t e = few ? launch_mma4(p, grid, s) : launch_tc4(p, grid, s);
         return e == cudaSuccess ? launch_join(p, grid, s) : e;
     }
     cut_for_simt(p);
