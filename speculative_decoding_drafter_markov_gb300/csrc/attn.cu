@@ -428,9 +428,9 @@ void cut_for_tc(Params &p, void *ws, int grid) {
     carve(p, ws, grid);
 }
 
-// units of 16 or 32 lines, of which a request has as few as the host's hint says
+// units of 8, 16 or 32 lines, as few as the host's hint says that a request has
 void cut_for_mma(Params &p, void *ws, int grid) {
-    const int most = p.a.max_rows * p.G <= 16 ? 16 : 32;
+    const int lines = p.a.max_rows * p.G, most = lines <= 8 ? 8 : lines <= 16 ? 16 : 32;
     p.heads = p.G < most ? p.G : most;
     p.subs = (p.G + p.heads - 1) / p.heads;
     p.block_rows = most / p.heads;
@@ -504,7 +504,7 @@ cudaError_t launch_tree_attention4(const dspark_tree_attention_args &a, void *ws
     Params p = params_of(a);
     if (tc4_supported(a)) {
         const int grid = sm_count();
-        const bool few = (long long)a.max_rows * p.G <= 64;
+        const bool few = (long long)a.max_rows * p.G <= 16;
         if (few) cut_for_mma(p, ws, grid);
         else cut_for_tc(p, ws, grid);
         cudaError_t e = few ? launch_mma4(p, grid, s) : launch_tc4(p, grid, s);

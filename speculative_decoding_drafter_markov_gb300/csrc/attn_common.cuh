@@ -97,7 +97,7 @@ cudaError_t launch_tc(const Params &p, int grid, cudaStream_t s);
 // over a cache in 4 bits, cut in the same way
 bool tc4_supported(const dspark_tree_attention_args &a);
 cudaError_t launch_tc4(const Params &p, int grid, cudaStream_t s);
-// the same for units of 16 or 32 lines (what launch_tc4 takes, it takes)
+// the same for units of 8, 16 or 32 lines (what launch_tc4 takes, it takes)
 cudaError_t launch_mma4(Params p, int grid, cudaStream_t s);
 // the fp32 kernel: units of kSimtLines lines, as the general CUDA-core kernel
 constexpr int kSimtLines = 16;

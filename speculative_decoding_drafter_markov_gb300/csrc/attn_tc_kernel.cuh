@@ -31,21 +31,24 @@ template <int DP_, int NQ_, bool FOUR_ = false>
 struct Shape {
     static constexpr int DP = DP_, NQ = NQ_;
     static constexpr bool FOUR = FOUR_;
-    static constexpr int kThreads = FOUR ? 512 : 384;
-    static constexpr int kReaders = FOUR ? 15 : 11;  // of pieces: two copy warps, the MMA warp, eight softmax warps, four that unpack
+    static constexpr int kThreads = FOUR ? 640 : 384;
+    static constexpr int kReaders = FOUR ? 19 : 11;  // of pieces: two copy warps, the MMA warp, eight softmax warps, eight that unpack
     static constexpr int kCols = DP / 64;        // a row is copied in blocks of 64 columns
     static constexpr int kBlock = 128 * 128;     // 128 rows of 64 16-bit elements
     static constexpr int kSlot = kCols * kBlock;
     // ring slots: what 227 KB hold beside Q, and the packed tiles' ring
     static constexpr int NS = FOUR ? (DP == 128 ? 5 - NQ : 6) : (DP == 128 ? 7 - NQ : 12);
-    static constexpr int NP = FOUR ? (DP == 128 ? 6 : 12) : 0;
+    // packed tiles: a ring for keys and one for values, each filled by one warp and emptied by one
+    // group in its order (in a ring for both, a warp that is a round ahead of the other kind
+    // would take the phase before for the one that it waits for)
+    static constexpr int NP = FOUR ? (DP == 128 ? 3 : 6) : 0;
     static constexpr int kPacked = 128 * DP / 16 * 9;  // codes, then scales, of 128 tokens
     static constexpr int kOffRing = NQ * kSlot;
     static constexpr int kOffPacked = kOffRing + NS * kSlot;
-    static constexpr int kOffMl = kOffPacked + NP * kPacked;  // float2 [2][128]
+    static constexpr int kOffMl = kOffPacked + 2 * NP * kPacked;  // float2 [2][128]
     static constexpr int kOffPiece = kOffMl + 2 * 128 * 8;    // Piece [kQueue], 64 bytes each
     static constexpr int kOffBar = kOffPiece + 64 * kQueue;
-    static constexpr int kBars = 2 * NS + 2 * NP + 13 + 2 * kQueue;
+    static constexpr int kBars = 2 * NS + 4 * NP + 13 + 2 * kQueue;
     // The reference that a weight is relative to stands kLift below the maximum: a weight of fp16 then
     // keeps ones down to 2^-31 of the largest, and none passes 2^15.
     static constexpr float kLift = FOUR ? 7.f : 0.f;
@@ -171,95 +174,92 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&two);
 }
 
-// The role of the four warps that unpack tiles of a cache in 4 bits into the ring: keys as
-// the bf16 numbers that they are, values as the eighths of them in fp16 (the whole range of
-// n s, 2^-16 to 401408, is exact there, and the weights beside them may be fp16).
-// A code word has the elements 2 p and 2 p + 1 in nibble p of its halves, so a shift, a mask
-// and the exponent of 128 (of 1024 in fp16) make two numbers 128 + (n + 8) of it, and one
-// multiply-add two values: 136 s has eight bits (17 times 8 .. 15), so nothing is rounded.
-// 2.0 instructions an element; with them a warp's four rows of 64 bytes are read without
-// a conflict of banks, and the 16-byte pieces of 8 lanes fall on all banks: lanes of
-// the upper columns write their second piece first.
-template <typename C>
+// The role of the eight warps that unpack tiles of a cache in 4 bits into the ring, four of
+// them keys (kKeys) as the bf16 numbers that they are, four values as the eighths of them in
+// fp16 (the whole range of n s, 2^-16 to 401408, is exact there, and the weights beside them
+// may be fp16).  A lane has 16 elements of a row, a scale's, per turn.
+template <typename C, bool kKeys>
 __device__ __forceinline__ void unpack_tiles(unsigned char *smem, const dspark_tree_attention_args &a, int warp, const Waiter &wait,
                                              Queue &queue, uint64_t *copied, uint64_t *copy_free, uint64_t *full, uint64_t *empty,
                                              int op_rows) {
     constexpr int kLanes = C::DP / 16, kRows = 32 / kLanes, kTurns = 32 / kRows;  // lanes of a row, rows and turns of a warp
     const int lane = threadIdx.x & 31, g = lane % kLanes, row0 = 32 * warp + lane / kLanes;
-    const bool in = 16 * g < a.D, flip = C::DP == 128 && g >= 4;
+    const bool in = 16 * g < a.D;
+    // a turn is kRows (4 or 8) rows further: the swizzle of its 16-byte pieces is that of the turn before with bit 2 turned,
+    // or the same.  Lanes of the upper columns write their second piece first, so that eight lanes' pieces fall on all banks.
+    const bool flip = C::DP == 128 && g >= 4;
+    const int first = (g >> 2) * C::kBlock + row0 * 128;
+    const int piece0 = (((2 * g + (flip ? 1 : 0)) & 7) ^ (row0 & 7)) << 4, piece1 = piece0 ^ 16;
+    constexpr int kTurn = C::DP == 128 ? 64 : 0;
     const int code_row = a.D / 2, scale_row = a.D / 16;
     // columns beyond D: zeros in every slot, once
     if (!in) {
 #pragma unroll 1
         for (int i = 0; i < C::NS * kTurns; ++i) {
-            const int row = row0 + (i % kTurns) * kRows;
-            unsigned char *at = smem + C::kOffRing + (i / kTurns) * C::kSlot + (g >> 2) * C::kBlock + row * 128;
-            *reinterpret_cast<uint4 *>(at + ((((2 * g) & 7) ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4 *>(at + ((((2 * g + 1) & 7) ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+            unsigned char *at = smem + C::kOffRing + (i / kTurns) * C::kSlot + first + (i % kTurns) * kRows * 128;
+            const int turn = (i % kTurns) & 1 ? kTurn : 0;
+            *reinterpret_cast<uint4 *>(at + (piece0 ^ turn)) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4 *>(at + (piece1 ^ turn)) = make_uint4(0u, 0u, 0u, 0u);
         }
     }
-    uint32_t pos = 0;
+    uint32_t base = 0;
     Piece x;
     while (queue.read_warp(wait, x)) {
         const bool dual = C::NQ == 2 && x.n > op_rows;
         const int n = x.t1 - x.t0;
-        for (int i = 0; i < 2 * n; ++i, ++pos) {
-            // the ring's order: K0 V0 K1 V1 .., or K0 K1 V0 K2 V1 .. (see key_place)
-            const bool keys = dual ? !(i & 1) : i == 0 || (i < 2 * n - 1 && (i & 1));
-            const int from = pos % C::NP, slot = pos % C::NS;
-            if (!wait.warp(&copied[from], (pos / C::NP) & 1u)) return;
-            const unsigned char *packed = smem + C::kOffPacked + from * C::kPacked;
-            uint2 w[kTurns];
-            uint32_t b[kTurns];
-#pragma unroll
-            for (int t = 0; t < kTurns; ++t) {
-                const int row = row0 + t * kRows;
-                w[t] = make_uint2(0u, 0u);
-                b[t] = 0;
-                if (in) {
-                    w[t] = *reinterpret_cast<const uint2 *>(packed + row * code_row + 8 * g);
-                    b[t] = packed[kTile * code_row + row * scale_row + g];
-                }
-            }
+        for (int i = 0; i < n; ++i) {
+            const uint32_t pos = base + (kKeys ? key_place(i, dual) : value_place(i, n, dual)), item = base / 2 + i;
+            const int from = item % C::NP, slot = pos % C::NS;
+            if (!wait.warp(&copied[from], (item / C::NP) & 1u)) return;
+            const unsigned char *packed = smem + C::kOffPacked + ((kKeys ? 0 : C::NP) + from) * C::kPacked;
+            const unsigned char *code = packed + row0 * code_row + 8 * g, *scale = packed + kTile * code_row + row0 * scale_row + g;
+            // (Slots are given back in the ring's order, and items of one kind are three places apart at most, no
+            // more than there are slots: the phase before the one waited for has passed.)
             if (!wait.warp(&empty[slot], ((pos / C::NS) & 1u) ^ 1u)) return;
-            unsigned char *to = smem + C::kOffRing + slot * C::kSlot + (g >> 2) * C::kBlock;
+            unsigned char *to = smem + C::kOffRing + slot * C::kSlot + first;
+            // Two turns at a time and no more: the code of all roles has to stay in the SM's first instruction caches (with eight
+            // turns unrolled four of ten stalls were for instructions, and a tile took twice the time).
+#pragma unroll 1
+            for (int t0 = 0; t0 < kTurns; t0 += 2) {
+                uint2 w[2];
+                uint32_t b[2];
 #pragma unroll
-            for (int t = 0; t < kTurns; ++t) {
-                const int row = row0 + t * kRows;
-                uint32_t r[2][4];
-                const uint32_t word[2] = {flip ? w[t].y : w[t].x, flip ? w[t].x : w[t].y};
-                if (keys) {
-                    const uint32_t s1 = b[t] == cache4::kNoNumbers ? 0x7fc0u : (b[t] + (111u << 3)) << 4;
-                    const uint32_t s2 = s1 * 0x10001u;
-                    const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162 *>(&s2);
-                    const __nv_bfloat162 off = __hmul2(s, __floats2bfloat162_rn(-136.f, -136.f));
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t v = ((word[h] >> (4 * e)) & 0x000f000fu) | 0x43004300u;
-                            const __nv_bfloat162 y = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v), s, off);
-                            r[h][e] = *reinterpret_cast<const uint32_t *>(&y);
-                        }
-                } else {
-                    const float s1 = b[t] == cache4::kNoNumbers ? __uint_as_float(0x7fc00000u) : __uint_as_float((b[t] + (108u << 3)) << 20);
-                    const __half2 s = __floats2half2_rn(s1, s1);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t v = ((word[h] >> (4 * e)) & 0x000f000fu) | 0x64006400u;
-                            const __half2 y = __hmul2(__hadd2(*reinterpret_cast<const __half2 *>(&v), __floats2half2_rn(-1032.f, -1032.f)), s);
-                            r[h][e] = *reinterpret_cast<const uint32_t *>(&y);
-                        }
-                }
-                if (in) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int chunk = 2 * g + (flip ? 1 - h : h);
-                        *reinterpret_cast<uint4 *>(to + row * 128 + (((chunk & 7) ^ (row & 7)) << 4)) = make_uint4(r[h][0], r[h][1], r[h][2], r[h][3]);
+                for (int t = 0; t < 2; ++t) {
+                    w[t] = make_uint2(0u, 0u);
+                    b[t] = 0;
+                    if (in) {
+                        w[t] = *reinterpret_cast<const uint2 *>(code + t * kRows * code_row);
+                        b[t] = scale[t * kRows * scale_row];
                     }
                 }
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    uint32_t r[2][4];
+                    const uint32_t word[2] = {flip ? w[t].y : w[t].x, flip ? w[t].x : w[t].y};
+                    if (kKeys) {
+                        const uint32_t s = b[t] == cache4::kNoNumbers ? 0x7fc07fc0u : cache4::bf16_scales(b[t]);
+                        const uint32_t off = cache4::bf16_offset(s);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) r[h][e] = cache4::bf16_of(word[h], e, s, off);
+                    } else {
+                        const float s1 = b[t] == cache4::kNoNumbers ? NAN : cache4::eighth_of(b[t]);
+                        const uint32_t s = pack_half(s1, s1);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) r[h][e] = cache4::half_of(word[h] >> (8 * (e >> 1)), e & 1, s);
+                    }
+                    if (in) {
+                        const int turn = t & 1 ? kTurn : 0;
+                        *reinterpret_cast<uint4 *>(to + t * kRows * 128 + (piece0 ^ turn)) = make_uint4(r[0][0], r[0][1], r[0][2], r[0][3]);
+                        *reinterpret_cast<uint4 *>(to + t * kRows * 128 + (piece1 ^ turn)) = make_uint4(r[1][0], r[1][1], r[1][2], r[1][3]);
+                    }
+                }
+                code += 2 * kRows * code_row;
+                scale += 2 * kRows * scale_row;
+                to += 2 * kRows * 128;
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
@@ -268,6 +268,7 @@ __device__ __forceinline__ void unpack_tiles(unsigned char *smem, const dspark_t
                 tc::mbar_arrive(&copy_free[from]);
             }
         }
+        base += 2 * (uint32_t)n;
     }
 }
 
@@ -283,8 +284,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     uint64_t *half_done = p_ready + 4, *q_full = half_done + 2, *o_free = q_full + 1, *both = o_free + 1,
              *drain = both + 1, *o_last = drain + 1;
     uint64_t *queue_full = o_last + 1, *queue_empty = queue_full + kQueue;
-    // what the copies fill: the packed tiles' ring, or the ring itself
-    uint64_t *copied = C::FOUR ? queue_empty + kQueue : full, *copy_free = C::FOUR ? copied + C::NP : empty;
+    // what the copies fill: the packed tiles' rings (keys, values), or the ring itself
+    uint64_t *copied = C::FOUR ? queue_empty + kQueue : full, *copy_free = C::FOUR ? copied + 2 * C::NP : empty;
     constexpr int kCopies = C::FOUR ? C::NP : C::NS;
     Piece *pieces = reinterpret_cast<Piece *>(smem + C::kOffPiece);
     uint32_t *bad = reinterpret_cast<uint32_t *>(smem + C::kOffBad);
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             tc::mbar_init(&full[i], C::FOUR ? 4 : 1);
             tc::mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < C::NP; ++i) {
+        for (int i = 0; i < 2 * C::NP; ++i) {
             tc::mbar_init(&copied[i], 1);
             tc::mbar_init(&copy_free[i], 4);
         }
@@ -378,6 +379,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         const bool values = warp == 10;
         const CUtensorMap *map = values ? &tmV : &tmK;
         uint32_t base = 0;  // slots before the piece
+        if (C::FOUR && values) copied += C::NP, copy_free += C::NP;
+        unsigned char *ring = smem + (C::FOUR ? C::kOffPacked + (values ? C::NP * C::kPacked : 0) : C::kOffRing);
         // a lane copies one block of columns of one box, or its codes or its scales
         constexpr int kParts = C::FOUR ? 2 : C::kCols;
         const int bx = lane / kParts, col = lane % kParts;
@@ -395,7 +398,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             for (int t = 0; t < n; ++t) {
                 const int tok0 = (x.t0 + t) * kTile, tok = tok0 + bx * tp.box;
                 const int boxes = (min(kTile, x.tokens - tok0) + tp.box - 1) / tp.box;
-                const uint32_t pos = base + (values ? value_place(t, n, dual) : key_place(t, dual));
+                const uint32_t pos = C::FOUR ? base / 2 + t : base + (values ? value_place(t, n, dual) : key_place(t, dual));
                 const int slot = pos % kCopies;
                 int go = 1;
                 if (lane == 0) {
@@ -416,10 +419,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                         const int bytes = col ? a.D / 16 : a.D / 2;
                         const unsigned char *from = cache + ((long long)pg * a.H + x.head) * cache4::page_bytes(a.page, a.D) +
                                                     (col ? cache4::code_bytes(a.page, a.D) : 0) + (long long)(tok - in_table * a.page) * bytes;
-                        tc::bulk_load(smem + C::kOffPacked + slot * C::kPacked + (col ? kTile * (a.D / 2) : 0) + bx * tp.box * bytes, from,
+                        tc::bulk_load(ring + slot * C::kPacked + (col ? kTile * (a.D / 2) : 0) + bx * tp.box * bytes, from,
                                       (uint32_t)(tp.box * bytes), &copied[slot]);
                     } else {
-                        tc::tma_load_3d(smem + C::kOffRing + slot * C::kSlot + col * C::kBlock + bx * tp.box * 128, map,
+                        tc::tma_load_3d(ring + slot * C::kSlot + col * C::kBlock + bx * tp.box * 128, map,
                                         &full[slot], 64 * col, tok - in_table * a.page, pg * a.H + x.head);
                     }
                 }
@@ -519,7 +522,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         __syncwarp();
     } else if (C::FOUR && warp >= 12) {
         // ------------------------------------------------------------ 4 bits to 16
-        if constexpr (C::FOUR) unpack_tiles<C>(smem, a, warp - 12, wait, queue, copied, copy_free, full, empty, tp.op_rows);
+        if constexpr (C::FOUR) {
+            if (warp < 16) unpack_tiles<C, true>(smem, a, warp - 12, wait, queue, copied, copy_free, full, empty, tp.op_rows);
+            else unpack_tiles<C, false>(smem, a, warp - 16, wait, queue, copied + C::NP, copy_free + C::NP, full, empty, tp.op_rows);
+        }
     } else {
         // ------------------------------------------------------------ softmax
         const int w = warp >> 2, q = warp & 3, row = 32 * q + lane;
@@ -599,7 +605,78 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     const uint32_t s_half = s_tmem + 64 * half;
-                    if (active) {
+                    if (C::FOUR && active && tail) {
+                        // what a line does not see, and all that lines beyond the unit's hold, becomes -inf before the loop below
+#pragma unroll 1
+                        for (int c = 0; c < 64; c += 32) {
+                            float s[32];
+                            tc::tmem_ld32(s_half + c, s);
+                            tc::tmem_wait_ld();
+                            const uint32_t see = live ? seen_bits(words, 2 * a.W, tok0 + 64 * half + c - x.len, x.rows, j) : 0u;
+                            uint32_t hidden[32];
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) hidden[i] = __float_as_uint(see & (1u << i) ? s[i] : -INFINITY);
+                            tc::tmem_st32(s_half + c, hidden);
+                        }
+                        tc::tmem_wait_st();
+                    }
+                    if (C::FOUR && active) {
+                        // 96 registers a thread (the warps that unpack need their share) and little code: 32 columns at
+                        // a time, read from tensor memory for their maximum and again for their weights
+                        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+                        for (int c = 0; c < 64; c += 32) {
+                            float s[32];
+                            tc::tmem_ld32(s_half + c, s);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) mx[i & 1] = fmaxf(mx[i & 1], s[i]);
+                        }
+                        const float top = fmaxf(mx[0], mx[1]) * scale;
+                        const bool over = top > m + (kSlack + C::kLift);
+                        if (__any_sync(0xffffffffu, over)) {
+                            const float to = over ? top - C::kLift : m;
+                            const float f = to == -INFINITY ? 1.f : ex2(m - to);
+                            m = to;
+                            l *= f;
+                            if (u > 0 || half > 0) {  // else nothing is in O
+                                if (half == 1) ok = wait.warp(&half_done[w], count & 1u);
+                                tc::tc_fence_after();
+#pragma unroll 1
+                                for (int c = 0; c < C::DP; c += 16) {
+                                    uint32_t o[16];
+                                    tc::tmem_ld16(o_tmem + c, o);
+                                    tc::tmem_wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                    tc::tmem_st16(o_tmem + c, o);
+                                }
+                            }
+                        }
+                        const float ref = m == -INFINITY ? 0.f : m;
+                        const float2 by = {scale, scale}, off = {-ref, -ref};
+                        float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll 1
+                        for (int c = 0; c < 64; c += 32) {
+                            float s[32];
+                            uint32_t r[16];
+                            tc::tmem_ld32(s_half + c, s);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 arg = fma2({s[2 * i], s[2 * i + 1]}, by, off);
+                                const float2 e = {ex2(arg.x), ex2(arg.y)};
+                                sum[i & 1] = add2(sum[i & 1], e);
+                                r[i] = pack_half(e.x, e.y);
+                            }
+                            tc::tmem_st16(s_half + c / 2, r);  // over columns that were read
+                        }
+                        sum[0] = add2(sum[0], sum[1]);
+                        l += sum[0].x + sum[0].y;
+                        tc::tmem_wait_st();
+                        tc::tc_fence_before();
+                    }
+                    if (!C::FOUR && active) {
                         float s[64];
                         tc::tmem_ld32(s_half, s);
                         tc::tmem_ld32(s_half + 32, s + 32);
@@ -620,9 +697,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                             for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], s[i + c]);
                         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
                         if (u == 0 && half == 0) {
-                            m = top - C::kLift;
-                        } else if (__any_sync(0xffffffffu, top > m + (kSlack + C::kLift))) {
-                            const float to = top > m + (kSlack + C::kLift) ? top - C::kLift : m;
+                            m = top;
+                        } else if (__any_sync(0xffffffffu, top > m + kSlack)) {
+                            const float to = top > m + kSlack ? top : m;
                             const float f = to == -INFINITY ? 1.f : ex2(m - to);
                             m = to;
                             l *= f;
@@ -650,7 +727,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                             const float2 arg = fma2({s[2 * i], s[2 * i + 1]}, by, off);
                             const float2 e = {ex2(arg.x), ex2(arg.y)};
                             sum[i & 1] = add2(sum[i & 1], e);
-                            r[i] = C::FOUR ? pack_half(e.x, e.y) : pack(e.x, e.y);
+                            r[i] = pack(e.x, e.y);
                         }
                         tc::tmem_st32(s_half, r);
                         sum[0] = add2(sum[0], sum[1]);

@@ -54,5 +54,43 @@ __device__ __forceinline__ float whole_of_bf16(float x, float inv) {
     return fminf(fmaxf(__fadd_rn(__fadd_rn(t, 12582912.f), -12582912.f), -7.f), 7.f);  // 1.5 2^23
 }
 
+// ---------------------------------------------------------------- two values at a time
+// A code word has elements 2 p and 2 p + 1 of eight in nibble p of its halves, so a shift and a
+// mask with an exponent make two numbers of it, and one or two operations the values.
+
+// (x & mask) | bits, in one instruction
+template <uint32_t kMask, uint32_t kBits>
+__device__ __forceinline__ uint32_t mask_or(uint32_t x) {
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(x), "r"(kMask), "r"(kBits));
+    return y;
+}
+// s(b) twice in bf16, b <= 254: (b + 888) << 4 are its bits
+__device__ __forceinline__ uint32_t bf16_scales(uint32_t b) { return b * 0x00100010u + 0x37803780u; }
+// -136 s: 17 s 8, eight bits, so it is exact
+__device__ __forceinline__ uint32_t bf16_offset(uint32_t s) {
+    uint32_t y;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(s), "r"(0xc308c308u));
+    return y;
+}
+// values of nibble p in bf16: 128 + (n + 8) by its bits, times s, minus 136 s
+__device__ __forceinline__ uint32_t bf16_of(uint32_t word, int p, uint32_t s, uint32_t off) {
+    const uint32_t v = mask_or<0x000f000fu, 0x43004300u>(word >> (4 * p));
+    uint32_t y;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(v), "r"(s), "r"(off));
+    return y;
+}
+// s(b) / 8, b <= 254.  Eighths of values, 2^-19 to 50176, are exact in fp16.
+__device__ __forceinline__ float eighth_of(uint32_t b) { return __uint_as_float(b * 0x00100000u + (108u << 23)); }
+// eighths of the values of nibble 0 (odd: 1) in fp16, s: s / 8 twice: 1024 + (n + 8), or
+// 1024 + 16 (n + 8) one nibble up, to n, times s
+__device__ __forceinline__ uint32_t half_of(uint32_t word, int odd, uint32_t s) {
+    uint32_t n, y;
+    if (odd) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(n) : "r"(mask_or<0x00f000f0u, 0x64006400u>(word)), "r"(0x2c002c00u), "r"(0xd480d480u));  // 1 / 16, -72
+    else asm("add.rn.f16x2 %0, %1, %2;" : "=r"(n) : "r"(mask_or<0x000f000fu, 0x64006400u>(word)), "r"(0xe408e408u));  // -1032
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(n), "r"(s));
+    return y;
+}
+
 }  // namespace cache4
 }  // namespace dspark
