@@ -181,25 +181,24 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
 template <typename C, bool kKeys>
 __device__ __forceinline__ void unpack_tiles(unsigned char *smem, const dspark_tree_attention_args &a, int warp, const Waiter &wait,
                                              Queue &queue, uint64_t *copied, uint64_t *copy_free, uint64_t *full, uint64_t *empty,
-                                             int op_rows) {
-    constexpr int kLanes = C::DP / 16, kRows = 32 / kLanes, kTurns = 32 / kRows;  // lanes of a row, rows and turns of a warp
-    const int lane = threadIdx.x & 31, g = lane % kLanes, row0 = 32 * warp + lane / kLanes;
+                                             int op_rows, int G) {
+    constexpr int kLanes = C::DP / 16, kRows = 32 / kLanes, kTurns = 8 / kRows;  // lanes of a row, rows of a turn, turns of eight rows
+    const int lane = threadIdx.x & 31, g = lane % kLanes, row = lane / kLanes;
     const bool in = 16 * g < a.D;
-    // a turn is kRows (4 or 8) rows further: the swizzle of its 16-byte pieces is that of the turn before with bit 2 turned,
-    // or the same.  Lanes of the upper columns write their second piece first, so that eight lanes' pieces fall on all banks.
+    // Lanes of the upper columns write their second piece first, so that eight lanes' pieces fall on all banks; the second
+    // turn's rows have bit 2 of the swizzle set.
     const bool flip = C::DP == 128 && g >= 4;
-    const int first = (g >> 2) * C::kBlock + row0 * 128;
-    const int piece0 = (((2 * g + (flip ? 1 : 0)) & 7) ^ (row0 & 7)) << 4, piece1 = piece0 ^ 16;
-    constexpr int kTurn = C::DP == 128 ? 64 : 0;
+    const int first = (g >> 2) * C::kBlock + row * 128;
+    const int piece0 = (((2 * g + (flip ? 1 : 0)) & 7) ^ row) << 4, piece1 = piece0 ^ 16;
     const int code_row = a.D / 2, scale_row = a.D / 16;
     // columns beyond D: zeros in every slot, once
     if (!in) {
 #pragma unroll 1
-        for (int i = 0; i < C::NS * kTurns; ++i) {
-            unsigned char *at = smem + C::kOffRing + (i / kTurns) * C::kSlot + first + (i % kTurns) * kRows * 128;
-            const int turn = (i % kTurns) & 1 ? kTurn : 0;
-            *reinterpret_cast<uint4 *>(at + (piece0 ^ turn)) = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4 *>(at + (piece1 ^ turn)) = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < C::NS * 4 * kTurns; ++i) {
+            const int t = i % kTurns, eight = 4 * warp + (i / kTurns) % 4;
+            unsigned char *at = smem + C::kOffRing + i / (4 * kTurns) * C::kSlot + first + eight * 1024 + t * kRows * 128;
+            *reinterpret_cast<uint4 *>(at + (piece0 ^ (64 * t))) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4 *>(at + (piece1 ^ (64 * t))) = make_uint4(0u, 0u, 0u, 0u);
         }
     }
     uint32_t base = 0;
@@ -207,24 +206,28 @@ __device__ __forceinline__ void unpack_tiles(unsigned char *smem, const dspark_t
     while (queue.read_warp(wait, x)) {
         const bool dual = C::NQ == 2 && x.n > op_rows;
         const int n = x.t1 - x.t0;
+        // This warp's rows of a tile, eight by eight: a softmax warp of each stream works beside warp q where the unit has
+        // lines 32 q and on; that warp gets fewer.
+        const int busy = dual ? 4 : min(4, (x.n * G + 31) >> 5), few = busy, many = busy < 4 ? (16 - busy * few) / (4 - busy) : 4;
+        const int eight0 = warp < busy ? warp * few : busy * few + (warp - busy) * many, eights = warp < busy ? few : many;
         for (int i = 0; i < n; ++i) {
             const uint32_t pos = base + (kKeys ? key_place(i, dual) : value_place(i, n, dual)), item = base / 2 + i;
             const int from = item % C::NP, slot = pos % C::NS;
             if (!wait.warp(&copied[from], (item / C::NP) & 1u)) return;
             const unsigned char *packed = smem + C::kOffPacked + ((kKeys ? 0 : C::NP) + from) * C::kPacked;
-            const unsigned char *code = packed + row0 * code_row + 8 * g, *scale = packed + kTile * code_row + row0 * scale_row + g;
+            const unsigned char *code = packed + (8 * eight0 + row) * code_row + 8 * g, *scale = packed + kTile * code_row + (8 * eight0 + row) * scale_row + g;
             // (Slots are given back in the ring's order, and items of one kind are three places apart at most, no
             // more than there are slots: the phase before the one waited for has passed.)
             if (!wait.warp(&empty[slot], ((pos / C::NS) & 1u) ^ 1u)) return;
-            unsigned char *to = smem + C::kOffRing + slot * C::kSlot + first;
-            // Two turns at a time and no more: the code of all roles has to stay in the SM's first instruction caches (with eight
-            // turns unrolled four of ten stalls were for instructions, and a tile took twice the time).
+            unsigned char *to = smem + C::kOffRing + slot * C::kSlot + first + eight0 * 1024;
+            // Eight rows at a time and no more: the code of all roles has to stay in the SM's first instruction caches (with all 32
+            // rows of a warp unrolled four of ten stalls were for instructions, and a tile took twice the time).
 #pragma unroll 1
-            for (int t0 = 0; t0 < kTurns; t0 += 2) {
-                uint2 w[2];
-                uint32_t b[2];
+            for (int e8 = 0; e8 < eights; ++e8) {
+                uint2 w[kTurns];
+                uint32_t b[kTurns];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
+                for (int t = 0; t < kTurns; ++t) {
                     w[t] = make_uint2(0u, 0u);
                     b[t] = 0;
                     if (in) {
@@ -233,7 +236,7 @@ __device__ __forceinline__ void unpack_tiles(unsigned char *smem, const dspark_t
                     }
                 }
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
+                for (int t = 0; t < kTurns; ++t) {
                     uint32_t r[2][4];
                     const uint32_t word[2] = {flip ? w[t].y : w[t].x, flip ? w[t].x : w[t].y};
                     if (kKeys) {
@@ -252,14 +255,13 @@ __device__ __forceinline__ void unpack_tiles(unsigned char *smem, const dspark_t
                             for (int e = 0; e < 4; ++e) r[h][e] = cache4::half_of(word[h] >> (8 * (e >> 1)), e & 1, s);
                     }
                     if (in) {
-                        const int turn = t & 1 ? kTurn : 0;
-                        *reinterpret_cast<uint4 *>(to + t * kRows * 128 + (piece0 ^ turn)) = make_uint4(r[0][0], r[0][1], r[0][2], r[0][3]);
-                        *reinterpret_cast<uint4 *>(to + t * kRows * 128 + (piece1 ^ turn)) = make_uint4(r[1][0], r[1][1], r[1][2], r[1][3]);
+                        *reinterpret_cast<uint4 *>(to + t * kRows * 128 + (piece0 ^ (64 * t))) = make_uint4(r[0][0], r[0][1], r[0][2], r[0][3]);
+                        *reinterpret_cast<uint4 *>(to + t * kRows * 128 + (piece1 ^ (64 * t))) = make_uint4(r[1][0], r[1][1], r[1][2], r[1][3]);
                     }
                 }
-                code += 2 * kRows * code_row;
-                scale += 2 * kRows * scale_row;
-                to += 2 * kRows * 128;
+                code += 8 * code_row;
+                scale += 8 * scale_row;
+                to += 1024;
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
@@ -523,8 +525,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     } else if (C::FOUR && warp >= 12) {
         // ------------------------------------------------------------ 4 bits to 16
         if constexpr (C::FOUR) {
-            if (warp < 16) unpack_tiles<C, true>(smem, a, warp - 12, wait, queue, copied, copy_free, full, empty, tp.op_rows);
-            else unpack_tiles<C, false>(smem, a, warp - 16, wait, queue, copied + C::NP, copy_free + C::NP, full, empty, tp.op_rows);
+            if (warp < 16) unpack_tiles<C, true>(smem, a, warp - 12, wait, queue, copied, copy_free, full, empty, tp.op_rows, p.G);
+            else unpack_tiles<C, false>(smem, a, warp - 16, wait, queue, copied + C::NP, copy_free + C::NP, full, empty, tp.op_rows, p.G);
         }
     } else {
         // ------------------------------------------------------------ softmax
