@@ -28,6 +28,11 @@ struct Eight<__nv_bfloat16> {
         v.x = u[0] | (unsigned)u[1] << 16, v.y = u[2] | (unsigned)u[3] << 16;
         v.z = u[4] | (unsigned)u[5] << 16, v.w = u[6] | (unsigned)u[7] << 16;
     }
+    // bits of the largest magnitude as a float; infinities and NaN are the largest of all
+    __device__ __forceinline__ unsigned most() const {
+        const unsigned m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+        return max(m << 16, m & 0xffff0000u);
+    }
     __device__ __forceinline__ void get(float (&x)[8]) const {
         const unsigned w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -40,7 +45,7 @@ struct Eight<__nv_bfloat16> {
         for (int i = 0; i < 4; ++i) w[i] = __byte_perm(__float_as_uint(x[2 * i]), __float_as_uint(x[2 * i + 1]), 0x7632);
         *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    static __device__ __forceinline__ float whole(float x, float, float inv) { return cache4::whole_of_bf16(x, inv); }
+    static __device__ __forceinline__ float coded(float x, float, float inv) { return cache4::coded_bf16(x, inv); }
 };
 template <>
 struct Eight<float> {
@@ -53,6 +58,14 @@ struct Eight<float> {
         a = make_float4(p[0], p[1], p[2], p[3]);
         b = make_float4(p[4], p[5], p[6], p[7]);
     }
+    __device__ __forceinline__ unsigned most() const {
+        float x[8];
+        get(x);
+        unsigned m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+        return m;
+    }
     __device__ __forceinline__ void get(float (&x)[8]) const {
         x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
     }
@@ -60,7 +73,7 @@ struct Eight<float> {
         reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
         reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
     }
-    static __device__ __forceinline__ float whole(float x, float s, float inv) { return cache4::whole_of(x, s, inv); }
+    static __device__ __forceinline__ float coded(float x, float s, float inv) { return 12582920.f + cache4::whole_of(x, s, inv); }
 };
 
 template <typename T, bool kWide, int kRows>
@@ -91,29 +104,28 @@ __global__ void __launch_bounds__(kThreads) cache_store4_kernel(const dspark_cac
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-        float x[8], most = 0.f;
-        if (slot[i] >= 0) {
-            v[i].get(x);
-            bool odd = false;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                most = fmaxf(most, fabsf(x[k]));
-                odd |= !(fabsf(x[k]) < INFINITY);
-            }
-            if (odd) most = INFINITY;  // the maximum skips a NaN
-        }
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        unsigned most = slot[i] >= 0 ? v[i].most() : 0u;
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
         if (slot[i] < 0) continue;
-        const unsigned byte = cache4::scale_byte(most);
+        float x[8];
+        v[i].get(x);
+        if (__uint_as_float(most) > cache4::kMostHeld) {  // beyond the largest scale
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = fminf(fmaxf(x[k], -cache4::kMostHeld), cache4::kMostHeld);
+        }
+        const unsigned byte = cache4::scale_byte(__uint_as_float(most));
         const float s = cache4::scale_of(byte), inv = __frcp_rn(s);
-        unsigned word = 0;
+        unsigned code[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const float n = Eight<T>::whole(x[k], s, inv);
-            word |= (__float_as_uint(n + 12582920.f) & 15u) << cache4::code_shift(k);  // 1.5 2^23 + 8
-            x[k] = n * s;
+            const float n = Eight<T>::coded(x[k], s, inv);
+            code[k] = __float_as_uint(n);
+            x[k] = (n - 12582920.f) * s;
         }
-        if (byte == cache4::kNoNumbers) word = 0x88888888u;
+        // elements 0 4 1 5 in the low halves of the four bytes, 2 6 3 7 in the high ones
+        const unsigned low = __byte_perm(__byte_perm(code[0], code[4], 0x0040), __byte_perm(code[1], code[5], 0x0040), 0x5410);
+        const unsigned high = __byte_perm(__byte_perm(code[2], code[6], 0x0040), __byte_perm(code[3], code[7], 0x0040), 0x5410);
+        const unsigned word = byte == cache4::kNoNumbers ? 0x88888888u : low + 16u * high;
         const int pg = (int)page.of(slot[i]), off = slot[i] - pg * a.page;
         unsigned char *at = cache + ((long long)pg * a.H + h) * cache4::page_bytes(a.page, a.D);
         *reinterpret_cast<unsigned *>(at + (long long)off * (a.D / 2) + e / 2) = word;

@@ -45,14 +45,16 @@ __device__ __forceinline__ float whole_of(float x, float s, float inv) {
     const float n = low + ((a > half || (a == half && ((int)low & 1))) ? 1.f : 0.f);
     return copysignf(fminf(n, 7.f), x);
 }
-// and for x of bf16: x / s is a quotient of eight bits and four, which is halfway between
-// two whole numbers or at least 2^-11 away (|x / s| between 1/4 and 16: a multiple
-// of 2^-6 / 30 off any odd half).  Rounded to a multiple of 2^-14 it is on the right side,
-// whatever the product with 1 / s loses.
-__device__ __forceinline__ float whole_of_bf16(float x, float inv) {
+// The same for x of bf16, as the float 1.5 2^23 + 8 + n (its lowest byte is the code): x / s is a
+// quotient of eight bits and four, which is halfway between two whole numbers or at
+// least 2^-11 away (|x / s| between 1/4 and 16: a multiple of 2^-6 / 30 off any odd half).
+// Rounded to a multiple of 2^-14 it is on the right side, whatever the product with 1 / s
+// loses.  It is within -7.44 .. 7.44 unless the scale is the largest there is.
+__device__ __forceinline__ float coded_bf16(float x, float inv) {
     const float t = __fadd_rn(__fmaf_rn(x, inv, 768.f), -768.f);  // 768 = 1.5 2^9
-    return fminf(fmaxf(__fadd_rn(__fadd_rn(t, 12582912.f), -12582912.f), -7.f), 7.f);  // 1.5 2^23
+    return __fadd_rn(t, 12582920.f);
 }
+constexpr float kMostHeld = 7.f * 57344.f;
 
 // ---------------------------------------------------------------- two values at a time
 // A code word has elements 2 p and 2 p + 1 of eight in nibble p of its halves, so a shift and a

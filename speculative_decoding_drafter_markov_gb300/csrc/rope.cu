@@ -148,11 +148,13 @@ __global__ void __launch_bounds__(32 * kWarps) rope_store_kernel(const __grid_co
     const long long item = (long long)blockIdx.x * kWarps + warp;
     const int i = (int)(item / r.splits), part = (int)(item - (long long)i * r.splits);
     if (i >= a.N) return;
-    int slot = 0;
-    if (a.slot) {
-        slot = checked_slot(a.slot[i], slots_of(a.n_pages, a.page), a.err);
-        if (slot < 0) return;
-    }
+    // everything that is read at the start is on its way before anything is waited for
+    int slot = a.slot ? a.slot[i] : 0;
+    const int pos = a.pos[i];
+    float freq[2] = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (lane + 32 * k < half) freq[k] = a.freq[lane + 32 * k];
     const int h0 = part * r.per_split, h1 = min(r.heads, h0 + r.per_split);
     // this thread's pieces of a head: pairs j0 .. j0 + E - 1
     const int in_head = lane % kLanes, j0 = in_head * E;
@@ -165,21 +167,39 @@ __global__ void __launch_bounds__(32 * kWarps) rope_store_kernel(const __grid_co
         at0 = turn ? j0 : a.rot + j0 - half;
         at1 = at0 + (turn ? half : (a.D - a.rot) / 2);
     }
-    // heads two at a time, their reads under way before the angles are known
+    // where the row's queries, keys and values come from and go to
+    const T *q_src = static_cast<const T *>(a.q) + i * a.q_row + at0, *k_src = static_cast<const T *>(a.k) + i * a.k_row + at0,
+            *v_src = static_cast<const T *>(a.v) + i * a.v_row + at0;
+    const int apart = at1 - at0;
+    // heads two at a time
     P x[2][2];
-    Head to[2];
-    auto fetch = [&](int h, P (&y)[2], Head &t) {
+    auto fetch = [&](int h, P (&y)[2]) {
         if (h >= h1 || !in) return;
-        t = r.head<T>(h, i, slot);
-        y[0].load(static_cast<const T *>(t.src) + at0);
-        y[1].load(static_cast<const T *>(t.src) + at1);
+        const T *src = h < a.Hq ? q_src + h * a.q_head : h < a.Hq + a.H ? k_src + (h - a.Hq) * a.k_head : v_src + (h - a.Hq - a.H) * a.v_head;
+        y[0].load(src);
+        y[1].load(src + apart);
     };
     const int first = h0 + lane / kLanes;
-    fetch(first, x[0], to[0]);
-    fetch(first + kHeads, x[1], to[1]);
-    const int pos = a.pos[i];
+    fetch(first, x[0]);
+    fetch(first + kHeads, x[1]);
+    if (a.slot) {
+        slot = checked_slot(slot, slots_of(a.n_pages, a.page), a.err);
+        if (slot < 0) return;
+    }
+    T *q_dst = static_cast<T *>(a.q_out) + i * a.q_out_row + at0, *k_dst, *v_dst = nullptr;
+    long long k_step = a.k_out_head;
+    if (a.slot) {
+        const int pg = (int)r.page.of(slot);
+        const long long at = ((long long)pg * a.H * a.page + (slot - pg * a.page)) * a.D + at0;
+        k_dst = static_cast<T *>(a.k_cache) + at;
+        v_dst = static_cast<T *>(a.v_cache) + at;
+        k_step = (long long)a.page * a.D;
+    } else {
+        k_dst = static_cast<T *>(a.k_out) + i * a.k_out_row + at0;
+    }
     if (h0 < a.Hq + a.H) {
-        for (int j = lane; j < half; j += 32) turned[warp][j] = cos_sin(turns_of(a.freq[j]), pos);
+        for (int j = lane, k = 0; j < half; j += 32, ++k)
+            turned[warp][j] = cos_sin(turns_of(k == 0 ? freq[0] : k == 1 ? freq[1] : a.freq[j]), pos);
         __syncwarp();
     }
     float c[E], s[E];
@@ -199,7 +219,8 @@ __global__ void __launch_bounds__(32 * kWarps) rope_store_kernel(const __grid_co
             for (int p = 0; p < 2; ++p)
 #pragma unroll
                 for (int k = 0; k < E; ++k) y[p][k] = live ? x[u][p].get(k) : 0.f;
-            const bool norm = live && to[u].weight != nullptr;
+            const T *weight = static_cast<const T *>(hu < a.Hq ? a.q_weight : hu < a.Hq + a.H ? a.k_weight : nullptr);
+            const bool norm = live && weight != nullptr, key = hu < a.Hq + a.H;  // a query or a key
             if (a.q_weight || a.k_weight) {
                 float sum = 0.f;
 #pragma unroll
@@ -222,7 +243,6 @@ __global__ void __launch_bounds__(32 * kWarps) rope_store_kernel(const __grid_co
                 }
                 if (norm) {
                     P w[2];
-                    const T *weight = static_cast<const T *>(to[u].weight);
                     w[0].load_shared(weight + at0);
                     w[1].load_shared(weight + at1);
 #pragma unroll
@@ -231,7 +251,7 @@ __global__ void __launch_bounds__(32 * kWarps) rope_store_kernel(const __grid_co
                         for (int k = 0; k < E; ++k) y[p][k] = y[p][k] * f * w[p].get(k);
                 }
             }
-            if (live && to[u].turn) {
+            if (live && key) {
                 if (turn) {
 #pragma unroll
                     for (int k = 0; k < E; ++k) {
@@ -249,11 +269,11 @@ __global__ void __launch_bounds__(32 * kWarps) rope_store_kernel(const __grid_co
                 }
             }
             if (live) {
-                T *dst = static_cast<T *>(to[u].dst);
-                x[u][0].store(dst + at0);
-                x[u][1].store(dst + at1);
+                T *dst = hu < a.Hq ? q_dst + hu * a.q_out_head : key ? k_dst + (hu - a.Hq) * k_step : v_dst + (hu - a.Hq - a.H) * k_step;
+                x[u][0].store(dst);
+                x[u][1].store(dst + apart);
             }
-            fetch(hu + 2 * kHeads, x[u], to[u]);
+            fetch(hu + 2 * kHeads, x[u]);
         }
     }
 }
