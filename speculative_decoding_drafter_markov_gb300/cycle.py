@@ -3,7 +3,8 @@ pass runs on the paged-cache operators.
 
 One cycle, all on the GPU and without a wait on the host: draft, schedule,
 flattened tags, batch map (pages, slots, positions), the target's pass (per layer
-cache writes and attention over the cache), the rules on its logits,
+norms and rotation of queries and keys if it has them, cache writes and attention
+over the cache, in 16 bits or in 4), the rules on its logits,
 verification, and the bookkeeping of what was accepted.  A request is verified no
 further than its text has room, and is done when that is full; a cycle for which
 the cache has not the pages changes nothing.  The target is a stand-in with random
@@ -25,10 +26,14 @@ from . import workloads as W
 
 class StandInTarget:
     """Embeddings, `layers` attention layers with residuals and a vocabulary
-    projection, random weights; keys and values live in paged caches."""
+    projection, random weights; keys and values live in paged caches.  With `rotary` positions
+    turn queries and keys, after a norm of each head, instead of being added to the
+    embeddings; with `bits` = 4 the caches hold keys and values in 4 bits."""
 
     def __init__(self, V, *, layers=2, Hq=8, H=2, D=64, n_pages=256, page=16, max_len=4096, dtype=torch.bfloat16, device="cuda",
-                 seed=0):
+                 seed=0, rotary=False, bits=16):
+        if bits not in (4, 16):
+            raise ValueError(f"caches of {bits} bits; there are 16 (the target's type) and 4")
         g = torch.Generator(device=device).manual_seed(seed)
         dm = Hq * D
         rand = lambda *n: (torch.randn(n, generator=g, device=device) / math.sqrt(n[-1])).to(dtype)  # noqa: E731
@@ -38,20 +43,37 @@ class StandInTarget:
         self.qkv = [rand((Hq + 2 * H) * D, dm) for _ in range(layers)]
         self.proj = [rand(dm, dm) for _ in range(layers)]
         self.head = rand(V, dm) * 4
-        cache = lambda: torch.zeros((n_pages, H, page, D), dtype=dtype, device=device)  # noqa: E731
+        self.rotary, self.bits = rotary, bits
+        if rotary:
+            self.freq = torch.pow(torch.tensor(1e4, dtype=torch.float64), -torch.arange(0, D, 2) / D).float().to(device)
+            weight = lambda: (1 + 0.1 * torch.randn(D, generator=g, device=device)).to(dtype)  # noqa: E731
+            self.norms = [(weight(), weight()) for _ in range(layers)]
+        if bits == 4:
+            cache = lambda: dsp.cache4(n_pages, H, page, D, device=device)  # noqa: E731
+        else:
+            cache = lambda: torch.zeros((n_pages, H, page, D), dtype=dtype, device=device)  # noqa: E731
         self.caches = [(cache(), cache()) for _ in range(layers)]
 
     def forward(self, tok, pos, slot, table, lens, row_start, *, mask=None, max_rows=1, err=None):
         """Target logits [N, V] of rows with these tokens, positions and slots;
         their keys and values are in the caches afterwards."""
-        x = self.emb[tok.long()] + self.place[pos.long()]
-        for (kc, vc), qkv, proj in zip(self.caches, self.qkv, self.proj):
+        x = self.emb[tok.long()] + (0 if self.rotary else self.place[pos.long()])
+        attend = dsp.tree_attention4 if self.bits == 4 else dsp.tree_attention
+        for i, ((kc, vc), qkv, proj) in enumerate(zip(self.caches, self.qkv, self.proj)):
             rows = torch.matmul(torch.nn.functional.rms_norm(x, x.shape[-1:]), qkv.T).view(x.shape[0], -1, self.D)
             q, k, v = rows.split([self.Hq, self.H, self.H], 1)
-            dsp.cache_store(k, v, slot, kc, vc, err=err)
+            stored = False
+            if self.rotary:
+                # into a 16-bit cache on the way; the other one takes the turned keys below
+                stored = self.bits != 4
+                cache = dict(slot=slot, k_cache=kc, v_cache=vc) if stored else {}
+                turned = dsp.rope_store(q, k, v, pos, self.freq, q_weight=self.norms[i][0], k_weight=self.norms[i][1], err=err, **cache)
+                q, k = turned["q"], turned.get("k")
+            if not stored:
+                (dsp.cache_store4 if self.bits == 4 else dsp.cache_store)(k, v, slot, kc, vc, err=err)
             # rows beyond the batch are not written by the attention
             out = {"out": torch.zeros((x.shape[0], self.Hq, self.D), dtype=x.dtype, device=x.device)}
-            dsp.tree_attention(q, kc, vc, table, lens, row_start, mask=mask, max_rows=max_rows, out=out, err=err)
+            attend(q, kc, vc, table, lens, row_start, mask=mask, max_rows=max_rows, out=out, err=err)
             x = x + torch.matmul(out["out"].flatten(1), proj.T)
         return torch.matmul(torch.nn.functional.rms_norm(x, x.shape[-1:]), self.head.T)
 
@@ -170,10 +192,12 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--cycles", type=int, default=8)
     ap.add_argument("--requests", type=int, default=6)
+    ap.add_argument("--rotary", action="store_true", help="a target with rotary positions")
+    ap.add_argument("--bits", type=int, default=16, choices=(4, 16), help="of the caches")
     a = ap.parse_args()
     R = a.requests
     per = lambda v: torch.full((R,), v, device="cuda")  # noqa: E731
-    s = small_server(R=R, rules=dict(rep=per(1.2), freq=per(0.1), pres=per(0.0)))
+    s = small_server(R=R, rules=dict(rep=per(1.2), freq=per(0.1), pres=per(0.0)), rotary=a.rotary, bits=a.bits)
     for c in range(a.cycles):
         o = s.cycle()
         print(f"cycle {c}: verified {int(o['ell'].sum())} drafted tokens, new tokens {int(o['n_new'].sum())}, "

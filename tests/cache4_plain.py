@@ -36,3 +36,13 @@ def cache_of(x):
     b, n = quantise(x)
     flat = x.shape[:2] + (-1,)
     return np.concatenate([pack(n).reshape(flat), b.reshape(flat)], -1), held(b, n)
+
+
+def values(cache, page, D):
+    """What a cache [pages, H, page D 9 / 16] of bytes stands for: [pages, H, page, D]."""
+    codes = cache[..., :page * D // 2].reshape(*cache.shape[:2], page, D // 8, 4)
+    n = np.zeros(codes.shape[:-1] + (8,), int)
+    for byte, (i, j) in enumerate(PLACES):
+        n[..., i], n[..., j] = (codes[..., byte] & 15).astype(int) - 8, (codes[..., byte] >> 4).astype(int) - 8
+    b = cache[..., page * D // 2:].reshape(*cache.shape[:2], page, D // 16)
+    return held(b, n.reshape(*cache.shape[:2], page, D))

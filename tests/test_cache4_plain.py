@@ -32,4 +32,5 @@ def test_values_again():
     # a step is a seventh of the largest, and up to 1/17 more or less by the scale's rounding
     assert (np.abs(v - x).reshape(4, 3, 8, 4, 16) <= g / 14 * 18 / 17).all()
     assert np.array_equal(c4.cache_of(v)[0], cache)
+    assert np.array_equal(c4.values(cache, 8, 64), v)
     assert np.array_equal((v.astype(np.float32).view(np.uint32) & 0xffff), np.zeros(v.shape))
