@@ -378,12 +378,19 @@ void carve(Params &p, void *ws, int grid) {
     p.part_o = reinterpret_cast<float *>(c);
 }
 
+// whether a request's lines, as far as the host knows, fit 16 columns
+static bool few_lines(const dspark_tree_attention_args &a) { return (long long)a.max_rows * (a.Hq / a.H) <= 16; }
+
+// the columns that they get
+static int mma_lines(const dspark_tree_attention_args &a) { return a.max_rows * (a.Hq / a.H) <= 8 ? 8 : 16; }
 cudaError_t launch_join(const Params &p, int grid, cudaStream_t s) {
     // a CTA for every line of a unit, as far as the host knows them; the first launch lets
     // them come up while it runs
     const long long lines = (long long)p.a.max_rows * p.heads;
     unsigned y = (unsigned)(lines < 1 ? 1 : lines < p.lines ? lines : p.lines);
     if (y > 32) y = 32;
+    // of many shares, warps', few have a unit to join, and that has few lines: a warp a line
+    if (grid > 4 * sm_count()) y = (y + kJoinWarps - 1) / kJoinWarps;
     auto kern = p.stride % 4 == 0 ? (p.stride <= 128 ? tree_attention_join<4, 1> : tree_attention_join<4, 2>)
                                   : (p.stride <= 64 ? tree_attention_join<1, 2> : tree_attention_join<1, 8>);
     return launch_close(kern, dim3(grid, y), 32 * kJoinWarps, 0, s, p);
@@ -391,8 +398,13 @@ cudaError_t launch_join(const Params &p, int grid, cudaStream_t s) {
 
 }  // namespace attn
 
-// (of a cache in 4 bits too: the same two ways of cutting)
-size_t tree_attention4_ws_bytes(const dspark_tree_attention_args &a) { return tree_attention_ws_bytes(a); }
+// (of a cache in 4 bits: these two ways of cutting, and that among warps)
+size_t tree_attention4_ws_bytes(const dspark_tree_attention_args &a) {
+    const size_t two = tree_attention_ws_bytes(a);
+    if (a.dtype != DSPARK_BF16 || a.D > 128 || !attn::few_lines(a)) return two;
+    const size_t warps = attn::workspace_bytes(attn::mma4_grid(), attn::mma_lines(a), a.D);
+    return warps > two ? warps : two;
+}
 
 size_t tree_attention_ws_bytes(const dspark_tree_attention_args &a) {
     // enough for either kernel: which one runs also depends on the pointers
@@ -428,15 +440,14 @@ void cut_for_tc(Params &p, void *ws, int grid) {
     carve(p, ws, grid);
 }
 
-// units of 8, 16 or 32 lines, as few as the host's hint says that a request has
-void cut_for_mma(Params &p, void *ws, int grid) {
-    const int lines = p.a.max_rows * p.G, most = lines <= 8 ? 8 : lines <= 16 ? 16 : 32;
-    p.heads = p.G < most ? p.G : most;
-    p.subs = (p.G + p.heads - 1) / p.heads;
-    p.block_rows = most / p.heads;
+// units of 8 or 16 lines
+void cut_for_mma(Params &p, void *ws, int shares) {
+    p.heads = p.G;
+    p.subs = 1;
+    p.block_rows = mma_lines(p.a) / p.heads;
     p.lines = p.block_rows * p.heads;
     p.stride = p.a.D;
-    carve(p, ws, grid);
+    carve(p, ws, shares);
 }
 
 // units of kSimtLines lines, for the kernels on the CUDA cores
@@ -504,11 +515,12 @@ cudaError_t launch_tree_attention4(const dspark_tree_attention_args &a, void *ws
     Params p = params_of(a);
     if (tc4_supported(a)) {
         const int grid = sm_count();
-        const bool few = (long long)a.max_rows * p.G <= 16;
-        if (few) cut_for_mma(p, ws, grid);
+        const bool few = few_lines(a);
+        const int shares = few ? mma4_grid() : grid;
+        if (few) cut_for_mma(p, ws, shares);
         else cut_for_tc(p, ws, grid);
-        cudaError_t e = few ? launch_mma4(p, grid, s) : launch_tc4(p, grid, s);
-        return e == cudaSuccess ? launch_join(p, grid, s) : e;
+        cudaError_t e = few ? launch_mma4(p, shares, s) : launch_tc4(p, grid, s);
+        return e == cudaSuccess ? launch_join(p, shares, s) : e;
     }
     cut_for_simt(p);
     return launch_simt<true>(p, ws, s);

@@ -8,13 +8,14 @@
 // shared memory: the fragments of an m16n8k16 product are unpacked where they are used.
 //
 // A unit's lines (rows x query heads of a group) are NT times 8, the columns of the products;
-// their rows are tokens, and then columns of values.  One warp walks the CTA's
-// share of the work and hands out its pieces; warp w of the NW others takes every NW-th step
-// of 32 tokens, with a running maximum and sum and 8 NT x D sums of its own, and the warps'
-// results are added at the piece's end like partials.  A warp copies its steps itself, by
-// cp.async into slots of its own, the next ones while it works on one, on into the next
-// piece.  (Bulk copies by one warp took 80 clocks each to issue, 1900 to 2600 a tile: more
-// than all the rest.)  Per step and warp:
+// their rows are tokens, and then columns of values.  The work is cut among the warps of the
+// whole GPU: each walks a share of its own, in tiles of 32 tokens, with a running maximum and
+// sum and 8 NT x D sums, and leaves what it has of a unit as a partial.  (Cut among CTAs, whose
+// warps took turns and met at the end of every unit, 128 caches of up to 16384 tokens took
+// @CTA@ us.)  A warp copies its tiles itself, by cp.async into slots of its own,
+// the next ones while it works on one, on into the next piece.  (Bulk copies by one warp
+// took 80 clocks each to issue, 1900 to 2600 per 128 tokens: more than all the rest.)
+// Per 16 tokens:
 //     S^T = K Q^T        K in bf16 (exactly), contracted over D in an order of its own:
 //                        lane j of four has columns j D/4 .. of a token, 16 adjacent bytes
 //     P = 2^(S scale log2(e) - m), rounded to fp16; m moves when a weight would pass 2^15
@@ -34,28 +35,30 @@ namespace attn {
 
 namespace {
 
-constexpr int kStep = 32;     // tokens of a step
+constexpr int kStepLog2 = 5, kStep = 1 << kStepLog2;  // tokens of a tile
 constexpr float kLift = 7.f;  // the reference stands below the maximum, as in attn_tc_kernel.cuh
 constexpr int kMmaUnitCost = 4;
+
+// A warp's place in its share: the piece that it works on and the next one, and the walk
+// (in shared memory: they are looked at between pieces).
+struct Pieces {
+    Piece x[2];
+    Walk<Params> walk;
+};
 
 // DP: D padded, NT: lines / 8, FULL: D is DP
 template <int DP_, int NT_, bool FULL_>
 struct MmaShape {
     static constexpr int DP = DP_, NT = NT_;
     static constexpr bool FULL = FULL_;
-    // with the walker 16 warps of 128 registers, 12 of 168 or 8 of 255
-    static constexpr int NW = NT == 1 ? 15 : NT == 2 ? 11 : 7, kThreads = 32 * (NW + 1);
-    static constexpr int kLines = 8 * NT;
-    static constexpr int kDepth = NT < 4 ? 2 : 3;       // slots of a warp, a step each
+    static constexpr int NW = 12, kThreads = 32 * NW;   // 168 registers a thread
     static constexpr int kSlot = kStep * DP / 16 * 18;  // codes of keys, of values, scales of keys, of values
-    static constexpr int kOffO = NW * kDepth * kSlot;   // float [NW][kLines][DP]
-    static constexpr int kOffQ = kOffO + NW * kLines * DP * 4;  // uint2 [DP / 16][32][NT]
-    static constexpr int kOffMl = kOffQ + NT * DP / 16 * 256;   // float2 [NW][kLines]
-    static constexpr int kOffPiece = kOffMl + NW * kLines * 8;
-    static constexpr int kOffBar = kOffPiece + 64 * kQueue;
-    static constexpr int kOffMisc = kOffBar + 8 * (2 * kQueue);
-    static constexpr int kSmem = kOffMisc + 8;
-    static_assert(kSlot % 16 == 0 && kOffPiece % 16 == 0, "places");
+    static constexpr int kQ = NT == 1 ? 0 : NT * DP / 16 * 256;  // uint2 [DP / 16][32][NT]; with 8 lines they stay in registers
+    static constexpr int kPieces = (int)(sizeof(Pieces) + 15) / 16 * 16;
+    static constexpr int kDepth = NT == 1 ? 4 : 3;      // slots, a tile each
+    static constexpr int kWarp = kDepth * kSlot + kQ + kPieces;
+    static constexpr int kSmem = NW * kWarp;
+    static_assert(kSlot % 16 == 0, "places");
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], const uint2 &b) {
@@ -74,59 +77,18 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// a barrier of the consuming warps; true where any of them says so
-__device__ __forceinline__ bool meet(int threads, bool any) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
-        : "=r"(r)
-        : "r"(any ? 1u : 0u), "r"(threads)
-        : "memory");
-    return r != 0;
-}
-
-// steps of a piece
-__device__ __forceinline__ int steps_of(const Piece &x) {
-    return (min(x.t1 << kTileLog2, x.tokens) - (x.t0 << kTileLog2) + kStep - 1) / kStep;
-}
-
-// ---------------------------------------------------------------- the walk
-template <typename C>
-__device__ __forceinline__ void hand_out(unsigned char *smem, const Params &p, const Waiter &wait, uint64_t *queue_full, uint64_t *queue_empty) {
-    const int lane = threadIdx.x & 31;
-    const Share share = share_of(p);
-    Walk walk(p, share);
-    if (lane == 0) p.join[blockIdx.x].pieces = 0;
-    Piece x;
-    bool more = true;
-    for (uint32_t k = 0; more; ++k) {
-        more = walk.next(x);
-        if (!more) x.r = -1;
-        const int i = k % kQueue;
-        if (!wait.warp(&queue_empty[i], ((k / kQueue) & 1u) ^ 1u)) break;
-        if (lane == 0) {
-            *reinterpret_cast<Piece *>(smem + C::kOffPiece + 64 * i) = x;
-            tc::mbar_arrive(&queue_full[i]);
-            if (more && x.t0 == 0 && x.t1 < x.tiles) p.join[blockIdx.x] = walk.join_of(x);
-        }
-    }
-}
-
 // ---------------------------------------------------------------- a warp's copies
-// Position of the next step to copy: of piece `piece` (counted over the CTA's pieces), step
-// s; the pages of its four groups of eight tokens (lane % 4) are fetched a step ahead.
-template <typename C>
+// The next tile to copy: tile t of the warp's piece `piece` (counted over its pieces, the one
+// after the piece worked on at most), its first token and the pages of its four groups of
+// eight tokens (lane % 4), fetched a tile ahead.
 struct Copies {
-    int piece, s, steps;   // s >= steps: none is left in the piece
-    uint32_t c0;           // the CTA's steps before the piece
-    int tok0, last;        // first token of the step; the unit's last one
-    int page, off;         // of this lane's group: page, token in it
-    int h;                 // key-value head
-    bool more;             // a piece follows
+    int piece, t, t1;  // t >= t1: none is left in the piece
+    int tok0, last;    // first token of the tile; the unit's last one
+    int page, off;     // of this lane's group: page, token in it
+    int h;             // key-value head
     uint32_t issued, used;
 
-    __device__ __forceinline__ bool any() const { return s < steps; }
+    __device__ __forceinline__ bool any() const { return t < t1; }
 };
 __device__ __forceinline__ void cp_async8(void *dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
@@ -135,63 +97,66 @@ __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
 }
 
-// ---------------------------------------------------------------- the consumers
-// the queries of a unit as fragments of the first product, zero beyond its lines and columns
-template <typename C>
-__device__ __forceinline__ void load_queries(unsigned char *smem, const Params &p, const Piece &x) {
-    constexpr int kParts = C::DP / 4, kLane = C::DP / 4;  // parts of 4 elements of a line; columns of a lane
+// ---------------------------------------------------------------- the kernel
+// fragment of the first product of a unit's queries: columns d .. d + 3 of line `line`, zero beyond the unit and D
+__device__ __forceinline__ uint2 query_of(const Params &p, const Piece &x, int line, int d) {
     const dspark_tree_attention_args &a = p.a;
-    const int h = x.head / p.subs, sub = x.head - h * p.subs;
-    const int head0 = h * p.G + sub * p.heads, heads = min(p.heads, p.G - sub * p.heads);
-    uint2 *q = reinterpret_cast<uint2 *>(smem + C::kOffQ);
-    for (int i = threadIdx.x; i < C::kLines * kParts; i += 32 * C::NW) {
-        const int line = i / kParts, d = (i % kParts) * 4, jj = line / p.heads, g = line - jj * p.heads;
-        uint2 v = make_uint2(0u, 0u);
-        if (jj < x.n && g < heads && d < a.D)
-            v = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.q) + (long long)(x.row0 + x.first + jj) * a.q_row +
-                                                 (head0 + g) * a.q_head + d);
-        const int j = d / kLane, ks = (d % kLane) / 4;
-        q[(ks * 32 + (line & 7) * 4 + j) * C::NT + (line >> 3)] = v;
-    }
+    const int h = x.head / p.subs, sub = x.head - h * p.subs, jj = line / p.heads, g = line - jj * p.heads;
+    if (jj >= x.n || sub * p.heads + g >= p.G || d >= a.D) return make_uint2(0u, 0u);
+    return *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(a.q) + (long long)(x.row0 + x.first + jj) * a.q_row +
+                                            (h * p.G + sub * p.heads + g) * a.q_head + d);
 }
 
 template <typename C>
-__device__ __forceinline__ void consume(unsigned char *smem, const Params &p, const Waiter &wait, uint64_t *queue_full, uint64_t *queue_empty) {
+__global__ void __launch_bounds__(C::kThreads, 1) tree_attention4_mma(const __grid_constant__ Params p) {
+    extern __shared__ __align__(1024) unsigned char smem[];
     constexpr int DP = C::DP, NT = C::NT, KS = DP / 16, MT = DP / 16, ND = DP / 8;  // steps of the first product, rows / 16 of the second, columns of a lane
     const dspark_tree_attention_args &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    after_predecessor();
     const int code_row = a.D / 2, scale_row = a.D / 16;
     const float scale = fmaxf(p.scale_log2, 1e-37f);  // 0 would make -inf x 0 of what is not seen
     const int token_r = (r >> 1) + 4 * (r & 1);  // token of a product's row r; of row r + 8 eight on
-    const uint2 *q = reinterpret_cast<const uint2 *>(smem + C::kOffQ) + lane * NT;
-    float *part = reinterpret_cast<float *>(smem + C::kOffO);
-    float2 *ml = reinterpret_cast<float2 *>(smem + C::kOffMl);
-    unsigned char *slots = smem + warp * (C::kDepth * C::kSlot);
-    auto piece_at = [&](int i) -> const Piece & { return *reinterpret_cast<const Piece *>(smem + C::kOffPiece + 64 * (i % kQueue)); };
-    auto wait_piece = [&](int i) { return wait.warp(&queue_full[i % kQueue], ((uint32_t)i / kQueue) & 1u); };
-    bool ok = true;
-    int now = 0;      // the piece being worked on
-    Copies<C> cp{-1, 0, 0, 0, 0, 0, 0, 0, 0, true, 0, 0};
-    // to the next step of this warp, in the piece being worked on or the one after it, and its pages
-    auto seek = [&]() {
-        while (!cp.any() && cp.more && cp.piece <= now && ok) {
-            cp.c0 += (uint32_t)cp.steps;
-            ++cp.piece;
-            ok = wait_piece(cp.piece);
-            if (!ok) break;
-            const Piece &y = piece_at(cp.piece);
-            cp.more = y.r >= 0;
-            cp.steps = cp.more ? steps_of(y) : 0;
-            cp.s = (warp + C::NW - cp.c0 % C::NW) % C::NW;
+    unsigned char *slots = smem + warp * C::kWarp;
+    uint2 *q = reinterpret_cast<uint2 *>(slots + C::kDepth * C::kSlot);
+    Pieces &mine = *reinterpret_cast<Pieces *>(slots + C::kDepth * C::kSlot + C::kQ);
+    const int cta = blockIdx.x * C::NW + warp;  // of as many shares as there are warps
+    {
+        const Share share = share_of(p, cta, gridDim.x * C::NW);
+        Walk<Params> walk(p, share);
+        if (lane == 0) {
+            p.join[cta].pieces = 0;
+            memcpy(static_cast<void *>(&mine.walk), &walk, sizeof walk);
         }
-        if (!cp.any()) return;
-        const Piece &y = piece_at(cp.piece);
-        cp.last = y.tokens - 1;
-        cp.tok0 = (y.t0 << kTileLog2) + cp.s * kStep;
-        cp.h = p.subs == 1 ? y.head : y.head / p.subs;
+        __syncwarp();
+    }
+    // takes the next piece of the walk into its place (n: counted over the warp's pieces); r < 0: none is left
+    auto take = [&](int n) {
+        if (lane == 0) {
+            Piece &y = mine.x[n & 1];
+            if (!mine.walk.next(y)) y.r = -1;
+            else if (y.t0 == 0 && y.t1 < y.tiles) p.join[cta] = mine.walk.join_of(y);
+        }
+        __syncwarp();
+    };
+    int now = 0;  // the piece worked on
+    Copies cp{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    // to the next tile, in the piece worked on or the one after it, and its pages
+    auto seek = [&]() {
+        if (!cp.any()) {
+            if (cp.piece > now) return;
+            const Piece &y = mine.x[++cp.piece & 1];
+            if (y.r < 0) return;
+            cp.t = y.t0;
+            cp.t1 = y.t1;
+            cp.last = y.tokens - 1;
+            cp.h = p.subs == 1 ? y.head : y.head / p.subs;
+        }
+        cp.tok0 = cp.t << kStepLog2;
         const int tok = min(cp.tok0 + 8 * j, cp.last & ~7), in_table = p.page.of(tok);
         cp.off = tok - in_table * a.page;
-        cp.page = a.table[(size_t)y.r * a.max_pages + in_table];
+        cp.page = a.table[(size_t)mine.x[cp.piece & 1].r * a.max_pages + in_table];
     };
     const long long page_bytes = cache4::page_bytes(a.page, a.D), codes = cache4::code_bytes(a.page, a.D);
     auto copy = [&]() {
@@ -222,28 +187,17 @@ __device__ __forceinline__ void consume(unsigned char *smem, const Params &p, co
         }
         tc::cp_async_commit();
         ++cp.issued;
-        cp.s += C::NW;
+        ++cp.t;
         seek();
     };
-    auto fill = [&]() {
-        while (cp.any() && cp.issued - cp.used < (uint32_t)C::kDepth) copy();
-    };
+    take(0);
+    if (mine.x[0].r < 0) return;
+    take(1);
     seek();
-    Piece x;
-    x.r = -1;
-    if (ok) x = piece_at(0);
-    if (x.r >= 0) {
-        fill();
-        load_queries<C>(smem, p, x);
-    }
-    if (meet(32 * C::NW, !ok)) {
-        tc::cp_async_wait<0>();
-        return;
-    }
-    uint32_t c0 = 0;  // steps before the piece
-    while (x.r >= 0) {
-        const int steps = steps_of(x);
-        fill();
+    for (;;) {
+        const Piece x = mine.x[now & 1];
+#pragma unroll 1
+        while (cp.any() && cp.issued - cp.used < (uint32_t)C::kDepth) copy();
         const int base_rel = a.mask ? 0 : x.first + 1;  // rows of the cycle before it are seen by every line
         // lines 2 j, 2 j + 1 (+ 8 i); columns r ND + 2 t, r ND + 2 t + 1
         float O[NT][MT][4];
@@ -258,15 +212,18 @@ __device__ __forceinline__ void consume(unsigned char *smem, const Params &p, co
             l[i] = make_float2(0.f, 0.f);
         }
         uint2 q_held[NT == 1 ? KS : 1];
-        if (NT == 1) {
 #pragma unroll
-            for (int k = 0; k < (NT == 1 ? KS : 0); ++k) q_held[k] = q[k * 32];
-        }
-        const uint32_t skip = (warp + C::NW - c0 % C::NW) % C::NW;
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const uint2 v = query_of(p, x, 8 * i + r, j * (DP / 4) + 4 * k);
+                if (NT == 1) q_held[NT == 1 ? k : 0] = v;
+                else q[(k * 32 + lane) * NT + i] = v;  // (each lane reads what it wrote)
+            }
 #pragma unroll 1
-        for (int s = skip; s < steps; s += C::NW) {
-            int tok0 = (x.t0 << kTileLog2) + s * kStep;
-            // copies of this step: the oldest; all but it may be under way where the slots are full
+        for (int s = x.t0; s < x.t1; ++s) {
+            int tok0 = s << kStepLog2;
+            // copies of this tile: the oldest; all but it may be under way where the slots are full
             if (cp.issued - cp.used == (uint32_t)C::kDepth) tc::cp_async_wait<C::kDepth - 1>();
             else tc::cp_async_wait<0>();
             __syncwarp();
@@ -330,7 +287,7 @@ __device__ __forceinline__ void consume(unsigned char *smem, const Params &p, co
                     } else {
 #pragma unroll
                         for (int i = 0; i < NT; i += 2) {
-                            const uint4 two = *reinterpret_cast<const uint4 *>(q + k * 32 * NT + i);
+                            const uint4 two = *reinterpret_cast<const uint4 *>(q + (k * 32 + lane) * NT + i);
                             mma_bf16(S[i], ka, make_uint2(two.x, two.y));
                             mma_bf16(S[NT == 1 ? 0 : i + 1], ka, make_uint2(two.z, two.w));
                         }
@@ -482,106 +439,56 @@ __device__ __forceinline__ void consume(unsigned char *smem, const Params &p, co
             }
             }
         }
-        c0 += (uint32_t)steps;
 
         // ---------------------------------------------------- the piece's end
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            float2 v = l[i];
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-                v.x += __shfl_xor_sync(0xffffffffu, v.x, d);
-                v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int line = 8 * i + 2 * j + u;
-                if (r == 0) ml[warp * C::kLines + line] = make_float2(u ? m[i].y : m[i].x, u ? v.y : v.x);
-                // columns ND r .. of the line, four at a time; where they go turns with the line (the banks)
-                float *row = part + (size_t)(warp * C::kLines + line) * DP;
-#pragma unroll
-                for (int n = 0; n < ND; n += 4) {
-                    const int chunk = r * (ND / 4) + n / 4;
-                    *reinterpret_cast<float4 *>(row + 4 * ((chunk & ~7) | ((chunk + (line >> 1)) & 7))) =
-                        make_float4(O[i][n / 2][u], O[i][n / 2][2 + u], O[i][n / 2 + 1][u], O[i][n / 2 + 1][2 + u]);
-                }
-            }
-        }
-        Piece y;
-        y.r = -1;
-        ok = ok && wait_piece(now + 1);
-        if (ok) y = piece_at(now + 1);
-        if (meet(32 * C::NW, !ok)) {
-            tc::cp_async_wait<0>();
-            return;
-        }
-        if (lane == 0) tc::mbar_arrive(&queue_empty[now % kQueue]);
-        ++now;
-        if (!cp.any()) seek();
         {
             const int h = x.head / p.subs, sub = x.head - h * p.subs;
-            const int head0 = h * p.G + sub * p.heads, heads = min(p.heads, p.G - sub * p.heads);
             const bool whole = x.slot < 0;
-            constexpr int kChunks = DP / 4;
-            for (int i = threadIdx.x; i < x.n * p.heads * kChunks; i += 32 * C::NW) {
-                const int line = i / kChunks, chunk = i % kChunks, jj = line / p.heads, g = line - jj * p.heads;
-                float M = -INFINITY, L = 0.f;
 #pragma unroll
-                for (int w = 0; w < C::NW; ++w) M = fmaxf(M, ml[w * C::kLines + line].x);
-                const float ref = M == -INFINITY ? 0.f : M;
-                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                const int place = 4 * ((chunk & ~7) | ((chunk + (line >> 1)) & 7));
+            for (int i = 0; i < NT; ++i) {
+                float2 sum = l[i];
 #pragma unroll
-                for (int w = 0; w < C::NW; ++w) {
-                    const float2 v = ml[w * C::kLines + line];
-                    const float f = ex2(v.x - ref);
-                    const float4 o = *reinterpret_cast<const float4 *>(part + (size_t)(w * C::kLines + line) * DP + place);
-                    L = fmaf(f, v.y, L);
-                    sum.x = fmaf(f, o.x, sum.x), sum.y = fmaf(f, o.y, sum.y), sum.z = fmaf(f, o.z, sum.z), sum.w = fmaf(f, o.w, sum.w);
+                for (int d = 4; d < 32; d <<= 1) {
+                    sum.x += __shfl_xor_sync(0xffffffffu, sum.x, d);
+                    sum.y += __shfl_xor_sync(0xffffffffu, sum.y, d);
                 }
-                if (g >= heads) continue;
-                const int d = 4 * chunk;
-                const float f = (whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f) * 8.f;
-                sum.x *= f, sum.y *= f, sum.z *= f, sum.w *= f;
-                const size_t at = (size_t)(x.row0 + x.first + jj) * a.Hq + head0 + g, to = (size_t)(whole ? 0 : x.slot) * p.lines + line;
-                if (d < a.D) {
-                    if (whole)
-                        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at * a.D + d) =
-                            make_uint2(pack(sum.x, sum.y), pack(sum.z, sum.w));
-                    else
-                        *reinterpret_cast<float4 *>(p.part_o + to * p.stride + d) = sum;
-                }
-                if (chunk == 0) {
-                    if (!whole) p.part_ml[to] = make_float2(M, L);
-                    else if (a.lse) a.lse[at] = lse_of(M, L);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int line = 8 * i + 2 * j + u, jj = line / p.heads, g = line - jj * p.heads;
+                    if (jj >= x.n || sub * p.heads + g >= p.G) continue;
+                    const float M = u ? m[i].y : m[i].x, L = u ? sum.y : sum.x;
+                    const float f = (whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f) * 8.f;  // (values were multiplied as eighths)
+                    const size_t at = (size_t)(x.row0 + x.first + jj) * a.Hq + h * p.G + sub * p.heads + g, to = (size_t)(whole ? 0 : x.slot) * p.lines + line;
+                    if (C::FULL || r * ND < a.D) {
+                        if (whole) {
+                            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + at * a.D + r * ND;
+#pragma unroll
+                            for (int t = 0; t < ND / 2; t += 4)
+                                *reinterpret_cast<uint4 *>(out + 2 * t) =
+                                    make_uint4(pack(O[i][t][u] * f, O[i][t][2 + u] * f), pack(O[i][t + 1][u] * f, O[i][t + 1][2 + u] * f),
+                                               pack(O[i][t + 2][u] * f, O[i][t + 2][2 + u] * f), pack(O[i][t + 3][u] * f, O[i][t + 3][2 + u] * f));
+                        } else {
+                            float *out = p.part_o + to * p.stride + r * ND;
+#pragma unroll
+                            for (int t = 0; t < ND / 2; t += 2)
+                                *reinterpret_cast<float4 *>(out + 2 * t) =
+                                    make_float4(O[i][t][u] * f, O[i][t][2 + u] * f, O[i][t + 1][u] * f, O[i][t + 1][2 + u] * f);
+                        }
+                    }
+                    if (r == 0) {
+                        if (!whole) p.part_ml[to] = make_float2(M, L);
+                        else if (a.lse) a.lse[at] = lse_of(M, L);
+                    }
                 }
             }
         }
-        if (y.r >= 0) load_queries<C>(smem, p, y);
-        if (meet(32 * C::NW, false)) return;
-        x = y;
+        // the next piece, which is known, and the one after it
+        ++now;
+        if (mine.x[now & 1].r < 0) return;
+        __syncwarp();
+        take(now + 1);
+        if (!cp.any()) seek();
     }
-}
-
-template <typename C>
-__global__ void __launch_bounds__(C::kThreads, 1) tree_attention4_mma(const __grid_constant__ Params p) {
-    extern __shared__ __align__(1024) unsigned char smem[];
-    uint64_t *queue_full = reinterpret_cast<uint64_t *>(smem + C::kOffBar), *queue_empty = queue_full + kQueue;
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::kOffMisc);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kQueue; ++i) {
-            tc::mbar_init(&queue_full[i], 1);
-            tc::mbar_init(&queue_empty[i], C::NW);
-        }
-        *abort_flag = 0;
-        tc::fence_mbar_init();
-    }
-    after_predecessor();
-    __syncthreads();
-    const Waiter wait{abort_flag, p.a.err};
-    if (threadIdx.x >= 32 * C::NW) hand_out<C>(smem, p, wait, queue_full, queue_empty);
-    else consume<C>(smem, p, wait, queue_full, queue_empty);
 }
 
 template <typename C>
@@ -593,27 +500,28 @@ cudaError_t launch_mma_as(const Params &p, int grid, cudaStream_t s) {
     return launch_close(kern, grid, C::kThreads, C::kSmem, s, p);
 }
 
-template <int DP, bool FULL>
-cudaError_t launch_lines(const Params &p, int nt, int grid, cudaStream_t s) {
-    return nt == 1   ? launch_mma_as<MmaShape<DP, 1, FULL>>(p, grid, s)
-           : nt == 2 ? launch_mma_as<MmaShape<DP, 2, FULL>>(p, grid, s)
-                     : launch_mma_as<MmaShape<DP, 4, FULL>>(p, grid, s);
-}
-
 }  // namespace
+
+// shares: one per warp
+int mma4_grid() { return sm_count() * MmaShape<128, 1, true>::NW; }
 
 cudaError_t launch_mma4(Params p, int grid, cudaStream_t s) {
     const dspark_tree_attention_args &a = p.a;
-    p.tile_log2 = kTileLog2;
+    p.tile_log2 = kStepLog2;
     p.small_rows = p.block_rows;
     p.small_places = p.large_places = div_by(1);
     p.page = div_by(a.page);
     p.ctas = div_by(grid);
     p.unit_cost = kMmaUnitCost;
-    const int nt = p.lines <= 8 ? 1 : p.lines <= 16 ? 2 : 4;
-    if (a.D == 128) return launch_lines<128, true>(p, nt, grid, s);
-    if (a.D == 64) return launch_lines<64, true>(p, nt, grid, s);
-    return a.D > 64 ? launch_lines<128, false>(p, nt, grid, s) : launch_lines<64, false>(p, nt, grid, s);
+    const int ctas = sm_count();
+    if (p.lines <= 8) {
+        if (a.D == 128) return launch_mma_as<MmaShape<128, 1, true>>(p, ctas, s);
+        if (a.D == 64) return launch_mma_as<MmaShape<64, 1, true>>(p, ctas, s);
+        return a.D > 64 ? launch_mma_as<MmaShape<128, 1, false>>(p, ctas, s) : launch_mma_as<MmaShape<64, 1, false>>(p, ctas, s);
+    }
+    if (a.D == 128) return launch_mma_as<MmaShape<128, 2, true>>(p, ctas, s);
+    if (a.D == 64) return launch_mma_as<MmaShape<64, 2, true>>(p, ctas, s);
+    return a.D > 64 ? launch_mma_as<MmaShape<128, 2, false>>(p, ctas, s) : launch_mma_as<MmaShape<64, 2, false>>(p, ctas, s);
 }
 
 }  // namespace attn

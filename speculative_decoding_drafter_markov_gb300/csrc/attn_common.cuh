@@ -38,9 +38,10 @@ __device__ __forceinline__ int plain_column(int d) {
     return (d & ~15) + 8 * pair + 2 * (in16 >> 2) + (d & 1);
 }
 
-// The CTA's share, found by one warp (all its lanes come here and get it): a run of
-// requests per lane, no barrier.
-__device__ inline Share share_of(const Params &p) {
+// The share of CTA `cta` of `grid` -- or of a warp, where the work is cut among warps --,
+// found by one warp (all its lanes come here and get it): a run of requests per lane, no
+// barrier.
+__device__ inline Share share_of(const Params &p, int cta, int grid) {
     const int lane = threadIdx.x & 31, R = p.a.R;
     const int per = (R + 31) / 32, r0 = min(R, lane * per), r1 = min(R, r0 + per);
     long long mine = 0;
@@ -51,7 +52,7 @@ __device__ inline Share share_of(const Params &p) {
         asm volatile("prefetch.global.L1 [%0];" ::"l"(p.a.len + r));
     }
 #pragma unroll 1
-    for (int r = r0; r < r1; ++r) mine = add_places(mine, request_places(p, p.request(r, blockIdx.x == 0)));
+    for (int r = r0; r < r1; ++r) mine = add_places(mine, request_places(p, p.request(r, cta == 0)));
     long long inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -59,11 +60,11 @@ __device__ inline Share share_of(const Params &p) {
         if (lane >= d) inc = add_places(inc, y);
     }
     long long total = __shfl_sync(0xffffffffu, inc, 31);
-    if (total > (long long)gridDim.x * kMostShare) {
-        if (lane == 0 && blockIdx.x == 0) set_err(p.a.err, DSPARK_ERR_UNSUPPORTED);
+    if (total > (long long)grid * kMostShare) {
+        if (lane == 0 && cta == 0) set_err(p.a.err, DSPARK_ERR_UNSUPPORTED);
         total = 0;
     }
-    Share s = share_places(p, total, blockIdx.x, gridDim.x);
+    Share s = share_places(p, total, cta, grid);
     if (s.n == 0) return s;
     long long begin = inc - mine;
     int r = r0;
@@ -79,6 +80,8 @@ __device__ inline Share share_of(const Params &p) {
     s.r_begin = __shfl_sync(0xffffffffu, begin, from);
     return s;
 }
+
+__device__ inline Share share_of(const Params &p) { return share_of(p, blockIdx.x, gridDim.x); }
 
 __device__ __forceinline__ void store_out(const Params &p, size_t at, float v) {
     if (p.a.dtype == DSPARK_BF16) static_cast<__nv_bfloat16 *>(p.a.out)[at] = __float2bfloat16_rn(v);
@@ -97,7 +100,8 @@ cudaError_t launch_tc(const Params &p, int grid, cudaStream_t s);
 // over a cache in 4 bits, cut in the same way
 bool tc4_supported(const dspark_tree_attention_args &a);
 cudaError_t launch_tc4(const Params &p, int grid, cudaStream_t s);
-// the same for units of 8, 16 or 32 lines (what launch_tc4 takes, it takes)
+// the same for units of 8 or 16 lines, cut among warps (what launch_tc4 takes, it takes)
+int mma4_grid();  // shares
 cudaError_t launch_mma4(Params p, int grid, cudaStream_t s);
 // the fp32 kernel: units of kSimtLines lines, as the general CUDA-core kernel
 constexpr int kSimtLines = 16;
