@@ -249,20 +249,30 @@ struct Cells {
     }
 };
 
-// kCols: groups of 32 E columns that a line has
-template <int E, int kCols>
-__global__ void __launch_bounds__(32 * kJoinWarps, 8) tree_attention_join(const __grid_constant__ Params p) {
+// kCols: groups of 32 E columns that a line has; kShares: CTAs' or warps' shares that a CTA here
+// looks after.  (Of the shares of 1824 warps one each took 11 us where 8 units had a piece to
+// join in 32 of them, and 14 where 1024 units had two or three.)
+template <int E, int kCols, int kShares>
+__global__ void __launch_bounds__(32 * kJoinWarps, 8) tree_attention_join(const __grid_constant__ Params p, int shares) {
     __shared__ float sum_o[kJoinWarps - 1][32 * E * kCols];
     after_predecessor();  // the partials are written
-    const Join n = p.join[blockIdx.x];
+    unsigned todo = 1;
+    if (kShares > 1) {
+        const int mine = blockIdx.x * kShares + (threadIdx.x & 31);
+        todo = __ballot_sync(0xffffffffu, (threadIdx.x & 31) < kShares && mine < shares && p.join[mine].pieces != 0);
+    }
+    for (; todo; todo &= todo - 1) {
+    const int share = blockIdx.x * kShares + (kShares > 1 ? __ffs(todo) - 1 : 0);
+    const Join n = p.join[share];
     if (n.pieces == 0) return;
+    if (kShares > 1) __syncthreads();  // sum_o of the share before was read
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.stride;
     // rounds of kAhead partials, and one for the weights, either way
     const int y = gridDim.y, turns = (n.lines + y - 1) / y, turns_warp = (n.lines + y * kJoinWarps - 1) / (y * kJoinWarps);
     const bool many = turns * ((n.pieces + kAhead * kJoinWarps - 1) / (kAhead * kJoinWarps) + 1) <
                       turns_warp * ((n.pieces + kAhead - 1) / kAhead + 1);
     // partial i: the first one, then the first partials of the CTAs after it
-    auto slot = [&](int i, int ln) { return (size_t)(i == 0 ? n.first : 2 * ((int)blockIdx.x + i)) * p.lines + ln; };
+    auto slot = [&](int i, int ln) { return (size_t)(i == 0 ? n.first : 2 * (share + i)) * p.lines + ln; };
     const int step = many ? kJoinWarps : 1;  // pieces of this warp: own, own + step, ..
     const int own = many ? warp : 0;
     for (int ln = many ? blockIdx.y : blockIdx.y * kJoinWarps + warp; ln < n.lines; ln += many ? gridDim.y : gridDim.y * kJoinWarps) {
@@ -344,6 +354,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 8) tree_attention_join(const 
             }
         if (p.a.lse && lane == 0) p.a.lse[at] = lse_of(M, L);
     }
+    }
 }
 
 template <typename T, int kDV, bool kFour = false>
@@ -383,17 +394,20 @@ static bool few_lines(const dspark_tree_attention_args &a) { return (long long)a
 
 // the columns that they get
 static int mma_lines(const dspark_tree_attention_args &a) { return a.max_rows * (a.Hq / a.H) <= 8 ? 8 : 16; }
-cudaError_t launch_join(const Params &p, int grid, cudaStream_t s) {
+cudaError_t launch_join(const Params &p, int grid, cudaStream_t s, bool warps) {
     // a CTA for every line of a unit, as far as the host knows them; the first launch lets
     // them come up while it runs
     const long long lines = (long long)p.a.max_rows * p.heads;
     unsigned y = (unsigned)(lines < 1 ? 1 : lines < p.lines ? lines : p.lines);
     if (y > 32) y = 32;
-    // of many shares, warps', few have a unit to join, and that has few lines: a warp a line
-    if (grid > 4 * sm_count()) y = (y + kJoinWarps - 1) / kJoinWarps;
-    auto kern = p.stride % 4 == 0 ? (p.stride <= 128 ? tree_attention_join<4, 1> : tree_attention_join<4, 2>)
-                                  : (p.stride <= 64 ? tree_attention_join<1, 2> : tree_attention_join<1, 8>);
-    return launch_close(kern, dim3(grid, y), 32 * kJoinWarps, 0, s, p);
+    if (warps) {  // shares of warps: strides of 16 to 128 floats
+        constexpr int kShares = 4;
+        auto kern = tree_attention_join<4, 1, kShares>;
+        return launch_close(kern, dim3((grid + kShares - 1) / kShares, y), 32 * kJoinWarps, 0, s, p, grid);
+    }
+    auto kern = p.stride % 4 == 0 ? (p.stride <= 128 ? tree_attention_join<4, 1, 1> : tree_attention_join<4, 2, 1>)
+                                  : (p.stride <= 64 ? tree_attention_join<1, 2, 1> : tree_attention_join<1, 8, 1>);
+    return launch_close(kern, dim3(grid, y), 32 * kJoinWarps, 0, s, p, grid);
 }
 
 }  // namespace attn
@@ -520,7 +534,7 @@ cudaError_t launch_tree_attention4(const dspark_tree_attention_args &a, void *ws
         if (few) cut_for_mma(p, ws, shares);
         else cut_for_tc(p, ws, grid);
         cudaError_t e = few ? launch_mma4(p, shares, s) : launch_tc4(p, grid, s);
-        return e == cudaSuccess ? launch_join(p, shares, s) : e;
+        return e == cudaSuccess ? launch_join(p, shares, s, few) : e;
     }
     cut_for_simt(p);
     return launch_simt<true>(p, ws, s);

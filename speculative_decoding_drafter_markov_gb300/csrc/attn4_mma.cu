@@ -9,10 +9,10 @@
 //
 // A unit's lines (rows x query heads of a group) are NT times 8, the columns of the products;
 // their rows are tokens, and then columns of values.  The work is cut among the warps of the
-// whole GPU: each walks a share of its own, in tiles of 32 tokens, with a running maximum and
+// whole GPU: each walks a share of its own, in steps of 32 tokens, with a running maximum and
 // sum and 8 NT x D sums, and leaves what it has of a unit as a partial.  (Cut among CTAs, whose
 // warps took turns and met at the end of every unit, 128 caches of up to 16384 tokens took
-// @CTA@ us.)  A warp copies its tiles itself, by cp.async into slots of its own,
+// @CTA@ us.)  A warp copies its steps itself, by cp.async into slots of its own,
 // the next ones while it works on one, on into the next piece.  (Bulk copies by one warp
 // took 80 clocks each to issue, 1900 to 2600 per 128 tokens: more than all the rest.)
 // Per 16 tokens:
@@ -28,6 +28,8 @@
 // What bounds it are the instructions that unpack: per two elements a mask with an
 // exponent (half rate), 3/4 of a shift for keys, 1/4 and as many byte permutations for values, and
 // one (keys) or two (values) fp16 operations, all of half the rate of fp32; 32 NT matrix products of 8 clocks.
+#include <new>
+
 #include "attn_tc_kernel.cuh"
 
 namespace dspark {
@@ -35,7 +37,8 @@ namespace attn {
 
 namespace {
 
-constexpr int kStepLog2 = 5, kStep = 1 << kStepLog2;  // tokens of a tile
+constexpr int kStepLog2 = 5, kStep = 1 << kStepLog2;  // tokens of a step
+constexpr int kMmaTileLog2 = 6;                       // of a tile, the least that a warp has of a unit
 constexpr float kLift = 7.f;  // the reference stands below the maximum, as in attn_tc_kernel.cuh
 constexpr int kMmaUnitCost = 4;
 
@@ -55,7 +58,7 @@ struct MmaShape {
     static constexpr int kSlot = kStep * DP / 16 * 18;  // codes of keys, of values, scales of keys, of values
     static constexpr int kQ = NT == 1 ? 0 : NT * DP / 16 * 256;  // uint2 [DP / 16][32][NT]; with 8 lines they stay in registers
     static constexpr int kPieces = (int)(sizeof(Pieces) + 15) / 16 * 16;
-    static constexpr int kDepth = NT == 1 ? 4 : 3;      // slots, a tile each
+    static constexpr int kDepth = NT == 1 ? 4 : 3;      // slots, a step each
     static constexpr int kWarp = kDepth * kSlot + kQ + kPieces;
     static constexpr int kSmem = NW * kWarp;
     static_assert(kSlot % 16 == 0, "places");
@@ -77,13 +80,19 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
+// steps of a piece: the first one, and the one after its last
+__device__ __forceinline__ int first_step(const Piece &x) { return x.t0 << (kMmaTileLog2 - kStepLog2); }
+__device__ __forceinline__ int last_step(const Piece &x) {
+    return min(x.t1 << (kMmaTileLog2 - kStepLog2), (int)(((unsigned)x.tokens + kStep - 1) >> kStepLog2));
+}
+
 // ---------------------------------------------------------------- a warp's copies
-// The next tile to copy: tile t of the warp's piece `piece` (counted over its pieces, the one
+// The next step to copy: step t of the warp's piece `piece` (counted over its pieces, the one
 // after the piece worked on at most), its first token and the pages of its four groups of
-// eight tokens (lane % 4), fetched a tile ahead.
+// eight tokens (lane % 4), fetched a step ahead.
 struct Copies {
     int piece, t, t1;  // t >= t1: none is left in the piece
-    int tok0, last;    // first token of the tile; the unit's last one
+    int tok0, last;    // first token of the step; the unit's last one
     int page, off;     // of this lane's group: page, token in it
     int h;             // key-value head
     uint32_t issued, used;
@@ -124,12 +133,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention4_mma(const __gr
     const int cta = blockIdx.x * C::NW + warp;  // of as many shares as there are warps
     {
         const Share share = share_of(p, cta, gridDim.x * C::NW);
-        Walk<Params> walk(p, share);
         if (lane == 0) {
             p.join[cta].pieces = 0;
-            memcpy(static_cast<void *>(&mine.walk), &walk, sizeof walk);
+            new (&mine.walk) Walk<Params>(p, share);
         }
-        __syncwarp();
     }
     // takes the next piece of the walk into its place (n: counted over the warp's pieces); r < 0: none is left
     auto take = [&](int n) {
@@ -142,14 +149,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention4_mma(const __gr
     };
     int now = 0;  // the piece worked on
     Copies cp{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0};
-    // to the next tile, in the piece worked on or the one after it, and its pages
+    // to the next step, in the piece worked on or the one after it, and its pages
     auto seek = [&]() {
         if (!cp.any()) {
             if (cp.piece > now) return;
             const Piece &y = mine.x[++cp.piece & 1];
             if (y.r < 0) return;
-            cp.t = y.t0;
-            cp.t1 = y.t1;
+            cp.t = first_step(y);
+            cp.t1 = last_step(y);
             cp.last = y.tokens - 1;
             cp.h = p.subs == 1 ? y.head : y.head / p.subs;
         }
@@ -221,9 +228,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention4_mma(const __gr
                 else q[(k * 32 + lane) * NT + i] = v;  // (each lane reads what it wrote)
             }
 #pragma unroll 1
-        for (int s = x.t0; s < x.t1; ++s) {
+        for (int s = first_step(x); s < last_step(x); ++s) {
             int tok0 = s << kStepLog2;
-            // copies of this tile: the oldest; all but it may be under way where the slots are full
+            // copies of this step: the oldest; all but it may be under way where the slots are full
             if (cp.issued - cp.used == (uint32_t)C::kDepth) tc::cp_async_wait<C::kDepth - 1>();
             else tc::cp_async_wait<0>();
             __syncwarp();
@@ -507,7 +514,7 @@ int mma4_grid() { return sm_count() * MmaShape<128, 1, true>::NW; }
 
 cudaError_t launch_mma4(Params p, int grid, cudaStream_t s) {
     const dspark_tree_attention_args &a = p.a;
-    p.tile_log2 = kStepLog2;
+    p.tile_log2 = kMmaTileLog2;
     p.small_rows = p.block_rows;
     p.small_places = p.large_places = div_by(1);
     p.page = div_by(a.page);

@@ -108,7 +108,8 @@ constexpr int kSimtLines = 16;
 bool f32_supported(const dspark_tree_attention_args &a);
 int f32_grid();
 cudaError_t launch_f32(Params p, int grid, cudaStream_t s);
-cudaError_t launch_join(const Params &p, int grid, cudaStream_t s);
+// warps: the shares are warps' (launch_mma4)
+cudaError_t launch_join(const Params &p, int grid, cudaStream_t s, bool warps = false);
 
 }  // namespace attn
 }  // namespace dspark
