@@ -389,11 +389,16 @@ void carve(Params &p, void *ws, int grid) {
     p.part_o = reinterpret_cast<float *>(c);
 }
 
-// whether a request's lines, as far as the host knows, fit 16 columns
-static bool few_lines(const dspark_tree_attention_args &a) { return (long long)a.max_rows * (a.Hq / a.H) <= 16; }
+// A cache in 4 bits: whether a request's lines, as far as the host knows, are few enough for
+// the warps' own products, in units of 16 lines at most, each of which unpacks the cache
+// for itself.  64 caches of up to 8192 tokens, 4 lines a row: up to 5 rows 123 us, against 194 on
+// tcgen05, 9 rows 140 and 198, 12 rows 195 and 213, 16 rows 234 and 228, 24 rows 289 and 209;
+// 8 caches of up to 131072 tokens: 9 rows 350 and 333, 17 rows 590 and 489.
+static bool few_lines(const dspark_tree_attention_args &a) { return (long long)a.max_rows * (a.Hq / a.H) <= 48; }
 
-// the columns that they get
+// a unit's lines.  (Units of 32 took 162 us where ones of 16 take 140.)
 static int mma_lines(const dspark_tree_attention_args &a) { return a.max_rows * (a.Hq / a.H) <= 8 ? 8 : 16; }
+
 cudaError_t launch_join(const Params &p, int grid, cudaStream_t s, bool warps) {
     // a CTA for every line of a unit, as far as the host knows them; the first launch lets
     // them come up while it runs
@@ -456,9 +461,10 @@ void cut_for_tc(Params &p, void *ws, int grid) {
 
 // units of 8 or 16 lines
 void cut_for_mma(Params &p, void *ws, int shares) {
-    p.heads = p.G;
-    p.subs = 1;
-    p.block_rows = mma_lines(p.a) / p.heads;
+    const int most = mma_lines(p.a);
+    p.heads = p.G < most ? p.G : most;
+    p.subs = (p.G + p.heads - 1) / p.heads;
+    p.block_rows = most / p.heads;
     p.lines = p.block_rows * p.heads;
     p.stride = p.a.D;
     carve(p, ws, shares);

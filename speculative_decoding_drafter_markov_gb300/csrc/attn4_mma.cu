@@ -12,7 +12,7 @@
 // whole GPU: each walks a share of its own, in steps of 32 tokens, with a running maximum and
 // sum and 8 NT x D sums, and leaves what it has of a unit as a partial.  (Cut among CTAs, whose
 // warps took turns and met at the end of every unit, 128 caches of up to 16384 tokens took
-// @CTA@ us.)  A warp copies its steps itself, by cp.async into slots of its own,
+// 344 us.)  A warp copies its steps itself, by cp.async into slots of its own,
 // the next ones while it works on one, on into the next piece.  (Bulk copies by one warp
 // took 80 clocks each to issue, 1900 to 2600 per 128 tokens: more than all the rest.)
 // Per 16 tokens:
@@ -40,7 +40,7 @@ namespace {
 constexpr int kStepLog2 = 5, kStep = 1 << kStepLog2;  // tokens of a step
 constexpr int kMmaTileLog2 = 6;                       // of a tile, the least that a warp has of a unit
 constexpr float kLift = 7.f;  // the reference stands below the maximum, as in attn_tc_kernel.cuh
-constexpr int kMmaUnitCost = 4;
+constexpr int kMmaUnitCost = 2;  // tiles: a unit's start and end (1 and 2 measured alike, 4 and 8 by 3 to 6 % worse)
 
 // A warp's place in its share: the piece that it works on and the next one, and the walk
 // (in shared memory: they are looked at between pieces).

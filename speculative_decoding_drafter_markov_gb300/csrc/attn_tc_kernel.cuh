@@ -169,6 +169,11 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
     const __nv_bfloat162 two = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&two);
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     const __half2 two = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&two);
@@ -632,7 +637,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                             tc::tmem_ld32(s_half + c, s);
                             tc::tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) mx[i & 1] = fmaxf(mx[i & 1], s[i]);
+                            for (int i = 0; i < 32; i += 2) mx[(i >> 1) & 1] = max3(mx[(i >> 1) & 1], s[i], s[i + 1]);
                         }
                         const float top = fmaxf(mx[0], mx[1]) * scale;
                         const bool over = top > m + (kSlack + C::kLift);

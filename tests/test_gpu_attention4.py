@@ -78,6 +78,41 @@ def test_single_rows(dtype, Hq, D):
     check(s, *call(s))
 
 
+@pytest.mark.parametrize("Hq,H,D,page,rows", [(16, 1, 128, 16, 1), (9, 1, 64, 16, 1), (24, 2, 96, 16, 4), (6, 2, 128, 8, 5), (48, 2, 64, 32, 2), (20, 1, 80, 16, 2),
+                                              (4, 1, 128, 16, 12), (15, 5, 48, 16, 3), (40, 1, 128, 64, 1), (2, 2, 32, 16, 48), (17, 1, 128, 16, 2)])
+def test_few_lines(Hq, H, D, page, rows):
+    """Units of 8 and of 16 lines: groups that fill them, that leave some over, that take several."""
+    lens = [0, 40, 700, 64, 1500, 31, 33]
+    for tree in (False, True):
+        s = make4(lens, [rows, 1, max(1, rows - 1), rows, (rows + 1) // 2, rows, 1], Hq, H, D, page, torch.bfloat16, seed=Hq + D, tree=tree)
+        check(s, *call(s))
+
+
+def test_no_rows_at_all():
+    s = make4([50, 0, 7], [1, 1, 1], 4, 2, 64, 16, torch.bfloat16)
+    out = {"out": torch.full((3, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda"), "lse": torch.full((3, 4), 7.0, device="cuda")}
+    for rows in (1, 40):
+        err = err_word()
+        dsp.tree_attention4(s["q"], s["k4"], s["v4"], s["table"], ints(s["lens"]), ints([0, 0, 0, 0]), max_rows=rows, out=out, err=err)
+        assert int(err) == 0 and (out["out"] == 7).all() and (out["lse"] == 7).all()
+
+
+@pytest.mark.parametrize("rows", [[2, 1, 1], [40, 2, 30]])
+def test_two_at_once(rows):
+    """Two calls on two streams, each with a workspace of its own, and again on one."""
+    cases = [make4([2000, 40, 333], rows, 8, 2, 128, 16, torch.bfloat16, seed=i) for i in range(2)]
+    want = [expect(s) for s in cases]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in cases]
+    for _ in range(3):
+        got = [call(s, stream=side) for s, side in zip(cases, sides)]
+        torch.cuda.synchronize()
+        for s, (o, err), w in zip(cases, got, want):
+            check(s, o, err, w)
+    for s, w in zip(cases, want):
+        check(s, *call(s), w)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("n,ctx,G", [(1, 0, 4), (64, 100, 1), (65, 127, 2), (128, 300, 4), (256, 1000, 3), (200, 5, 8)])
 def test_trees(dtype, n, ctx, G):
