@@ -391,9 +391,9 @@ void carve(Params &p, void *ws, int grid) {
 
 // A cache in 4 bits: whether a request's lines, as far as the host knows, are few enough for
 // the warps' own products, in units of 16 lines at most, each of which unpacks the cache
-// for itself.  64 caches of up to 8192 tokens, 4 lines a row: up to 5 rows 123 us, against 194 on
-// tcgen05, 9 rows 140 and 198, 12 rows 195 and 213, 16 rows 234 and 228, 24 rows 289 and 209;
-// 8 caches of up to 131072 tokens: 9 rows 350 and 333, 17 rows 590 and 489.
+// for itself.  64 caches of up to 8192 tokens, 4 lines a row: up to 5 rows 121 us, against 193 on
+// tcgen05, 9 rows 141 and 191, 12 rows 192 and 202, 16 rows 229 and 220, 24 rows 289 and 199;
+// 8 caches of up to 131072 tokens: 9 rows 339 and 330, 17 rows 590 and 460.
 static bool few_lines(const dspark_tree_attention_args &a) { return (long long)a.max_rows * (a.Hq / a.H) <= 48; }
 
 // a unit's lines.  (Units of 32 took 162 us where ones of 16 take 140.)

@@ -31,8 +31,14 @@ template <int DP_, int NQ_, bool FOUR_ = false>
 struct Shape {
     static constexpr int DP = DP_, NQ = NQ_;
     static constexpr bool FOUR = FOUR_;
-    static constexpr int kThreads = FOUR ? 640 : 384;
-    static constexpr int kReaders = FOUR ? 19 : 11;  // of pieces: two copy warps, the MMA warp, eight softmax warps, eight that unpack
+    // Warps that unpack keys, and as many values.  Two of each leave the softmax 128 registers a thread, which hold a row's
+    // 64 scores at once (kHold), four of each 96, and the scores are read twice from tensor memory, 32 at a time.
+    // One operand (8 caches of up to 131072 tokens, up to 128 lines): 461 us with two of each, 485 with four.  Two operands want
+    // a tile in half the time per line: 16 trees of up to 64 rows 168 and 152.
+    static constexpr int kUnpack = NQ == 1 ? 2 : 4;
+    static constexpr bool kHold = !FOUR || NQ == 1;
+    static constexpr int kThreads = FOUR ? 384 + 64 * kUnpack : 384;
+    static constexpr int kReaders = FOUR ? 11 + 2 * kUnpack : 11;  // of pieces: two copy warps, the MMA warp, eight softmax warps, those that unpack
     static constexpr int kCols = DP / 64;        // a row is copied in blocks of 64 columns
     static constexpr int kBlock = 128 * 128;     // 128 rows of 64 16-bit elements
     static constexpr int kSlot = kCols * kBlock;
@@ -179,15 +185,16 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&two);
 }
 
-// The role of the eight warps that unpack tiles of a cache in 4 bits into the ring, four of
-// them keys (kKeys) as the bf16 numbers that they are, four values as the eighths of them in
+// The role of the warps that unpack tiles of a cache in 4 bits into the ring, half of them
+// keys (kKeys) as the bf16 numbers that they are, half values as the eighths of them in
 // fp16 (the whole range of n s, 2^-16 to 401408, is exact there, and the weights beside them
 // may be fp16).  A lane has 16 elements of a row, a scale's, per turn.
 template <typename C, bool kKeys>
 __device__ __forceinline__ void unpack_tiles(unsigned char *smem, const dspark_tree_attention_args &a, int warp, const Waiter &wait,
                                              Queue &queue, uint64_t *copied, uint64_t *copy_free, uint64_t *full, uint64_t *empty,
-                                             int op_rows, int G) {
+                                             int op_rows) {
     constexpr int kLanes = C::DP / 16, kRows = 32 / kLanes, kTurns = 8 / kRows;  // lanes of a row, rows of a turn, turns of eight rows
+    constexpr int kEights = 16 / C::kUnpack;  // eights of rows of a tile and warp
     const int lane = threadIdx.x & 31, g = lane % kLanes, row = lane / kLanes;
     const bool in = 16 * g < a.D;
     // Lanes of the upper columns write their second piece first, so that eight lanes' pieces fall on all banks; the second
@@ -195,13 +202,13 @@ __device__ __forceinline__ void unpack_tiles(unsigned char *smem, const dspark_t
     const bool flip = C::DP == 128 && g >= 4;
     const int first = (g >> 2) * C::kBlock + row * 128;
     const int piece0 = (((2 * g + (flip ? 1 : 0)) & 7) ^ row) << 4, piece1 = piece0 ^ 16;
-    const int code_row = a.D / 2, scale_row = a.D / 16;
+    const int code_row = a.D / 2, scale_row = a.D / 16, eight0 = kEights * warp;
     // columns beyond D: zeros in every slot, once
     if (!in) {
 #pragma unroll 1
-        for (int i = 0; i < C::NS * 4 * kTurns; ++i) {
-            const int t = i % kTurns, eight = 4 * warp + (i / kTurns) % 4;
-            unsigned char *at = smem + C::kOffRing + i / (4 * kTurns) * C::kSlot + first + eight * 1024 + t * kRows * 128;
+        for (int i = 0; i < C::NS * kEights * kTurns; ++i) {
+            const int t = i % kTurns, eight = eight0 + (i / kTurns) % kEights;
+            unsigned char *at = smem + C::kOffRing + i / (kEights * kTurns) * C::kSlot + first + eight * 1024 + t * kRows * 128;
             *reinterpret_cast<uint4 *>(at + (piece0 ^ (64 * t))) = make_uint4(0u, 0u, 0u, 0u);
             *reinterpret_cast<uint4 *>(at + (piece1 ^ (64 * t))) = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -211,10 +218,6 @@ __device__ __forceinline__ void unpack_tiles(unsigned char *smem, const dspark_t
     while (queue.read_warp(wait, x)) {
         const bool dual = C::NQ == 2 && x.n > op_rows;
         const int n = x.t1 - x.t0;
-        // This warp's rows of a tile, eight by eight: a softmax warp of each stream works beside warp q where the unit has
-        // lines 32 q and on; that warp gets fewer.
-        const int busy = dual ? 4 : min(4, (x.n * G + 31) >> 5), few = busy, many = busy < 4 ? (16 - busy * few) / (4 - busy) : 4;
-        const int eight0 = warp < busy ? warp * few : busy * few + (warp - busy) * many, eights = warp < busy ? few : many;
         for (int i = 0; i < n; ++i) {
             const uint32_t pos = base + (kKeys ? key_place(i, dual) : value_place(i, n, dual)), item = base / 2 + i;
             const int from = item % C::NP, slot = pos % C::NS;
@@ -228,7 +231,7 @@ __device__ __forceinline__ void unpack_tiles(unsigned char *smem, const dspark_t
             // Eight rows at a time and no more: the code of all roles has to stay in the SM's first instruction caches (with all 32
             // rows of a warp unrolled four of ten stalls were for instructions, and a tile took twice the time).
 #pragma unroll 1
-            for (int e8 = 0; e8 < eights; ++e8) {
+            for (int e8 = 0; e8 < kEights; ++e8) {
                 uint2 w[kTurns];
                 uint32_t b[kTurns];
 #pragma unroll
@@ -313,12 +316,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         tc::tc_fence_before();
     } else if (tid == 0) {
         for (int i = 0; i < C::NS; ++i) {
-            tc::mbar_init(&full[i], C::FOUR ? 4 : 1);
+            tc::mbar_init(&full[i], C::FOUR ? C::kUnpack : 1);
             tc::mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2 * C::NP; ++i) {
             tc::mbar_init(&copied[i], 1);
-            tc::mbar_init(&copy_free[i], 4);
+            tc::mbar_init(&copy_free[i], C::kUnpack);
         }
         tc::mbar_init(&s_full[0], 1);
         tc::mbar_init(&s_full[1], 1);
@@ -530,8 +533,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     } else if (C::FOUR && warp >= 12) {
         // ------------------------------------------------------------ 4 bits to 16
         if constexpr (C::FOUR) {
-            if (warp < 16) unpack_tiles<C, true>(smem, a, warp - 12, wait, queue, copied, copy_free, full, empty, tp.op_rows, p.G);
-            else unpack_tiles<C, false>(smem, a, warp - 16, wait, queue, copied + C::NP, copy_free + C::NP, full, empty, tp.op_rows, p.G);
+            if (warp < 12 + C::kUnpack) unpack_tiles<C, true>(smem, a, warp - 12, wait, queue, copied, copy_free, full, empty, tp.op_rows);
+            else unpack_tiles<C, false>(smem, a, warp - 12 - C::kUnpack, wait, queue, copied + C::NP, copy_free + C::NP, full, empty, tp.op_rows);
         }
     } else {
         // ------------------------------------------------------------ softmax
@@ -627,7 +630,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                         }
                         tc::tmem_wait_st();
                     }
-                    if (C::FOUR && active) {
+                    if (!C::kHold && active) {
                         // 96 registers a thread (the warps that unpack need their share) and little code: 32 columns at
                         // a time, read from tensor memory for their maximum and again for their weights
                         float mx[2] = {-INFINITY, -INFINITY};
@@ -683,12 +686,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                         tc::tmem_wait_st();
                         tc::tc_fence_before();
                     }
-                    if (!C::FOUR && active) {
+                    if (C::kHold && active) {
                         float s[64];
                         tc::tmem_ld32(s_half, s);
                         tc::tmem_ld32(s_half + 32, s + 32);
                         tc::tmem_wait_ld();
-                        if (tail) {
+                        if (!C::FOUR && tail) {
 #pragma unroll
                             for (int c = 0; c < 2; ++c) {
                                 // lines beyond the unit's see nothing; what they hold is not read
@@ -698,30 +701,37 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                             }
                         }
                         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        if (C::FOUR) {
 #pragma unroll
-                        for (int i = 0; i < 64; i += 4)
+                            for (int i = 0; i < 64; i += 2) mx[(i >> 1) & 1] = max3(mx[(i >> 1) & 1], s[i], s[i + 1]);
+                        } else {
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], s[i + c]);
-                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-                        if (u == 0 && half == 0) {
+                            for (int i = 0; i < 64; i += 4)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], s[i + c]);
+                        }
+                        const float top = (C::FOUR ? fmaxf(mx[0], mx[1]) : fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]))) * scale;
+                        if (!C::FOUR && u == 0 && half == 0) {
                             m = top;
-                        } else if (__any_sync(0xffffffffu, top > m + kSlack)) {
-                            const float to = top > m + kSlack ? top : m;
+                        } else if (__any_sync(0xffffffffu, top > m + (kSlack + C::kLift))) {
+                            const float to = top > m + (kSlack + C::kLift) ? top - C::kLift : m;
                             const float f = to == -INFINITY ? 1.f : ex2(m - to);
                             m = to;
                             l *= f;
-                            // the products so far are in O: those of the tile before were
-                            // issued before this tile's S, that of the first half says so
-                            if (half == 1) ok = wait.warp(&half_done[w], count & 1u);
-                            tc::tc_fence_after();
+                            if (!C::FOUR || u > 0 || half > 0) {  // else nothing is in O
+                                // the products so far are in O: those of the tile before were
+                                // issued before this tile's S, that of the first half says so
+                                if (half == 1) ok = wait.warp(&half_done[w], count & 1u);
+                                tc::tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < C::DP; c += 16) {
-                                uint32_t o[16];
-                                tc::tmem_ld16(o_tmem + c, o);
-                                tc::tmem_wait_ld();
+                                for (int c = 0; c < C::DP; c += 16) {
+                                    uint32_t o[16];
+                                    tc::tmem_ld16(o_tmem + c, o);
+                                    tc::tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                tc::tmem_st16(o_tmem + c, o);
+                                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                    tc::tmem_st16(o_tmem + c, o);
+                                }
                             }
                         }
                         const float ref = m == -INFINITY ? 0.f : m;
@@ -734,7 +744,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
                             const float2 arg = fma2({s[2 * i], s[2 * i + 1]}, by, off);
                             const float2 e = {ex2(arg.x), ex2(arg.y)};
                             sum[i & 1] = add2(sum[i & 1], e);
-                            r[i] = pack(e.x, e.y);
+                            r[i] = C::FOUR ? pack_half(e.x, e.y) : pack(e.x, e.y);
                         }
                         tc::tmem_st32(s_half, r);
                         sum[0] = add2(sum[0], sum[1]);
