@@ -548,6 +548,18 @@ def cache_store(k, v, slot, k_cache, v_cache, *, err=None, stream=None):
     return (_bind or _target()).cache_store(k, v, slot, k_cache, v_cache, err)
 
 
+def _on_stream(stream, call, *args, **kw):
+    """call(*args, **kw) on `stream`; what the tensors of the call hold is kept from being handed out
+    again until the stream has come past it, so temporaries of another stream may be passed."""
+    with torch.cuda.stream(stream):
+        got = call(*args, **kw)
+    out = kw.get("out") or {}
+    for t in (*args, *kw.values(), *out.values()):
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    return got
+
+
 def rope_store(q, k, v, pos, freq, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, slot=None, k_cache=None,
                v_cache=None, out=None, err=None, stream=None):
     """Norms of the heads of q [N, Hq, D] and k [N, H, D] (where their weight [D] is given),
@@ -557,9 +569,8 @@ def rope_store(q, k, v, pos, freq, *, q_weight=None, k_weight=None, eps=1e-6, in
     fused projection are fine; q or k may be None.  Returns {"q"} and, without slot, {"k"}
     of the rows' shapes; an `out` passed in may hold q and k themselves, or views."""
     if stream is not None:
-        with torch.cuda.stream(stream):
-            return rope_store(q, k, v, pos, freq, q_weight=q_weight, k_weight=k_weight, eps=eps, interleaved=interleaved,
-                              slot=slot, k_cache=k_cache, v_cache=v_cache, out=out, err=err)
+        return _on_stream(stream, rope_store, q, k, v, pos, freq, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                          interleaved=interleaved, slot=slot, k_cache=k_cache, v_cache=v_cache, out=out, err=err)
     return (_bind or _target()).rope_store(q, k, v, pos, freq, q_weight, k_weight, eps, interleaved, slot, k_cache, v_cache,
                                            out, err)
 
@@ -577,8 +588,7 @@ def cache_store4(k, v, slot, k_cache, v_cache, *, values=False, out=None, err=No
     caches in 4 bits (from cache4).  With `values`, or with `out`, returns {"k", "v"}: what
     the cache then holds of the rows, in their type."""
     if stream is not None:
-        with torch.cuda.stream(stream):
-            return cache_store4(k, v, slot, k_cache, v_cache, values=values, out=out, err=err)
+        return _on_stream(stream, cache_store4, k, v, slot, k_cache, v_cache, values=values, out=out, err=err)
     return (_bind or _target()).cache_store4(k, v, slot, k_cache, v_cache, values, out, err)
 
 
@@ -609,9 +619,8 @@ def tree_attention4(q, k_cache, v_cache, table, lens, row_start, *, mask=None, s
     """tree_attention over caches in 4 bits (from cache4, filled by cache_store4); ws scratch
     of tree_attention4_workspace_size bytes."""
     if stream is not None:
-        with torch.cuda.stream(stream):
-            return tree_attention4(q, k_cache, v_cache, table, lens, row_start, mask=mask, scale=scale, max_rows=max_rows,
-                                   out=out, ws=ws, err=err)
+        return _on_stream(stream, tree_attention4, q, k_cache, v_cache, table, lens, row_start, mask=mask, scale=scale,
+                          max_rows=max_rows, out=out, ws=ws, err=err)
     return (_bind or _target()).tree_attention4(q, k_cache, v_cache, table, lens, row_start, mask, scale, max_rows, out, ws,
                                                 err)
 

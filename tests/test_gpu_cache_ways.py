@@ -150,6 +150,34 @@ def whole_text_logits(t, text):
     return norm(x) @ t.head.float().T
 
 
+def test_temporaries_on_a_busy_stream():
+    """What is passed with `stream` and let go at once is not handed out again before the stream has used it."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    H, D, page, N = 2, 64, 16, 33
+    rand = lambda *n: torch.randn(n, generator=g, device="cuda").bfloat16()  # noqa: E731
+    q, k, v, freq = rand(N, 4, D), rand(N, H, D), rand(N, H, D), torch.rand(D // 2, generator=g, device="cuda")
+    ints = lambda t: torch.as_tensor(t, dtype=torch.int32).cuda()  # noqa: E731
+    side = torch.cuda.Stream()
+
+    def run(stream):
+        caches = [dsp.cache4(3, H, page, D) for _ in range(2)]
+        torch.cuda.synchronize()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(20_000_000)
+        junk = []
+        turned = dsp.rope_store(q.clone(), k.clone(), None, ints(range(N)), freq, stream=stream)
+        junk += [torch.full((1 << i,), 3, dtype=torch.int32, device="cuda") for i in range(6, 13)]
+        dsp.cache_store4(k.clone(), v.clone(), ints(range(N)), *caches, stream=stream)
+        junk += [torch.full((1 << i,), 5, dtype=torch.int32, device="cuda") for i in range(6, 13)]
+        got = dsp.tree_attention4(q.clone(), *caches, ints([[0, 1, 2]]), ints([0]), ints([0, N]), max_rows=N, stream=stream)
+        junk += [torch.full((1 << i,), 7, dtype=torch.int32, device="cuda") for i in range(6, 13)]
+        torch.cuda.synchronize()
+        return turned["q"], turned["k"], *caches, got["out"], got["lse"]
+
+    assert all(torch.equal(a, b) for a, b in zip(run(None), run(side)))
+
+
 @pytest.mark.parametrize("D,page", [(64, 16), (128, 8)])
 def test_server_with_rotary_positions(D, page):
     """As the server's own test: logits against the target over the whole text (its tolerance, for the same reason)."""
