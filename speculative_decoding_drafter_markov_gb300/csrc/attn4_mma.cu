@@ -40,6 +40,7 @@ namespace {
 constexpr int kStepLog2 = 5, kStep = 1 << kStepLog2;  // tokens of a step
 constexpr int kMmaTileLog2 = 6;                       // of a tile, the least that a warp has of a unit
 constexpr float kLift = 7.f;  // the reference stands below the maximum, as in attn_tc_kernel.cuh
+constexpr int kMmaMostShare = kMostShare >> 4;  // places of a warp's share: its SM's twelve are minutes of work
 constexpr int kMmaUnitCost = 2;  // tiles: a unit's start and end (1 and 2 measured alike, 4 and 8 by 3 to 6 % worse)
 
 // A warp's place in its share: the piece that it works on and the next one, and the walk
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention4_mma(const __gr
     Pieces &mine = *reinterpret_cast<Pieces *>(slots + C::kDepth * C::kSlot + C::kQ);
     const int cta = blockIdx.x * C::NW + warp;  // of as many shares as there are warps
     {
-        const Share share = share_of(p, cta, gridDim.x * C::NW);
+        const Share share = share_of(p, cta, gridDim.x * C::NW, kMmaMostShare);
         if (lane == 0) {
             p.join[cta].pieces = 0;
             new (&mine.walk) Walk<Params>(p, share);

@@ -40,8 +40,8 @@ __device__ __forceinline__ int plain_column(int d) {
 
 // The share of CTA `cta` of `grid` -- or of a warp, where the work is cut among warps --,
 // found by one warp (all its lanes come here and get it): a run of requests per lane, no
-// barrier.
-__device__ inline Share share_of(const Params &p, int cta, int grid) {
+// barrier.  `most`: places of a share, at most kMostShare; more are reported.
+__device__ inline Share share_of(const Params &p, int cta, int grid, int most) {
     const int lane = threadIdx.x & 31, R = p.a.R;
     const int per = (R + 31) / 32, r0 = min(R, lane * per), r1 = min(R, r0 + per);
     long long mine = 0;
@@ -60,7 +60,7 @@ __device__ inline Share share_of(const Params &p, int cta, int grid) {
         if (lane >= d) inc = add_places(inc, y);
     }
     long long total = __shfl_sync(0xffffffffu, inc, 31);
-    if (total > (long long)grid * kMostShare) {
+    if (total > (long long)grid * most) {
         if (lane == 0 && cta == 0) set_err(p.a.err, DSPARK_ERR_UNSUPPORTED);
         total = 0;
     }
@@ -81,7 +81,7 @@ __device__ inline Share share_of(const Params &p, int cta, int grid) {
     return s;
 }
 
-__device__ inline Share share_of(const Params &p) { return share_of(p, blockIdx.x, gridDim.x); }
+__device__ inline Share share_of(const Params &p) { return share_of(p, blockIdx.x, gridDim.x, kMostShare); }
 
 __device__ __forceinline__ void store_out(const Params &p, size_t at, float v) {
     if (p.a.dtype == DSPARK_BF16) static_cast<__nv_bfloat16 *>(p.a.out)[at] = __float2bfloat16_rn(v);

@@ -321,6 +321,58 @@ def test_rows_beyond_the_batch_stay():
     check(s, {k: v[:5] for k, v in out.items()}, err_word())
 
 
+PAGE = 45691136  # 47 of them are the 2^31 - 256 tokens that a table may name
+
+
+def one_long_page():
+    """Caches of one page, keys and values of 0: codes of 8."""
+    pair = [dsp.cache4(1, 1, PAGE, 16) for _ in range(2)]
+    for cache in pair:
+        cache[:, :, :PAGE * 8] = 0x88
+    return pair
+
+
+@pytest.mark.parametrize("R,hint", [(43, 1), (5, 300)])
+def test_tokens_to_the_end_of_32_bits(R, hint):
+    """Caches whose tokens are 47 times the same page, the last one a table may name.  Keys of
+    zero, values of 0 but for a few that hold 63/64 for 1 (7 times the scale 9/64) in each column: sums of
+    whole numbers of 63 2^-6 (of their eighths, times a weight of 2^7: of 1/4) below 2^24 of those, and means.
+    Partials are joined in fp32, eight at most at a time: 8 2^-24."""
+    kc, vc = one_long_page()
+    rng = np.random.default_rng(1)
+    count = [1, 100, 5000, 70000, 200000, 17, 2, 0]
+    rows = {}
+    for d, n in enumerate(count):
+        at = np.unique(np.concatenate([[0] * (n > 0), rng.integers(1, PAGE - 1, 2 * n)])).astype(np.int64)[:n]
+        at[1:][-1:] = PAGE - 1
+        rows[d] = at
+    slots = np.unique(np.concatenate(list(rows.values())))
+    v = np.zeros((len(slots), 1, 16), np.float32)
+    for d, at in rows.items():
+        v[np.searchsorted(slots, at), 0, d] = 1
+    v = torch.from_numpy(v).cuda()
+    dsp.cache_store4(torch.zeros_like(v), v, ints(slots), kc, vc)
+    tokens, err = PAGE * 47, err_word()
+    assert tokens == 0x7fffff00
+    q = torch.ones((R, 1, 16), dtype=torch.bfloat16, device="cuda")
+    got = dsp.tree_attention4(q, kc, vc, torch.zeros((R, 47), dtype=torch.int32, device="cuda"), ints([tokens - 1] * R), ints(list(range(R + 1))),
+                              max_rows=hint, err=err)
+    assert int(err) == 0
+    want = torch.tensor(count + [0] * 8, dtype=torch.float64, device="cuda") * (63 / 64) / PAGE
+    assert ((got["out"].double() - want).abs() <= (2.0 ** -8 + 8 * 2.0 ** -24) * want).all()
+    lse = np.log(float(tokens))
+    assert ((got["lse"].double() - lse).abs() <= 1e-6 * (1 + lse)).all()
+
+
+def test_calls_of_hours_are_refused():
+    """8192 caches of 2^31 - 256 tokens: reported, and no row is written."""
+    R, (kc, vc), err = 8192, one_long_page(), err_word()
+    out = {"out": torch.full((R, 1, 16), 7.0, dtype=torch.bfloat16, device="cuda"), "lse": torch.full((R, 1), 7.0, device="cuda")}
+    dsp.tree_attention4(torch.ones((R, 1, 16), dtype=torch.bfloat16, device="cuda"), kc, vc, torch.zeros((R, 47), dtype=torch.int32, device="cuda"),
+                        ints([PAGE * 47 - 1] * R), ints(list(range(R + 1))), out=out, err=err)
+    assert int(err) == _lib.ERR_UNSUPPORTED and (out["out"] == 7).all() and (out["lse"] == 7).all()
+
+
 def test_same_bits_again():
     for rows in ([5, 2, 1], [33, 2, 1]):
         s = make4([9000, 40, 333], rows, 8, 2, 128, 16, torch.bfloat16, seed=1)
