@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) cache_store4_kernel(const dspark_cac
     int slot[kRows];
     Eight<T> v[kRows];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) slot[i] = in && row0 + i < a.N ? a.slot[row0 + i] : -1;
+    for (int i = 0; i < kRows; ++i) slot[i] = in && (unsigned)row0 + i < (unsigned)a.N ? a.slot[row0 + i] : -1;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         slot[i] = checked_slot(slot[i], slots, a.err);
@@ -145,7 +145,7 @@ cudaError_t store_as(const dspark_cache_store4_args &a, const Page &page, cudaSt
     const int pieces = 2 * a.H * (a.D / 8), y = (pieces + kThreads - 1) / kThreads;
     // four rows a thread where that leaves every SM a few CTAs, else one
     const bool many = (long long)a.N * y >= 4ll * 4 * sm_count();
-    return many ? launch_close(cache_store4_kernel<T, kWide, 4>, dim3((a.N + 3) / 4, y), kThreads, 0, s, a, page)
+    return many ? launch_close(cache_store4_kernel<T, kWide, 4>, dim3((a.N - 1) / 4 + 1, y), kThreads, 0, s, a, page)
                 : launch_close(cache_store4_kernel<T, kWide, 1>, dim3(a.N, y), kThreads, 0, s, a, page);
 }
 

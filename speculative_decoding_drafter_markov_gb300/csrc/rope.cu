@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(32 * kWarps) rope_store_kernel(const __grid_co
     after_predecessor();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = a.rot / 2;
     const long long item = (long long)blockIdx.x * kWarps + warp;
+    if (item >= (long long)a.N * r.splits) return;
     const int i = (int)(item / r.splits), part = (int)(item - (long long)i * r.splits);
-    if (i >= a.N) return;
     // everything that is read at the start is on its way before anything is waited for
     int slot = a.slot ? a.slot[i] : 0;
     const int pos = a.pos[i];
@@ -287,8 +287,8 @@ __global__ void __launch_bounds__(32 * kWarps) rope_store_any(const __grid_const
     after_predecessor();
     const int lane = threadIdx.x & 31;
     const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (item >= (long long)a.N * r.heads) return;
     const int i = (int)(item / r.heads), h = (int)(item - (long long)i * r.heads);
-    if (i >= a.N) return;
     int slot = 0;
     if (a.slot) {
         slot = checked_slot(a.slot[i], slots_of(a.n_pages, a.page), a.err);
