@@ -584,7 +584,14 @@ DSPARK_API int dspark_tree_attention(const dspark_tree_attention_args *a, void *
 /* The same attention over caches in 4 bits (above), k_cache and v_cache [n_pages, H,
  * page * D * 9 / 16] bytes; dtype is that of q and out.  What is said of
  * dspark_tree_attention holds: what a row sees, rows that see nothing, errors, sums in
- * fp32.  On the CUDA cores.  A workspace of its own size. */
+ * fp32, the bits do not depend on timing.  bf16 with D up to 128, pages whose largest
+ * power of two (128 counted at most) is at least 8 and times D a multiple of 256, a
+ * scale that is not negative, Hq / H up to 128, and q (its strides too) and out
+ * 16-byte aligned, runs on the tensor cores: keys are exact in bf16, values in fp16,
+ * and the softmax weights are rounded to fp16 for the second product (2^-11 of a weight,
+ * below the rounding of out); everything else on the CUDA cores in fp32.  max_rows
+ * chooses between kernels and tile shapes, and the workspace's size depends on it: size it
+ * with the max_rows of the call. */
 DSPARK_API size_t dspark_tree_attention4_workspace_size(const dspark_tree_attention_args *a);
 DSPARK_API int dspark_tree_attention4(const dspark_tree_attention_args *a, void *ws, dspark_stream_t stream);
 

@@ -1,5 +1,14 @@
 // rope.cu -- queries, keys and values of the rows on their way into the attention: the
 // norm of each head, the rotation by position, the append to the paged cache.
+//
+// What has to be done is one read and one write of every row; the sines and cosines of a row are
+// shared by its heads, so a warp takes a whole row where there are rows enough.  A run of a
+// server's cycle (64 requests of up to 9 rows, 32 query heads on 8 of 128) takes 4.8 us, a launch
+// and the trips from slot and position to the store, and 24 prompts of up to 8192 rows (418 MB) 81 us,
+// 5.2 TB/s: 0.76 of a plain copy's rate.  There 56 % of the issue slots are used and the DRAM half of
+// its cycles; what is left is waiting for the loads of two heads a thread (stalls: 2.8 of 9 cycles an
+// instruction for memory, 1.7 for fixed latencies), and more heads under way cost registers and with
+// them warps.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
