@@ -51,8 +51,7 @@ __device__ __forceinline__ float whole_of(float x, float s, float inv) {
 // Rounded to a multiple of 2^-14 it is on the right side, whatever the product with 1 / s
 // loses.  It is within -7.44 .. 7.44 unless the scale is the largest there is.
 __device__ __forceinline__ float coded_bf16(float x, float inv) {
-    const float t = __fadd_rn(__fmaf_rn(x, inv, 768.f), -768.f);  // 768 = 1.5 2^9
-    return __fadd_rn(t, 12582920.f);
+    return __fadd_rn(__fmaf_rn(x, inv, 768.f), 12582920.f - 768.f);  // 768 = 1.5 2^9
 }
 constexpr float kMostHeld = 7.f * 57344.f;
 
