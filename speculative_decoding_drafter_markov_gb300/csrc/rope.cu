@@ -3,9 +3,9 @@
 //
 // What has to be done is one read and one write of every row; the sines and cosines of a row are
 // shared by its heads, so a warp takes a whole row where there are rows enough.  A run of a
-// server's cycle (64 requests of up to 9 rows, 32 query heads on 8 of 128) takes 4.8 us, a launch
-// and the trips from slot and position to the store, and 24 prompts of up to 8192 rows (418 MB) 81 us,
-// 5.2 TB/s: 0.76 of a plain copy's rate.  There 56 % of the issue slots are used and the DRAM half of
+// server's cycle (64 requests of up to 9 rows, 32 query heads on 8 of 128) takes 5 us, a launch
+// and the trips from slot and position to the store, and 24 prompts of up to 8192 rows (418 MB) 79 us,
+// 5.3 TB/s: 0.78 of a plain copy's rate.  There 56 % of the issue slots are used and the DRAM half of
 // its cycles; what is left is waiting for the loads of two heads a thread (stalls: 2.8 of 9 cycles an
 // instruction for memory, 1.7 for fixed latencies), and more heads under way cost registers and with
 // them warps.
@@ -132,15 +132,15 @@ struct PieceOf {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
         else return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
     }
-    __device__ __forceinline__ void set(const float (&x)[E]) {
+    __device__ __forceinline__ void set(const float2 (&x)[E / 2]) {
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) w[i] = __float_as_uint(x[i]);
+            for (int i = 0; i < E / 2; ++i) w[2 * i] = __float_as_uint(x[i].x), w[2 * i + 1] = __float_as_uint(x[i].y);
         } else {
 #pragma unroll
-            for (int i = 0; i < E; i += 2) {
-                const __nv_bfloat162 two = __floats2bfloat162_rn(x[i], x[i + 1]);
-                w[i >> 1] = *reinterpret_cast<const unsigned *>(&two);
+            for (int i = 0; i < E / 2; ++i) {
+                const __nv_bfloat162 two = __floats2bfloat162_rn(x[i].x, x[i].y);
+                w[i] = *reinterpret_cast<const unsigned *>(&two);
             }
         }
     }
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(32 * kWarps) rope_store_kernel(const __grid_co
             *v_src = static_cast<const T *>(a.v) + i * a.v_row + at0;
     const int apart = at1 - at0;
     // heads two at a time
-    P x[2][2];
+    P x[2][2] = {};  // (zeros in the threads beyond D: part of their heads' sums)
     auto fetch = [&](int h, P (&y)[2]) {
         if (h >= h1 || !in) return;
         const T *src = h < a.Hq ? q_src + h * a.q_head : h < a.Hq + a.H ? k_src + (h - a.Hq) * a.k_head : v_src + (h - a.Hq - a.H) * a.v_head;
@@ -223,19 +223,20 @@ __global__ void __launch_bounds__(32 * kWarps) rope_store_kernel(const __grid_co
         for (int u = 0; u < 2; ++u) {
             const int hu = h + u * kHeads;
             const bool live = hu < h1 && in;
-            float y[2][E];
+            float2 y[2][E / 2];  // in pairs: half the instructions
 #pragma unroll
             for (int p = 0; p < 2; ++p)
 #pragma unroll
-                for (int k = 0; k < E; ++k) y[p][k] = live ? x[u][p].get(k) : 0.f;
+                for (int k = 0; k < E; k += 2) y[p][k / 2] = make_float2(x[u][p].get(k), x[u][p].get(k + 1));
             const T *weight = static_cast<const T *>(hu < a.Hq ? a.q_weight : hu < a.Hq + a.H ? a.k_weight : nullptr);
             const bool norm = live && weight != nullptr, key = hu < a.Hq + a.H;  // a query or a key
             if (a.q_weight || a.k_weight) {
-                float sum = 0.f;
+                float2 squares = {0.f, 0.f};
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
 #pragma unroll
-                    for (int k = 0; k < E; ++k) sum = fmaf(y[p][k], y[p][k], sum);
+                    for (int k = 0; k < E / 2; ++k) squares = fma2(y[p][k], y[p][k], squares);
+                float sum = squares.x + squares.y;
 #pragma unroll
                 for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                 float f = rsqrtf(fmaf(sum, inv_D, a.eps));
@@ -245,7 +246,10 @@ __global__ void __launch_bounds__(32 * kWarps) rope_store_kernel(const __grid_co
 #pragma unroll
                     for (int p = 0; p < 2; ++p)
 #pragma unroll
-                        for (int k = 0; k < E; ++k) scaled = fmaf(y[p][k] * 0x1p-64f, y[p][k] * 0x1p-64f, scaled);
+                        for (int k = 0; k < E / 2; ++k) {
+                            const float v0 = y[p][k].x * 0x1p-64f, v1 = y[p][k].y * 0x1p-64f;
+                            scaled = fmaf(v1, v1, fmaf(v0, v0, scaled));
+                        }
 #pragma unroll
                     for (int d = 1; d < kLanes; d <<= 1) scaled += __shfl_xor_sync(0xffffffffu, scaled, d);
                     if (!(sum <= 3.4e38f)) f = rsqrtf(fmaf(scaled, inv_D, a.eps * 0x1p-128f)) * 0x1p-64f;
@@ -257,19 +261,25 @@ __global__ void __launch_bounds__(32 * kWarps) rope_store_kernel(const __grid_co
 #pragma unroll
                     for (int p = 0; p < 2; ++p)
 #pragma unroll
-                        for (int k = 0; k < E; ++k) y[p][k] = y[p][k] * f * w[p].get(k);
+                        for (int k = 0; k < E; k += 2) y[p][k / 2] = mul2(mul2(y[p][k / 2], {f, f}), {w[p].get(k), w[p].get(k + 1)});
                 }
             }
             if (live && key) {
                 if (turn) {
 #pragma unroll
-                    for (int k = 0; k < E; ++k) {
-                        // pair k: elements k of both pieces, or neighbours
-                        float &p0 = kNeighbours ? y[2 * k / E][2 * k % E] : y[0][k];
-                        float &p1 = kNeighbours ? y[2 * k / E][2 * k % E + 1] : y[1][k];
-                        const float b0 = p0, b1 = p1;
-                        p0 = fmaf(b0, c[k], -b1 * s[k]);
-                        p1 = fmaf(b1, c[k], b0 * s[k]);
+                    for (int k = 0; k < E; k += 2) {
+                        // pairs k and k + 1: elements of both pieces, or neighbours
+                        const float2 c2 = {c[k], c[k + 1]}, s2 = {s[k], s[k + 1]}, less = {-s[k], -s[k + 1]};
+                        if (kNeighbours) {
+                            float2 &v0 = y[2 * k / E][k % (E / 2)], &v1 = y[2 * (k + 1) / E][(k + 1) % (E / 2)];
+                            const float2 a0 = {v0.x, v1.x}, b0 = {v0.y, v1.y}, p0 = fma2(a0, c2, mul2(b0, less)), p1 = fma2(b0, c2, mul2(a0, s2));
+                            v0 = {p0.x, p1.x};
+                            v1 = {p0.y, p1.y};
+                        } else {
+                            const float2 b0 = y[0][k / 2], b1 = y[1][k / 2];
+                            y[0][k / 2] = fma2(b0, c2, mul2(b1, less));
+                            y[1][k / 2] = fma2(b1, c2, mul2(b0, s2));
+                        }
                     }
                 }
                 if (turn || norm) {
