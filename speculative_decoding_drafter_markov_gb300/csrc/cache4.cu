@@ -1,10 +1,10 @@
 // cache4.cu -- the write of the rows' keys and values into a cache of 4 bits.
 //
-// One read of the rows and a write of 9/32 of it; what bounds it is the arithmetic: a maximum over 16
-// elements, the nearest scale, and per element an exact rounding, two operations in bf16.  24 prompts of
-// up to 8192 rows (8 heads of 128, keys and values, 159 MB moved) take 31 us, 5.2 TB/s, 0.76 of a plain copy's
-// rate, with 79 % of the issue slots used (the integer pipe, for scales, codes and their packing, 55 %); a cycle's rows
-// (64 requests of up to 9) 4.7 us, which the call on the host takes.
+// One read of the rows and a write of 9/32 of it; beside that a maximum over 16 elements, the
+// nearest scale, and per element an exact rounding, two operations in bf16.  24 prompts of
+// up to 8192 rows (8 heads of 128, keys and values, 159 MB moved) take 29 us, 5.5 TB/s, 0.81 of a plain copy's
+// rate, with 70 % of the issue slots used, most stalls for the rows (5.1 of 12 cycles an instruction).  A cycle's rows (64 requests of up
+// to 9) take 4.7 us, which is the call on the host.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -17,12 +17,12 @@ namespace dspark {
 
 namespace {
 
-// A thread has 8 elements of a row -- keys or values, head and columns are found once --
-// and takes them from kRows rows, all reads under way together; its neighbour has the
-// other 8 of the 16 that share a scale.  Reads, codes and the values given back are
-// adjacent among the threads of a warp.  (With the row's number compared as a difference in place of
-// an unsigned sum the prompts took 41 us: the four slots were then read one by one.)
-constexpr int kThreads = 256;
+// A thread has the 16 elements of a row that share a scale -- keys or values, head and columns
+// are found once -- and takes them from kRows rows, all reads under way together.  (8 elements a
+// thread, its neighbour with the other 8, four rows: 30.9 us for the prompts above; 16 and four rows 30.0,
+// two rows 29.0.  With the row's number compared as a difference in place of an unsigned sum 41 against 33 us at
+// that stage: the four slots were then read one by one.)
+constexpr int kThreads = 128;
 
 template <typename T>
 struct Eight;
@@ -86,15 +86,15 @@ struct Eight<float> {
 template <typename T, bool kWide, int kRows>
 __global__ void __launch_bounds__(kThreads) cache_store4_kernel(const dspark_cache_store4_args a, const Page page) {
     after_predecessor();
-    const int per_head = a.D / 8, per_row = a.H * per_head;
+    const int per_head = a.D / 16, per_row = a.H * per_head;
     int piece = blockIdx.y * kThreads + threadIdx.x;
-    const bool in = piece < 2 * per_row;  // (per_row is even: a pair of threads is in or out together)
+    const bool in = piece < 2 * per_row;
     const bool values = piece >= per_row;
     if (values) piece -= per_row;
-    const int h = piece / per_head, e = (piece - h * per_head) * 8;
+    const int h = piece / per_head, e = (piece - h * per_head) * 16;
     const T *src = static_cast<const T *>(values ? a.v : a.k) + (values ? a.v_head : a.k_head) * h + e;
     const long long row = values ? a.v_row : a.k_row;
-    // this thread's codes and, for an even one, scale of the first token of page 0; what a page and a token add
+    // this thread's codes and scale of the first token of page 0; what a page and a token add
     const long long page_bytes = cache4::page_bytes(a.page, a.D), page_step = page_bytes * a.H;
     unsigned char *codes = (values ? a.v_cache : a.k_cache) + page_bytes * h + e / 2;
     unsigned char *scales = codes - e / 2 + cache4::code_bytes(a.page, a.D) + e / 16;
@@ -103,57 +103,61 @@ __global__ void __launch_bounds__(kThreads) cache_store4_kernel(const dspark_cac
     const unsigned slots = slots_of(a.n_pages, a.page);
     const int row0 = blockIdx.x * kRows;
     int slot[kRows];
-    Eight<T> v[kRows];
+    Eight<T> v[kRows][2];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) slot[i] = in && (unsigned)row0 + i < (unsigned)a.N ? a.slot[row0 + i] : -1;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         slot[i] = checked_slot(slot[i], slots, a.err);
         if (slot[i] < 0) continue;
-        if (kWide) v[i].load(src + (row0 + i) * row);
-        else v[i].load_each(src + (row0 + i) * row);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            if (kWide) v[i][p].load(src + (row0 + i) * row + 8 * p);
+            else v[i][p].load_each(src + (row0 + i) * row + 8 * p);
+        }
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-        unsigned most = slot[i] >= 0 ? v[i].most() : 0u;
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
         if (slot[i] < 0) continue;
-        float x[8];
-        v[i].get(x);
-        if (__uint_as_float(most) > cache4::kMostHeld) {  // beyond the largest scale
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = fminf(fmaxf(x[k], -cache4::kMostHeld), cache4::kMostHeld);
-        }
+        const unsigned most = max(v[i][0].most(), v[i][1].most());
+        const bool beyond = __uint_as_float(most) > cache4::kMostHeld;  // the largest scale
         const unsigned byte = cache4::scale_byte(__uint_as_float(most));
         const float s = cache4::scale_of(byte), inv = __fdividef(1.f, s);  // (a last bit or two is nothing to what takes it)
-        unsigned code[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float n = Eight<T>::coded(x[k], s, inv);
-            code[k] = __float_as_uint(n);
-        }
-        // elements 0 4 1 5 in the low halves of the four bytes, 2 6 3 7 in the high ones
-        const unsigned low = __byte_perm(__byte_perm(code[0], code[4], 0x0040), __byte_perm(code[1], code[5], 0x0040), 0x5410);
-        const unsigned high = __byte_perm(__byte_perm(code[2], code[6], 0x0040), __byte_perm(code[3], code[7], 0x0040), 0x5410);
-        const unsigned word = byte == cache4::kNoNumbers ? 0x88888888u : low + 16u * high;
         const unsigned pg = page.of(slot[i]), off = slot[i] - pg * page.size;
         const long long at = pg * page_step;
-        *reinterpret_cast<unsigned *>(codes + at + (unsigned long long)off * code_row) = word;
-        if (e % cache4::kGroup == 0) scales[at + (unsigned long long)off * scale_row] = (unsigned char)byte;
-        if (held) {
+        unsigned word[2];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = byte == cache4::kNoNumbers ? s : (__uint_as_float(code[k]) - 12582920.f) * s;
-            Eight<T>::store(held + (row0 + i) * ((long long)a.H * a.D) + h * a.D + e, x);
+        for (int p = 0; p < 2; ++p) {
+            float x[8];
+            v[i][p].get(x);
+            if (beyond) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = fminf(fmaxf(x[k], -cache4::kMostHeld), cache4::kMostHeld);
+            }
+            unsigned code[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) code[k] = __float_as_uint(Eight<T>::coded(x[k], s, inv));
+            // elements 0 4 1 5 in the low halves of the four bytes, 2 6 3 7 in the high ones
+            const unsigned low = __byte_perm(__byte_perm(code[0], code[4], 0x0040), __byte_perm(code[1], code[5], 0x0040), 0x5410);
+            const unsigned high = __byte_perm(__byte_perm(code[2], code[6], 0x0040), __byte_perm(code[3], code[7], 0x0040), 0x5410);
+            word[p] = byte == cache4::kNoNumbers ? 0x88888888u : low + 16u * high;
+            if (held) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = byte == cache4::kNoNumbers ? s : (__uint_as_float(code[k]) - 12582920.f) * s;
+                Eight<T>::store(held + (row0 + i) * ((long long)a.H * a.D) + h * a.D + e + 8 * p, x);
+            }
         }
+        *reinterpret_cast<uint2 *>(codes + at + (unsigned long long)off * code_row) = make_uint2(word[0], word[1]);
+        scales[at + (unsigned long long)off * scale_row] = (unsigned char)byte;
     }
 }
 
 template <typename T, bool kWide>
 cudaError_t store_as(const dspark_cache_store4_args &a, const Page &page, cudaStream_t s) {
-    const int pieces = 2 * a.H * (a.D / 8), y = (pieces + kThreads - 1) / kThreads;
-    // four rows a thread where that leaves every SM a few CTAs, else one
-    const bool many = (long long)a.N * y >= 4ll * 4 * sm_count();
-    return many ? launch_close(cache_store4_kernel<T, kWide, 4>, dim3((a.N - 1) / 4 + 1, y), kThreads, 0, s, a, page)
+    const int pieces = 2 * a.H * (a.D / 16), y = (pieces + kThreads - 1) / kThreads;
+    // two rows a thread where that leaves every SM a few CTAs, else one
+    const bool many = (long long)a.N * y >= 2ll * 8 * sm_count();
+    return many ? launch_close(cache_store4_kernel<T, kWide, 2>, dim3((a.N - 1) / 2 + 1, y), kThreads, 0, s, a, page)
                 : launch_close(cache_store4_kernel<T, kWide, 1>, dim3(a.N, y), kThreads, 0, s, a, page);
 }
 

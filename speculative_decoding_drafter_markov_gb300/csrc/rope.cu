@@ -5,10 +5,10 @@
 // shared by its heads, so a warp takes a whole row where there are rows enough.  A run of a
 // server's cycle (64 requests of up to 9 rows, 32 query heads on 8 of 128) takes 5 us, a launch
 // and the trips from slot and position to the store, and 24 prompts of up to 8192 rows (418 MB) 79 us,
-// 5.3 TB/s: 0.78 of a plain copy's rate.  There 56 % of the issue slots are used and the DRAM half of
-// its cycles; what is left is waiting for the loads of two heads a thread (stalls: 2.8 of 9 cycles an
-// instruction for memory, 1.7 for fixed latencies), and more heads under way cost registers and with
-// them warps.
+// 5.3 TB/s: 0.78 of a plain copy's rate.  There 47 % of the issue slots are used and the DRAM 58 % of
+// its cycles; what is left is waiting for the loads of two heads a thread (stalls: 3.8 of 10 cycles an
+// instruction for memory, 2.2 for fixed latencies).  Six, seven or eight CTAs an SM by fewer registers took
+// 80, 85 and 93 us, warps that stay and fetch the next row's first heads ahead 82 (at 81 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
