@@ -519,8 +519,9 @@ DSPARK_API int dspark_rope_store(const dspark_rope_store_args *a, dspark_stream_
  * [n_pages, H, page * D * 9 / 16] bytes on a boundary of 16. */
 
 /* Keys and values of the rows into their slots of such caches; slots, strides and the
- * rest as for dspark_cache_store.  k_out and v_out, given both or neither, get the values
- * that the cache then holds, in the type of the rows (skipped rows are not written).
+ * rest as for dspark_cache_store, but that two rows with one slot may leave the codes of one
+ * with scales of the other: slots are to differ.  k_out and v_out, given both or neither, get
+ * the values that the cache then holds, in the type of the rows (skipped rows are not written).
  * One launch, no workspace. */
 typedef struct {
     int32_t N, H, D;          /* rows, key-value heads, head size               */
