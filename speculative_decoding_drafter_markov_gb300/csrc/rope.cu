@@ -46,6 +46,18 @@ __device__ __forceinline__ float2 cos_sin(unsigned long long turns, int pos) {
     return make_float2(c, s);
 }
 
+// ---------------------------------------------------------------- squares beyond fp32
+// Where the sum of squares passes fp32 it is formed of (x 2^-96)^2, 2^64 each at most; some |x| is
+// 2^60 or more, and only elements below 2^-27 of that lose bits.  1 / root is then between
+// 2^-128 and 2^-60, which may be subnormal, so half of 2^-96 goes to x beforehand: x 2^-48 is exact
+// wherever the result is a normal number.
+constexpr float kDown = 0x1p-96f, kHalfDown = 0x1p-48f;
+__device__ __forceinline__ bool beyond_fp32(float sum) { return !(sum <= 3.4e38f); }
+// 2^48 / root of the squares' mean and eps: what x 2^-48 is multiplied with
+__device__ __forceinline__ float factor_beyond(float scaled, float inv_D, float eps) {
+    return rsqrtf(fmaf(scaled, inv_D, eps * kDown * kDown)) * kHalfDown;
+}
+
 template <typename T>
 __device__ __forceinline__ T round_to(float v);
 template <>
@@ -240,19 +252,24 @@ __global__ void __launch_bounds__(32 * kWarps) rope_store_kernel(const __grid_co
 #pragma unroll
                 for (int d = 1; d < kLanes; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                 float f = rsqrtf(fmaf(sum, inv_D, a.eps));
-                if (__any_sync(0xffffffffu, !(sum <= 3.4e38f))) {
-                    // beyond fp32: the sum of (x 2^-64)^2
+                if (__any_sync(0xffffffffu, beyond_fp32(sum))) {
                     float scaled = 0.f;
 #pragma unroll
                     for (int p = 0; p < 2; ++p)
 #pragma unroll
                         for (int k = 0; k < E / 2; ++k) {
-                            const float v0 = y[p][k].x * 0x1p-64f, v1 = y[p][k].y * 0x1p-64f;
+                            const float v0 = y[p][k].x * kDown, v1 = y[p][k].y * kDown;
                             scaled = fmaf(v1, v1, fmaf(v0, v0, scaled));
                         }
 #pragma unroll
                     for (int d = 1; d < kLanes; d <<= 1) scaled += __shfl_xor_sync(0xffffffffu, scaled, d);
-                    if (!(sum <= 3.4e38f)) f = rsqrtf(fmaf(scaled, inv_D, a.eps * 0x1p-128f)) * 0x1p-64f;
+                    if (norm && beyond_fp32(sum)) {
+                        f = factor_beyond(scaled, inv_D, a.eps);
+#pragma unroll
+                        for (int p = 0; p < 2; ++p)
+#pragma unroll
+                            for (int k = 0; k < E / 2; ++k) y[p][k] = mul2(y[p][k], {kHalfDown, kHalfDown});
+                    }
                 }
                 if (norm) {
                     P w[2];
@@ -316,11 +333,11 @@ __global__ void __launch_bounds__(32 * kWarps) rope_store_any(const __grid_const
     const Head to = r.head<T>(h, i, slot);
     const T *src = static_cast<const T *>(to.src), *weight = static_cast<const T *>(to.weight);
     T *dst = static_cast<T *>(to.dst);
-    float f = 1.f;
+    float f = 1.f, down = 1.f;
     if (weight) {
         float sum = 0.f, scaled = 0.f;
         for (int d = lane; d < a.D; d += 32) {
-            const float v = to_f32(src[d]), w = v * 0x1p-64f;
+            const float v = to_f32(src[d]), w = v * kDown;
             sum = fmaf(v, v, sum);
             scaled = fmaf(w, w, scaled);
         }
@@ -330,7 +347,11 @@ __global__ void __launch_bounds__(32 * kWarps) rope_store_any(const __grid_const
             scaled += __shfl_xor_sync(0xffffffffu, scaled, d);
         }
         const float inv_D = 1.f / (float)a.D;
-        f = sum <= 3.4e38f ? rsqrtf(fmaf(sum, inv_D, a.eps)) : rsqrtf(fmaf(scaled, inv_D, a.eps * 0x1p-128f)) * 0x1p-64f;
+        f = rsqrtf(fmaf(sum, inv_D, a.eps));
+        if (beyond_fp32(sum)) {
+            f = factor_beyond(scaled, inv_D, a.eps);
+            down = kHalfDown;
+        }
     }
     const int half = a.rot / 2, pos = a.pos[i];
     for (int j = lane; j < (a.D + 1) / 2; j += 32) {
@@ -341,8 +362,8 @@ __global__ void __launch_bounds__(32 * kWarps) rope_store_any(const __grid_const
         if (to.turn && (turn || weight)) {
             float b0 = to_f32(v0), b1 = to_f32(v1);
             if (weight) {
-                b0 = b0 * f * to_f32(weight[d0]);
-                if (two) b1 = b1 * f * to_f32(weight[d1]);
+                b0 = b0 * down * f * to_f32(weight[d0]);
+                if (two) b1 = b1 * down * f * to_f32(weight[d1]);
             }
             if (turn) {
                 const float2 cs = cos_sin(turns_of(a.freq[j]), pos);
