@@ -589,10 +589,12 @@ DSPARK_API int dspark_tree_attention(const dspark_tree_attention_args *a, void *
  * power of two (128 counted at most) is at least 8 and times D a multiple of 256, a
  * scale that is not negative, Hq / H up to 128, and q (its strides too) and out
  * 16-byte aligned, runs on the tensor cores: keys are exact in bf16, values in fp16,
- * and the softmax weights are rounded to fp16 for the second product (2^-11 of a weight,
- * below the rounding of out); everything else on the CUDA cores in fp32.  max_rows
- * chooses between kernels and tile shapes, and the workspace's size depends on it: size it
- * with the max_rows of the call. */
+ * and the softmax weights are rounded to fp16 for the second product: by 2^-11 of a weight
+ * that is 2^-21 of its row's largest or more, by 2^-32 of the largest below that.  (The
+ * second part adds up to 2^-32 n max |v| at most over n tokens that are all so small: less than
+ * the rounding of an output of that size up to 2^23 tokens.)  Everything else on
+ * the CUDA cores in fp32.  max_rows chooses between kernels and tile shapes, and the
+ * workspace's size depends on it: size it with the max_rows of the call. */
 DSPARK_API size_t dspark_tree_attention4_workspace_size(const dspark_tree_attention_args *a);
 DSPARK_API int dspark_tree_attention4(const dspark_tree_attention_args *a, void *ws, dspark_stream_t stream);
 

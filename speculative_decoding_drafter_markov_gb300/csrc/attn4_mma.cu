@@ -18,7 +18,10 @@
 // Per 16 tokens:
 //     S^T = K Q^T        K in bf16 (exactly), contracted over D in an order of its own:
 //                        lane j of four has columns j D/4 .. of a token, 16 adjacent bytes
-//     P = 2^(S scale log2(e) - m), rounded to fp16; m moves when a weight would pass 2^15
+//     P = 2^(S scale log2(e) - m), rounded to fp16; m moves when a weight would pass 2^15, to 7
+//                        below the maximum, so that a weight loses 2^-11 of it, or 2^-32 of the largest
+//                        where it is below 2^-21 of that (bf16 would lose 2^-8; the sum is of the
+//                        weights before they are rounded)
 //     O^T += V^T P^T     V in fp16 as eighths (exactly); lane r of eight has the D / 8 columns
 //                        from r D/8 on, two of them rows r and r + 8 of each product
 // The 16 rows of a product are tokens in the order 0 4 1 5 2 6 3 7, 8 12 .., so that the tokens

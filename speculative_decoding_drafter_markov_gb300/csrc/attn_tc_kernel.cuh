@@ -55,8 +55,9 @@ struct Shape {
     static constexpr int kOffPiece = kOffMl + 2 * 128 * 8;    // Piece [kQueue], 64 bytes each
     static constexpr int kOffBar = kOffPiece + 64 * kQueue;
     static constexpr int kBars = 2 * NS + 4 * NP + 13 + 2 * kQueue;
-    // The reference that a weight is relative to stands kLift below the maximum: a weight of fp16 then
-    // keeps ones down to 2^-31 of the largest, and none passes 2^15.
+    // The reference that a weight is relative to stands kLift below the maximum: a weight of fp16 is then
+    // off by 2^-11 of it, or by 2^-32 of the largest where it is below 2^-21 of that (and zero below
+    // 2^-32), and none passes 2^15.  (bf16 would lose 2^-8; the sum is of the weights before they are rounded.)
     static constexpr float kLift = FOUR ? 7.f : 0.f;
     static constexpr int kOffBad = kOffBar + 8 * kBars;     // uint32 [3][8]
     static constexpr int kOffMisc = kOffBad + 96;           // tmem slot, abort flag
