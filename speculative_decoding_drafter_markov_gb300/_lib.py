@@ -567,7 +567,9 @@ def rope_store(q, k, v, pos, freq, *, q_weight=None, k_weight=None, eps=1e-6, in
     or with `interleaved` of neighbours, and with slot [N] int32 the append of k and v
     to the caches [n_pages, H, page, D], in one pass (include/dspark.h).  Views of a
     fused projection are fine; q or k may be None.  Returns {"q"} and, without slot, {"k"}
-    of the rows' shapes; an `out` passed in may hold q and k themselves, or views."""
+    of the rows' shapes; an `out` passed in may hold q and k themselves, or views.  Rows whose
+    slot is negative (page_map's rows beyond the batch) or beyond the cache are left out: their "q" is
+    not written, so without `out` it is what the memory held before."""
     if stream is not None:
         return _on_stream(stream, rope_store, q, k, v, pos, freq, q_weight=q_weight, k_weight=k_weight, eps=eps,
                           interleaved=interleaved, slot=slot, k_cache=k_cache, v_cache=v_cache, out=out, err=err)
@@ -586,7 +588,8 @@ def cache4(n_pages, H, page, D, *, device="cuda"):
 def cache_store4(k, v, slot, k_cache, v_cache, *, values=False, out=None, err=None, stream=None):
     """Write the rows' keys and values k, v [N, H, D] into the slots slot [N] int32 of
     caches in 4 bits (from cache4).  With `values`, or with `out`, returns {"k", "v"}: what
-    the cache then holds of the rows, in their type."""
+    the cache then holds of the rows, in their type; rows whose slot is negative or beyond the cache
+    are not written there either (without `out` they are what the memory held before)."""
     if stream is not None:
         return _on_stream(stream, cache_store4, k, v, slot, k_cache, v_cache, values=values, out=out, err=err)
     return (_bind or _target()).cache_store4(k, v, slot, k_cache, v_cache, values, out, err)
