@@ -391,12 +391,19 @@ void carve(Params &p, void *ws, int grid) {
 
 // A cache in 4 bits: whether a request's lines, as far as the host knows, are few enough for
 // the warps' own products, in units of 16 lines at most, each of which unpacks the cache
-// for itself.  64 caches of up to 8192 tokens, 4 lines a row: up to 5 rows 121 us, against 193 on
-// tcgen05, 9 rows 141 and 191, 12 rows 192 and 202, 16 rows 229 and 220, 24 rows 289 and 199;
-// 8 caches of up to 131072 tokens: 9 rows 339 and 330, 17 rows 590 and 460.
+// for itself.  Both kernels on the same calls, by events around a call (6 us above back-to-back
+// times), 8 heads of 128, the warps' products first, tcgen05 second:
+//     64 caches of up to 8192 tokens, groups of 4, up to 5 rows 115 and 182 us, 9 rows 135 and 183,
+//     12 rows 186 and 198, 13 rows 187 and 210, 16 rows 224 and 213, 24 rows 282 and 193;
+//     48 lines in groups of 1, 2, 3, 8: 182 and 204, 178 and 187, 199 and 212, 165 and 184;
+//     64 lines in groups of 1, 2, 8: 204 and 179, 195 and 182, 198 and 183;
+//     groups of 7, 42 and 56 lines: 162 and 183, 197 and 182.
+// The lines alone are not all of it: tcgen05 is ahead from 36 lines on over few and long caches
+// (8 of up to 131072, groups of 4: 20 lines 188 and 230, 36 lines 336 and 324, 48 lines 331 and 264)
+// and with large groups (32 caches, 48 lines in groups of 16 and 48: 100 and 97, 110 and 89).
 static bool few_lines(const dspark_tree_attention_args &a) { return (long long)a.max_rows * (a.Hq / a.H) <= 48; }
 
-// a unit's lines.  (Units of 32 took 162 us where ones of 16 take 140.)
+// a unit's lines.  (Units of 32 took 162 us where ones of 16 took 140 at that stage.)
 static int mma_lines(const dspark_tree_attention_args &a) { return a.max_rows * (a.Hq / a.H) <= 8 ? 8 : 16; }
 
 cudaError_t launch_join(const Params &p, int grid, cudaStream_t s, bool warps) {

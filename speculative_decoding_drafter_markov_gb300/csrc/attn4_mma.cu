@@ -28,12 +28,14 @@
 // whose values four lanes read are adjacent, and both reads are free of bank conflicts.  P^T
 // comes from S^T's fragments by an 8 x 8 transposition in the warp.
 //
-// 128 caches of up to 16384 tokens, a row of 8 query heads on each of 8 (911 MB): 248 us, 3.7 TB/s, 0.54 of a plain copy's rate;
-// 64 caches of up to 8192, 9 rows: 128 us.  56 % of the issue slots are used (twelve warps an SM, three for a
-// scheduler), 44 % of the integer pipe, 26 % of the fp16 one, 17 % of the matrix pipe.
-// What bounds it are the instructions that unpack: per two elements a mask with an
-// exponent (half rate), 3/4 of a shift for keys, 1/4 and as many byte permutations for values, and
-// one (keys) or two (values) fp16 operations, all of half the rate of fp32; 32 NT matrix products of 8 clocks.
+// 128 caches of up to 16384 tokens, a row of 8 query heads on each of 8 (911 MB): 247 us, 3.7 TB/s, 0.54 of a plain copy's rate;
+// 64 caches of up to 8192, up to 9 rows of 4 query heads: 128 us.  56 % of the issue slots are used (twelve warps an SM, three for a
+// scheduler; counters of half of the tokens), 44 % of the integer pipe, 26 % of the fp16 one, 17 % of the matrix pipe: no
+// pipe is full.  A warp's own chain bounds it -- keys, S, vote, weights, transposition, values -- and three warps do not
+// fill its waits.  Most of its instructions unpack: per two elements a mask with an exponent, 3/4 of a shift for
+// keys, 1/4 and as many byte permutations for values, and one (keys) or two (values) fp16 operations,
+// all of half the rate of fp32; 32 NT matrix products of 8 clocks.  MmaShape<128, 2, true> spills 12 bytes a thread at
+// 168 registers.  Head sizes between 64 and 128 run as 128 with columns of zeros: D = 80 and 96 take as long as 128 does.
 #include <new>
 
 #include "attn_tc_kernel.cuh"

@@ -5,11 +5,13 @@
 // others unpack them into the ring that the MMAs read (unpack_tiles), keys and values apart.
 // Scores are products of bf16 numbers, weights and values of fp16 ones.
 //
-// 8 caches of up to 131072 tokens, 17 rows of 4 query heads (810 MB, 79 GFLOP): 446 us, as long as over 16-bit
+// 8 caches of up to 131072 tokens, up to 17 rows of 4 query heads (810 MB, 79 GFLOP): 446 us, as long as over 16-bit
 // caches (419) of 3.6 times the bytes; 16 trees of up to 64 rows over up to 16384 tokens: 140 us (97).
 // What bounds it is the chain of a tile: keys unpacked and visible to the tensor cores (700 clocks of work and
 // 1300 until the fence has passed), S, its softmax (3200 clocks for 128 x 128 with the other roles beside it), the
-// second product.  The tensor pipe works for 38 % of the time, half of the issue slots are used, by waits too.
+// second product.  Over a quarter of the first case's tokens the tensor pipe works for 38 % of the time and half of the
+// issue slots are used, by waits too.  Every shape spills: 40 to 44 bytes of stores and 48 to 76 of loads a thread at 128
+// registers (one operand) or 96 (two).  Head sizes between 64 and 128 run as 128.
 #include "attn_tc_kernel.cuh"
 
 namespace dspark {

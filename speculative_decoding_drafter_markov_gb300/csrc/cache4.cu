@@ -3,8 +3,9 @@
 // One read of the rows and a write of 9/32 of it; beside that a maximum over 16 elements, the
 // nearest scale, and per element an exact rounding, two operations in bf16.  24 prompts of
 // up to 8192 rows (8 heads of 128, keys and values, 159 MB moved) take 29 us, 5.5 TB/s, 0.81 of a plain copy's
-// rate, with 70 % of the issue slots used, most stalls for the rows (5.1 of 12 cycles an instruction).  A cycle's rows (64 requests of up
-// to 9) take 4.7 us, which is the call on the host.
+// rate, with 70 % of the issue slots used, most stalls for the rows (5.1 of 12 cycles an instruction).  That is with the values that the
+// cache then holds written back; by events around a call (4 us more) 33 us with them and 23 without (89 MB: instructions bound that
+// call), in fp32 58 and 46.  A cycle's rows (64 requests of up to 9) take 4.7 us, which is the call on the host.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -8,7 +8,9 @@
 // 5.3 TB/s: 0.78 of a plain copy's rate.  There 47 % of the issue slots are used and the DRAM 58 % of
 // its cycles; what is left is waiting for the loads of two heads a thread (stalls: 3.8 of 10 cycles an
 // instruction for memory, 2.2 for fixed latencies).  Six, seven or eight CTAs an SM by fewer registers took
-// 80, 85 and 93 us, warps that stay and fetch the next row's first heads ahead 82 (at 81 us).
+// 80, 85 and 93 us, warps that stay and fetch the next row's first heads ahead 82 (at 81 us).  Lanes
+// beyond a head's pieces carry nothing: with heads of 80 or 96 (8 lanes, 5 or 6 in use) the same rows take
+// 79 and 81 us by events around a call, where heads of 128 take 85.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
