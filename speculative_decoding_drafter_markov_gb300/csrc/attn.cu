@@ -262,98 +262,98 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 8) tree_attention_join(const 
         todo = __ballot_sync(0xffffffffu, (threadIdx.x & 31) < kShares && mine < shares && p.join[mine].pieces != 0);
     }
     for (; todo; todo &= todo - 1) {
-    const int share = blockIdx.x * kShares + (kShares > 1 ? __ffs(todo) - 1 : 0);
-    const Join n = p.join[share];
-    if (n.pieces == 0) return;
-    if (kShares > 1) __syncthreads();  // sum_o of the share before was read
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.stride;
-    // rounds of kAhead partials, and one for the weights, either way
-    const int y = gridDim.y, turns = (n.lines + y - 1) / y, turns_warp = (n.lines + y * kJoinWarps - 1) / (y * kJoinWarps);
-    const bool many = turns * ((n.pieces + kAhead * kJoinWarps - 1) / (kAhead * kJoinWarps) + 1) <
-                      turns_warp * ((n.pieces + kAhead - 1) / kAhead + 1);
-    // partial i: the first one, then the first partials of the CTAs after it
-    auto slot = [&](int i, int ln) { return (size_t)(i == 0 ? n.first : 2 * (share + i)) * p.lines + ln; };
-    const int step = many ? kJoinWarps : 1;  // pieces of this warp: own, own + step, ..
-    const int own = many ? warp : 0;
-    for (int ln = many ? blockIdx.y : blockIdx.y * kJoinWarps + warp; ln < n.lines; ln += many ? gridDim.y : gridDim.y * kJoinWarps) {
-        const int jj = ln / p.heads, g = ln - jj * p.heads;
-        if (g >= n.heads) continue;
-        float2 ml = lane < n.pieces ? p.part_ml[slot(lane, ln)] : make_float2(-INFINITY, 0.f);
-        Cells<E> next[kAhead][kCols];
-        auto fetch = [&](int i0) {
+        const int share = blockIdx.x * kShares + (kShares > 1 ? __ffs(todo) - 1 : 0);
+        const Join n = p.join[share];
+        if (n.pieces == 0) return;
+        if (kShares > 1) __syncthreads();  // sum_o of the share before was read
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.stride;
+        // rounds of kAhead partials, and one for the weights, either way
+        const int y = gridDim.y, turns = (n.lines + y - 1) / y, turns_warp = (n.lines + y * kJoinWarps - 1) / (y * kJoinWarps);
+        const bool many = turns * ((n.pieces + kAhead * kJoinWarps - 1) / (kAhead * kJoinWarps) + 1) <
+                          turns_warp * ((n.pieces + kAhead - 1) / kAhead + 1);
+        // partial i: the first one, then the first partials of the CTAs after it
+        auto slot = [&](int i, int ln) { return (size_t)(i == 0 ? n.first : 2 * (share + i)) * p.lines + ln; };
+        const int step = many ? kJoinWarps : 1;  // pieces of this warp: own, own + step, ..
+        const int own = many ? warp : 0;
+        for (int ln = many ? blockIdx.y : blockIdx.y * kJoinWarps + warp; ln < n.lines; ln += many ? gridDim.y : gridDim.y * kJoinWarps) {
+            const int jj = ln / p.heads, g = ln - jj * p.heads;
+            if (g >= n.heads) continue;
+            float2 ml = lane < n.pieces ? p.part_ml[slot(lane, ln)] : make_float2(-INFINITY, 0.f);
+            Cells<E> next[kAhead][kCols];
+            auto fetch = [&](int i0) {
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int i = i0 + u * step;
-                const float *from = p.part_o + slot(i, ln) * D;
+                for (int u = 0; u < kAhead; ++u) {
+                    const int i = i0 + u * step;
+                    const float *from = p.part_o + slot(i, ln) * D;
 #pragma unroll
-                for (int c = 0; c < kCols; ++c)
-                    if (i < n.pieces && E * (lane + 32 * c) < D) next[u][c].load(from + E * (lane + 32 * c));
-            }
-        };
-        fetch(own);
-        float M = ml.x;
-        for (int i = 32 + lane; i < n.pieces; i += 32) M = fmaxf(M, p.part_ml[slot(i, ln)].x);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-        const float ref = M == -INFINITY ? 0.f : M;
-        float o[kCols][E], w = ex2(ml.x - ref), L = w * ml.y;
-        for (int i = 32 + lane; i < n.pieces; i += 32) {
-            const float2 x = p.part_ml[slot(i, ln)];
-            L = fmaf(ex2(x.x - ref), x.y, L);
-        }
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
-#pragma unroll
-        for (int c = 0; c < kCols; ++c)
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[c][e] = 0.f;
-        int chunk = 0;  // w is the weight of piece chunk + lane
-        for (int i0 = own; i0 < n.pieces; i0 += kAhead * step) {
-            if (i0 != own) fetch(i0);
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int i = i0 + u * step;
-                if (i >= n.pieces) break;
-                if (i >= chunk + 32) {
-                    chunk = i & ~31;
-                    w = chunk + lane < n.pieces ? ex2(p.part_ml[slot(chunk + lane, ln)].x - ref) : 0.f;
+                    for (int c = 0; c < kCols; ++c)
+                        if (i < n.pieces && E * (lane + 32 * c) < D) next[u][c].load(from + E * (lane + 32 * c));
                 }
-                const float wi = __shfl_sync(0xffffffffu, w, i - chunk);
+            };
+            fetch(own);
+            float M = ml.x;
+            for (int i = 32 + lane; i < n.pieces; i += 32) M = fmaxf(M, p.part_ml[slot(i, ln)].x);
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+            const float ref = M == -INFINITY ? 0.f : M;
+            float o[kCols][E], w = ex2(ml.x - ref), L = w * ml.y;
+            for (int i = 32 + lane; i < n.pieces; i += 32) {
+                const float2 x = p.part_ml[slot(i, ln)];
+                L = fmaf(ex2(x.x - ref), x.y, L);
+            }
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[c][e] = 0.f;
+            int chunk = 0;  // w is the weight of piece chunk + lane
+            for (int i0 = own; i0 < n.pieces; i0 += kAhead * step) {
+                if (i0 != own) fetch(i0);
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int i = i0 + u * step;
+                    if (i >= n.pieces) break;
+                    if (i >= chunk + 32) {
+                        chunk = i & ~31;
+                        w = chunk + lane < n.pieces ? ex2(p.part_ml[slot(chunk + lane, ln)].x - ref) : 0.f;
+                    }
+                    const float wi = __shfl_sync(0xffffffffu, w, i - chunk);
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c)
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            if (E * (lane + 32 * c) < D) o[c][e] = fmaf(wi, next[u][c].v[e], o[c][e]);
+                }
+            }
+            if (many) {
+                __syncthreads();
+                if (warp > 0) {
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c)
+#pragma unroll
+                        for (int e = 0; e < E; ++e) sum_o[warp - 1][E * (lane + 32 * c) + e] = o[c][e];
+                }
+                __syncthreads();
+                if (warp > 0) continue;
 #pragma unroll
                 for (int c = 0; c < kCols; ++c)
 #pragma unroll
                     for (int e = 0; e < E; ++e)
-                        if (E * (lane + 32 * c) < D) o[c][e] = fmaf(wi, next[u][c].v[e], o[c][e]);
-            }
-        }
-        if (many) {
-            __syncthreads();
-            if (warp > 0) {
 #pragma unroll
-                for (int c = 0; c < kCols; ++c)
-#pragma unroll
-                    for (int e = 0; e < E; ++e) sum_o[warp - 1][E * (lane + 32 * c) + e] = o[c][e];
+                        for (int x = 0; x < kJoinWarps - 1; ++x) o[c][e] += sum_o[x][E * (lane + 32 * c) + e];
             }
-            __syncthreads();
-            if (warp > 0) continue;
+            const size_t at = (size_t)(n.row + jj) * p.a.Hq + n.head + g;
+            const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
             for (int c = 0; c < kCols; ++c)
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-#pragma unroll
-                    for (int x = 0; x < kJoinWarps - 1; ++x) o[c][e] += sum_o[x][E * (lane + 32 * c) + e];
+                for (int e = 0; e < E; ++e) {
+                    const int place = E * (lane + 32 * c) + e, d = p.mixed ? plain_column(place) : place;
+                    if (place < D && d < p.a.D) store_out(p, at * p.a.D + d, o[c][e] * inv);
+                }
+            if (p.a.lse && lane == 0) p.a.lse[at] = lse_of(M, L);
         }
-        const size_t at = (size_t)(n.row + jj) * p.a.Hq + n.head + g;
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-        for (int c = 0; c < kCols; ++c)
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int place = E * (lane + 32 * c) + e, d = p.mixed ? plain_column(place) : place;
-                if (place < D && d < p.a.D) store_out(p, at * p.a.D + d, o[c][e] * inv);
-            }
-        if (p.a.lse && lane == 0) p.a.lse[at] = lse_of(M, L);
-    }
     }
 }
 

@@ -254,210 +254,210 @@ __global__ void __launch_bounds__(C::kThreads, 1) tree_attention4_mma(const __gr
             // 16 tokens at a time (in a loop that is not unrolled 5 % slower, all 32 tokens in one go 4 %)
 #pragma unroll
             for (int t = 0; t < 2; ++t, tok0 += 16, kcode += 16 * code_row, vcode += 16 * code_row, kscale += 16 * scale_row, vscale += 16 * scale_row) {
-            // ------------------------------------------------ S^T = K Q^T
-            float S[NT][4];
+                // ------------------------------------------------ S^T = K Q^T
+                float S[NT][4];
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+                for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) S[i][e] = 0.f;
-            {
-                uint32_t kw[2][KS / 2], ks[2][KS / 4], koff[2][KS / 4];
-                uint32_t bytes[2][KS / 4], most = 0;
+                    for (int e = 0; e < 4; ++e) S[i][e] = 0.f;
+                {
+                    uint32_t kw[2][KS / 2], ks[2][KS / 4], koff[2][KS / 4];
+                    uint32_t bytes[2][KS / 4], most = 0;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int tok = 8 * u + token_r;
-                    const unsigned char *at = kcode + tok * code_row + j * (DP / 8), *sc = kscale + tok * scale_row + j * (DP / 64);
-                    if (C::FULL && DP == 128) {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(at);
-                        kw[u][0] = w.x, kw[u][1] = w.y, kw[u][KS / 2 - 2] = w.z, kw[u][KS / 2 - 1] = w.w;
-                    } else {
+                    for (int u = 0; u < 2; ++u) {
+                        const int tok = 8 * u + token_r;
+                        const unsigned char *at = kcode + tok * code_row + j * (DP / 8), *sc = kscale + tok * scale_row + j * (DP / 64);
+                        if (C::FULL && DP == 128) {
+                            const uint4 w = *reinterpret_cast<const uint4 *>(at);
+                            kw[u][0] = w.x, kw[u][1] = w.y, kw[u][KS / 2 - 2] = w.z, kw[u][KS / 2 - 1] = w.w;
+                        } else {
+#pragma unroll
+                            for (int g = 0; g < KS / 4; ++g) {
+                                uint2 w = make_uint2(0u, 0u);
+                                if (C::FULL || j * (DP / 4) + 16 * g < D) w = *reinterpret_cast<const uint2 *>(at + 8 * g);
+                                kw[u][2 * g] = w.x, kw[u][2 * g + 1] = w.y;
+                            }
+                        }
 #pragma unroll
                         for (int g = 0; g < KS / 4; ++g) {
-                            uint2 w = make_uint2(0u, 0u);
-                            if (C::FULL || j * (DP / 4) + 16 * g < D) w = *reinterpret_cast<const uint2 *>(at + 8 * g);
-                            kw[u][2 * g] = w.x, kw[u][2 * g + 1] = w.y;
+                            const bool in = C::FULL || j * (DP / 4) + 16 * g < D;
+                            bytes[u][g] = in ? sc[g] : 0u;
+                            most = max(most, bytes[u][g]);
+                            ks[u][g] = cache4::bf16_scales(bytes[u][g]);
                         }
                     }
+                    if (most == cache4::kNoNumbers) {
 #pragma unroll
-                    for (int g = 0; g < KS / 4; ++g) {
-                        const bool in = C::FULL || j * (DP / 4) + 16 * g < D;
-                        bytes[u][g] = in ? sc[g] : 0u;
-                        most = max(most, bytes[u][g]);
-                        ks[u][g] = cache4::bf16_scales(bytes[u][g]);
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int g = 0; g < KS / 4; ++g)
+                                if (bytes[u][g] == cache4::kNoNumbers) ks[u][g] = 0x7fc07fc0u;
                     }
-                }
-                if (most == cache4::kNoNumbers) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
                         for (int g = 0; g < KS / 4; ++g)
-                            if (bytes[u][g] == cache4::kNoNumbers) ks[u][g] = 0x7fc07fc0u;
-                }
+                            koff[u][g] = cache4::bf16_offset(ks[u][g]);
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                    for (int k = 0; k < KS; ++k) {
+                        const int w = k >> 1, p0 = 2 * (k & 1), g = k >> 2;
+                        const uint32_t ka[4] = {cache4::bf16_of(kw[0][w], p0, ks[0][g], koff[0][g]), cache4::bf16_of(kw[1][w], p0, ks[1][g], koff[1][g]),
+                                                cache4::bf16_of(kw[0][w], p0 + 1, ks[0][g], koff[0][g]), cache4::bf16_of(kw[1][w], p0 + 1, ks[1][g], koff[1][g])};
+                        if (NT == 1) {
+                            mma_bf16(S[0], ka, q_held[NT == 1 ? k : 0]);
+                        } else {
 #pragma unroll
-                    for (int g = 0; g < KS / 4; ++g)
-                        koff[u][g] = cache4::bf16_offset(ks[u][g]);
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    const int w = k >> 1, p0 = 2 * (k & 1), g = k >> 2;
-                    const uint32_t ka[4] = {cache4::bf16_of(kw[0][w], p0, ks[0][g], koff[0][g]), cache4::bf16_of(kw[1][w], p0, ks[1][g], koff[1][g]),
-                                            cache4::bf16_of(kw[0][w], p0 + 1, ks[0][g], koff[0][g]), cache4::bf16_of(kw[1][w], p0 + 1, ks[1][g], koff[1][g])};
-                    if (NT == 1) {
-                        mma_bf16(S[0], ka, q_held[NT == 1 ? k : 0]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < NT; i += 2) {
-                            const uint4 two = *reinterpret_cast<const uint4 *>(q + (k * 32 + lane) * NT + i);
-                            mma_bf16(S[i], ka, make_uint2(two.x, two.y));
-                            mma_bf16(S[NT == 1 ? 0 : i + 1], ka, make_uint2(two.z, two.w));
+                            for (int i = 0; i < NT; i += 2) {
+                                const uint4 two = *reinterpret_cast<const uint4 *>(q + (k * 32 + lane) * NT + i);
+                                mma_bf16(S[i], ka, make_uint2(two.x, two.y));
+                                mma_bf16(S[NT == 1 ? 0 : i + 1], ka, make_uint2(two.z, two.w));
+                            }
                         }
                     }
                 }
-            }
-            // ------------------------------------------------ the values' words, and the slot is free
-            uint32_t vw[4][ND / 8], vs[4], v_most = 0;
-            {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int tok = 4 * e + j;
-                    const bool in = C::FULL || r * ND < D;
-                    const unsigned char *at = vcode + tok * code_row + r * (ND / 2);
-                    if (DP == 128) {
-                        uint2 w = make_uint2(0u, 0u);
-                        if (in) w = *reinterpret_cast<const uint2 *>(at);
-                        vw[e][0] = w.x, vw[e][ND / 8 - 1] = w.y;
-                    } else {
-                        vw[e][0] = in ? *reinterpret_cast<const uint32_t *>(at) : 0u;
-                    }
-                    vs[e] = in ? vscale[tok * scale_row + r * ND / 16] : 0u;
-                    v_most = max(v_most, vs[e]);
-                }
-            }
-            uint32_t no_numbers = 0u;  // tokens of this step whose scale of columns r ND .. is NaN for those who see them
-            if (tail) {
-                // what some lines do not see must not reach them as 0 x NaN: it counts as zeros here, and
-                // the lines that do see it are told below
-#pragma unroll 1
-                for (int i = 0; i < 16; ++i) {
-                    const int rel = tok0 + i - x.len;
-                    if (rel < base_rel || tok0 + i >= x.tokens || r * ND >= D) continue;
-                    if (vscale[i * scale_row + r * ND / 16] == cache4::kNoNumbers) no_numbers |= 1u << i;
-                }
-            }
-            if (t) {
-                __syncwarp();
-                ++cp.used;
-                if (cp.any()) copy();
-            }
-            // ------------------------------------------------ the weights
-            uint32_t see[NT][2];
-            if (tail) {
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int line = 8 * i + 2 * j + u, jj = line / p.heads, row = x.first + jj;
-                        see[i][u] = 0;
-                        if (jj < x.n) {
-                            const uint32_t *words = a.mask ? reinterpret_cast<const uint32_t *>(a.mask + (size_t)(x.row0 + row) * a.W) : nullptr;
-                            see[i][u] = seen_bits(words, 2 * a.W, tok0 - x.len, x.rows, row);
-                        }
-                    }
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (!((see[i][e & 1] >> (8 * (e >> 1) + token_r)) & 1u)) S[i][e] = -INFINITY;
-            }
-            float2 top[NT];
-            bool over = false;
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                top[i].x = fmaxf(S[i][0], S[i][2]) * scale;
-                top[i].y = fmaxf(S[i][1], S[i][3]) * scale;
-                over |= top[i].x > m[i].x + (kLift + kSlack) || top[i].y > m[i].y + (kLift + kSlack);
-            }
-            if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    float2 v = top[i], f;
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) {
-                        v.x = fmaxf(v.x, __shfl_xor_sync(0xffffffffu, v.x, d));
-                        v.y = fmaxf(v.y, __shfl_xor_sync(0xffffffffu, v.y, d));
-                    }
-                    const float2 to = make_float2(v.x > m[i].x + (kLift + kSlack) ? v.x - kLift : m[i].x,
-                                                  v.y > m[i].y + (kLift + kSlack) ? v.y - kLift : m[i].y);
-                    f.x = to.x == -INFINITY ? 1.f : ex2(m[i].x - to.x);
-                    f.y = to.y == -INFINITY ? 1.f : ex2(m[i].y - to.y);
-                    m[i] = to;
-                    l[i].x *= f.x;
-                    l[i].y *= f.y;
-#pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        O[i][t][0] *= f.x, O[i][t][1] *= f.y;
-                        O[i][t][2] *= f.x, O[i][t][3] *= f.y;
-                    }
-                }
-            }
-            uint2 P[NT];
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                const float2 by = {scale, scale}, off = {m[i].x == -INFINITY ? 0.f : -m[i].x, m[i].y == -INFINITY ? 0.f : -m[i].y};
-                const float2 a0 = fma2({S[i][0], S[i][1]}, by, off), a1 = fma2({S[i][2], S[i][3]}, by, off);
-                const float2 e0 = {ex2(a0.x), ex2(a0.y)}, e1 = {ex2(a1.x), ex2(a1.y)};
-                l[i] = add2(l[i], add2(e0, e1));
-                P[i] = make_uint2(transpose8(pack_half(e0.x, e0.y)), transpose8(pack_half(e1.x, e1.y)));
-            }
-            // ------------------------------------------------ O^T += V^T P^T
-            {
-                uint32_t sv[2];
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float f[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) f[e] = cache4::eighth_of(vs[2 * half + e]);
-                    if (tail || v_most == cache4::kNoNumbers) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int tok = tok0 + 8 * half + 4 * e + j;
-                            const bool bad = vs[2 * half + e] == cache4::kNoNumbers;
-                            if (tail && (tok >= x.tokens || (bad && tok - x.len >= base_rel))) f[e] = 0.f;
-                            else if (bad) f[e] = NAN;
-                        }
-                    }
-                    sv[half] = pack_half(f[0], f[1]);
-                }
-#pragma unroll
-                for (int w = 0; w < ND / 8; ++w) {
-                    // the elements of even and of odd places of two tokens side by side, for either half of the 16
-                    uint32_t two[2][2];
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        two[half][0] = __byte_perm(vw[2 * half][w], vw[2 * half + 1][w], 0x5410);
-                        two[half][1] = __byte_perm(vw[2 * half][w], vw[2 * half + 1][w], 0x7632);
-                    }
+                // ------------------------------------------------ the values' words, and the slot is free
+                uint32_t vw[4][ND / 8], vs[4], v_most = 0;
+                {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int sh = 8 * (e >> 1), odd = e & 1;
-                        const uint32_t va[4] = {cache4::half_of(two[0][0] >> sh, odd, sv[0]), cache4::half_of(two[0][1] >> sh, odd, sv[0]),
-                                                cache4::half_of(two[1][0] >> sh, odd, sv[1]), cache4::half_of(two[1][1] >> sh, odd, sv[1])};
-#pragma unroll
-                        for (int i = 0; i < NT; ++i) mma_f16(O[i][4 * w + e], va, P[i]);
+                        const int tok = 4 * e + j;
+                        const bool in = C::FULL || r * ND < D;
+                        const unsigned char *at = vcode + tok * code_row + r * (ND / 2);
+                        if (DP == 128) {
+                            uint2 w = make_uint2(0u, 0u);
+                            if (in) w = *reinterpret_cast<const uint2 *>(at);
+                            vw[e][0] = w.x, vw[e][ND / 8 - 1] = w.y;
+                        } else {
+                            vw[e][0] = in ? *reinterpret_cast<const uint32_t *>(at) : 0u;
+                        }
+                        vs[e] = in ? vscale[tok * scale_row + r * ND / 16] : 0u;
+                        v_most = max(v_most, vs[e]);
                     }
                 }
-            }
-            if (tail && no_numbers) {
+                uint32_t no_numbers = 0u;  // tokens of this step whose scale of columns r ND .. is NaN for those who see them
+                if (tail) {
+                    // what some lines do not see must not reach them as 0 x NaN: it counts as zeros here, and
+                    // the lines that do see it are told below
+#pragma unroll 1
+                    for (int i = 0; i < 16; ++i) {
+                        const int rel = tok0 + i - x.len;
+                        if (rel < base_rel || tok0 + i >= x.tokens || r * ND >= D) continue;
+                        if (vscale[i * scale_row + r * ND / 16] == cache4::kNoNumbers) no_numbers |= 1u << i;
+                    }
+                }
+                if (t) {
+                    __syncwarp();
+                    ++cp.used;
+                    if (cp.any()) copy();
+                }
+                // ------------------------------------------------ the weights
+                uint32_t see[NT][2];
+                if (tail) {
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
+                    for (int i = 0; i < NT; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (see[i][e & 1] & no_numbers) {
-#pragma unroll
-                            for (int t = 0; t < MT; ++t) O[i][t][e] = NAN;
+                        for (int u = 0; u < 2; ++u) {
+                            const int line = 8 * i + 2 * j + u, jj = line / p.heads, row = x.first + jj;
+                            see[i][u] = 0;
+                            if (jj < x.n) {
+                                const uint32_t *words = a.mask ? reinterpret_cast<const uint32_t *>(a.mask + (size_t)(x.row0 + row) * a.W) : nullptr;
+                                see[i][u] = seen_bits(words, 2 * a.W, tok0 - x.len, x.rows, row);
+                            }
                         }
-            }
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (!((see[i][e & 1] >> (8 * (e >> 1) + token_r)) & 1u)) S[i][e] = -INFINITY;
+                }
+                float2 top[NT];
+                bool over = false;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    top[i].x = fmaxf(S[i][0], S[i][2]) * scale;
+                    top[i].y = fmaxf(S[i][1], S[i][3]) * scale;
+                    over |= top[i].x > m[i].x + (kLift + kSlack) || top[i].y > m[i].y + (kLift + kSlack);
+                }
+                if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        float2 v = top[i], f;
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) {
+                            v.x = fmaxf(v.x, __shfl_xor_sync(0xffffffffu, v.x, d));
+                            v.y = fmaxf(v.y, __shfl_xor_sync(0xffffffffu, v.y, d));
+                        }
+                        const float2 to = make_float2(v.x > m[i].x + (kLift + kSlack) ? v.x - kLift : m[i].x,
+                                                      v.y > m[i].y + (kLift + kSlack) ? v.y - kLift : m[i].y);
+                        f.x = to.x == -INFINITY ? 1.f : ex2(m[i].x - to.x);
+                        f.y = to.y == -INFINITY ? 1.f : ex2(m[i].y - to.y);
+                        m[i] = to;
+                        l[i].x *= f.x;
+                        l[i].y *= f.y;
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) {
+                            O[i][t][0] *= f.x, O[i][t][1] *= f.y;
+                            O[i][t][2] *= f.x, O[i][t][3] *= f.y;
+                        }
+                    }
+                }
+                uint2 P[NT];
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const float2 by = {scale, scale}, off = {m[i].x == -INFINITY ? 0.f : -m[i].x, m[i].y == -INFINITY ? 0.f : -m[i].y};
+                    const float2 a0 = fma2({S[i][0], S[i][1]}, by, off), a1 = fma2({S[i][2], S[i][3]}, by, off);
+                    const float2 e0 = {ex2(a0.x), ex2(a0.y)}, e1 = {ex2(a1.x), ex2(a1.y)};
+                    l[i] = add2(l[i], add2(e0, e1));
+                    P[i] = make_uint2(transpose8(pack_half(e0.x, e0.y)), transpose8(pack_half(e1.x, e1.y)));
+                }
+                // ------------------------------------------------ O^T += V^T P^T
+                {
+                    uint32_t sv[2];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        float f[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) f[e] = cache4::eighth_of(vs[2 * half + e]);
+                        if (tail || v_most == cache4::kNoNumbers) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int tok = tok0 + 8 * half + 4 * e + j;
+                                const bool bad = vs[2 * half + e] == cache4::kNoNumbers;
+                                if (tail && (tok >= x.tokens || (bad && tok - x.len >= base_rel))) f[e] = 0.f;
+                                else if (bad) f[e] = NAN;
+                            }
+                        }
+                        sv[half] = pack_half(f[0], f[1]);
+                    }
+#pragma unroll
+                    for (int w = 0; w < ND / 8; ++w) {
+                        // the elements of even and of odd places of two tokens side by side, for either half of the 16
+                        uint32_t two[2][2];
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            two[half][0] = __byte_perm(vw[2 * half][w], vw[2 * half + 1][w], 0x5410);
+                            two[half][1] = __byte_perm(vw[2 * half][w], vw[2 * half + 1][w], 0x7632);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int sh = 8 * (e >> 1), odd = e & 1;
+                            const uint32_t va[4] = {cache4::half_of(two[0][0] >> sh, odd, sv[0]), cache4::half_of(two[0][1] >> sh, odd, sv[0]),
+                                                    cache4::half_of(two[1][0] >> sh, odd, sv[1]), cache4::half_of(two[1][1] >> sh, odd, sv[1])};
+#pragma unroll
+                            for (int i = 0; i < NT; ++i) mma_f16(O[i][4 * w + e], va, P[i]);
+                        }
+                    }
+                }
+                if (tail && no_numbers) {
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (see[i][e & 1] & no_numbers) {
+#pragma unroll
+                                for (int t = 0; t < MT; ++t) O[i][t][e] = NAN;
+                            }
+                }
             }
         }
 
